@@ -69,6 +69,11 @@ typedef enum MOSAIC_INT_ENUM {
     MOSAIC_BF16 = 1               /* bfloat16 (upper half of binary32) */
 } mosaic_dtype_t;
 
+typedef enum MOSAIC_INT_ENUM {
+    MOSAIC_E4M3 = 0,              /* OCP FP8 E4M3 codes, largest value 448 */
+    MOSAIC_INT8 = 1               /* 8-bit integers -127 .. 127 (two's complement) */
+} mosaic_code_t;
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mosaic_status_string(mosaic_status_t s);
 
@@ -313,6 +318,133 @@ mosaic_status_t mosaic_masked_logits_fp8(const void *H, int64_t L, int64_t d, co
                                          const uint8_t *Wq, const float *w_scale, int64_t V, void *out,
                                          int64_t chunk_rows, mosaic_dtype_t out_dtype, void *workspace,
                                          int64_t workspace_bytes, void *stream);
+
+/* --------------------------------------- norm and INT8 head of the masked rows --- */
+
+/* Residual addition with root-mean-square norm: the final norm in front of the LM head,
+ * whose masked rows are all that head needs ([MR] 核心观察 #2), or any norm of a layer.
+ * For row i < n of the results, with j = row_idx[i] (or i when row_idx is NULL):
+ *   s_k = X[j, k] + R[j, k]                              (R NULL: s = X)
+ *   y_k = s_k * gain[k] / sqrt(mean_k(s_k^2) + eps)
+ *   sum[i, k] = s_k,  out[i, k] = y_k,
+ *   q[i, k]   = RNE(y_k * (top / amax)),  scale[i] = amax / top,  amax = max_k |y_k|,
+ * top = 448 (MOSAIC_E4M3) or 127 (MOSAIC_INT8).  All arithmetic is fp32; sum, out and q are
+ * each rounded once, from unrounded fp32 values.  A zero row has zero codes and scale 0.
+ *   X, R      [nsrc, d] in in_dtype (F32 or BF16), row strides ldx, ldr >= d elements.
+ *   gain      [d] in gain_dtype.  eps > 0 and finite.
+ *   row_idx   NULL or int32[rows], any order, repeats allowed.  A value outside [0, nsrc)
+ *             gives a row of NaN (codes zero, scale NaN).
+ *   count     NULL (n = rows), or int32* in device memory, read when the kernel starts:
+ *             n = min(max(*count, 0), rows).  Rows >= n of every output are not written.
+ *   sum, out, q (with scale)   each may be NULL, not all three.  sum is [rows, d] in
+ *             in_dtype with row stride ldsum; out is [rows, d] contiguous in in_dtype; q is
+ *             [rows, d] bytes; scale is float[rows].  Without row_idx, sum may be X or R
+ *             itself (same pointer and stride): the residual stream is updated in place.
+ *             No other overlap of outputs with inputs or each other is allowed.
+ * A row holding a NaN or an infinity (or whose result does) has that scale and zero codes.
+ * Any d >= 1 and element-aligned pointers; multiples of 8 elements at 16-byte aligned rows
+ * take the vector form.  rows == 0: OK, nothing enqueued.  Row strides below d, a NULL
+ * required pointer, misalignment, sum aliasing an input with row_idx or another stride, or
+ * rows > nsrc without row_idx: INVALID_ARG.  nsrc or d of 2^31 and more: UNSUPPORTED. */
+mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, int64_t ldr, int64_t nsrc, int64_t d,
+                                   mosaic_dtype_t in_dtype, const void *gain, mosaic_dtype_t gain_dtype, float eps,
+                                   const int32_t *row_idx, const int32_t *count, int64_t rows, void *sum,
+                                   int64_t ldsum, void *out, mosaic_code_t code, void *q, float *scale,
+                                   void *stream);
+
+/* INT8 codes of rows, as mosaic_quantize_rows_fp8 makes E4M3 codes: amax = max_k |x_k|,
+ * scale = amax / 127, q_k = RNE(x_k * (127 / amax)), each fp32 operation rounded to nearest
+ * even.  Used once for the weight W (one scale per vocabulary entry, the product's channel).
+ * Arguments as there (row_idx values outside [0, nsrc) give rows of zero codes and scale
+ * NaN), without alignment or size requirements on d: any d >= 1, X aligned to its elements.
+ * rows == 0 or d == 0: OK, nothing enqueued. */
+mosaic_status_t mosaic_quantize_rows_int8(const void *X, int64_t nsrc, int64_t d, mosaic_dtype_t in_dtype,
+                                          const int32_t *row_idx, int64_t rows, int8_t *q, float *scale,
+                                          void *stream);
+
+/* The LM head on codes in hand: out[i, v] = (sum_k Hq[i, k] * Wq[v, k]) * h_scale[i] *
+ * w_scale[v] for i < n, v < V.
+ *   code     MOSAIC_INT8: the sums are exact (int32), converted to fp32, multiplied by
+ *            h_scale[i], then by w_scale[v]; out_dtype F32 or BF16 (round to nearest even).
+ *            Any 1 <= d <= 131071; Hq, Wq of any alignment.  The fast forms take d % 128
+ *            == 0 and 16-byte aligned codes.  Codes of -128 are allowed.
+ *            MOSAIC_E4M3: what mosaic_masked_logits_fp8 computes from these codes, in one
+ *            chunk, with its requirements: d % 128 == 0, out_dtype BF16, count NULL (else
+ *            UNSUPPORTED), 16-byte aligned Hq, Wq and w_scale.
+ *   Hq [M, d], Wq [V, d] codes, row-major and contiguous; h_scale float[M], w_scale float[V].
+ *   count    NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.
+ *   out      [M, V] row-major, aligned to 16 bytes.  Rows >= n are not written.
+ * M == 0 or V == 0: OK, nothing enqueued.  The results do not depend on M, on count or on
+ * which form runs.  More than 2^24 - 1 tiles of 64 x 64 outputs: UNSUPPORTED. */
+mosaic_status_t mosaic_quantized_logits(mosaic_code_t code, const void *Hq, const float *h_scale, int64_t M,
+                                        const int32_t *count, const void *Wq, const float *w_scale, int64_t V,
+                                        int64_t d, void *out, mosaic_dtype_t out_dtype, void *stream);
+
+/* Workspace bytes of mosaic_masked_logits_int8 for M rows in chunks of chunk_rows: C * d
+ * rounded up to 16, plus 4 * C, with C the rows of the largest chunk; 0 for M == 0; -1 on a
+ * negative size or overflow. */
+int64_t mosaic_logits_int8_workspace_bytes(int64_t M, int64_t chunk_rows, int64_t d);
+
+/* The INT8 form of mosaic_masked_logits_fp8: each chunk's rows H[idx[i]] are quantized into
+ * `workspace` as mosaic_quantize_rows_int8 does, then multiplied as by
+ * mosaic_quantized_logits (out_dtype F32 or BF16).  H is [L, d] in in_dtype (F32 or BF16,
+ * element-aligned); Wq int8 [V, d] and w_scale float[V] come from mosaic_quantize_rows_int8
+ * on W; idx, chunk_rows, stream and errors as there; workspace >=
+ * mosaic_logits_int8_workspace_bytes(M, chunk_rows, d) bytes, 16-byte aligned.  An idx value
+ * outside [0, L) gives a row of NaN (or INVALID_ARG under MOSAIC_CHECK_IDX=1).  Results do
+ * not depend on chunk_rows. */
+mosaic_status_t mosaic_masked_logits_int8(const void *H, int64_t L, int64_t d, mosaic_dtype_t in_dtype,
+                                          const int32_t *idx, int64_t M, const int8_t *Wq, const float *w_scale,
+                                          int64_t V, void *out, int64_t chunk_rows, mosaic_dtype_t out_dtype,
+                                          void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------- distillation --- */
+
+/* Loss of the masked rows' logits against a teacher's K top logits of each row, for
+ * training a student (a quantized head, a model of fewer steps) on the positions that are
+ * sampled.  For row i < n, with t_j = teacher_logits[i, j] at c_j = teacher_ids[i, j]; an
+ * entry with c_j outside [0, V) or t_j = -inf is absent:
+ *   p_j = softmax of t / T over the present entries
+ *   m = max_v z_v,  l = log(sum_v exp((z_v - m) / T)),  log q_v = (z_v - m) / T - l
+ *   loss[i] = T^2 * sum_j p_j (log p_j - log q_{c_j}),   stats[i] = (m, l)
+ *   grad[i, v] = grad_loss[i] * T * (q_v - sum_{j: c_j = v} p_j)
+ * All arithmetic is fp32; grad is rounded once to the logits' type.  A row without a present
+ * entry has loss 0 and gradient 0.  Logits of -inf are allowed (q_v = 0; a loss of +inf
+ * where the teacher has mass there); a row of nothing but -inf, or with a NaN or +inf, has
+ * loss and gradient NaN.  An entry named more than once counts with all its shares.
+ *   logits          [M, V] in dtype (F32 or BF16), row stride ldz >= V elements.
+ *   teacher_logits  [M, K] in teacher_dtype, teacher_ids int32[M, K], contiguous; 0 <= K <=
+ *                   1024 (more: UNSUPPORTED; K == 0: every row is without entries).
+ *   temperature     2^-20 <= T <= 2^20, else INVALID_ARG.
+ *   count           NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.
+ *   loss float[M], stats float[M, 2] (8-byte aligned).
+ *   grad            NULL (the loss alone), or [M, V] in dtype with row stride ldg >= V: the
+ *                   gradient too, in the same call.  It may be logits itself (same pointer
+ *                   and stride); no other overlap is allowed.
+ *   grad_loss       NULL (1) or float[M], the gradient with respect to loss.
+ *   workspace       >= mosaic_distill_topk_workspace_bytes(M, V) bytes, 16-byte aligned
+ *                   (NULL if that is 0); calls that overlap in time need one each.
+ * Rows >= n of every output are not written.  M == 0: OK, nothing enqueued.  V == 0 with M >
+ * 0, a NULL required pointer, misalignment, strides below V or a short workspace:
+ * INVALID_ARG.  M or V of 2^31 and more: UNSUPPORTED. */
+mosaic_status_t mosaic_distill_topk(const void *logits, int64_t ldz, int64_t M, int64_t V, mosaic_dtype_t dtype,
+                                    const void *teacher_logits, mosaic_dtype_t teacher_dtype,
+                                    const int32_t *teacher_ids, int64_t K, float temperature, const int32_t *count,
+                                    float *loss, float *stats, const float *grad_loss, void *grad, int64_t ldg,
+                                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of mosaic_distill_topk for M rows over V vocabulary entries (0 where every
+ * row has a workgroup of its own), or -1 on a negative size. */
+int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V);
+
+/* The gradient alone, from the stats that mosaic_distill_topk left for the same logits and
+ * teacher: for a backward pass that comes later.  Arguments and errors as there (grad
+ * required; it may be logits itself). */
+mosaic_status_t mosaic_distill_topk_grad(const void *logits, int64_t ldz, int64_t M, int64_t V,
+                                         mosaic_dtype_t dtype, const void *teacher_logits,
+                                         mosaic_dtype_t teacher_dtype, const int32_t *teacher_ids, int64_t K,
+                                         float temperature, const int32_t *count, const float *stats,
+                                         const float *grad_loss, void *grad, int64_t ldg, void *stream);
 
 /* ------------------------------------------------------------ host helpers --- */
 

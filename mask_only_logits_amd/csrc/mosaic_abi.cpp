@@ -19,31 +19,12 @@
 #include <utility>
 
 #include "../../include/mosaic.h"
+#include "abi_common.h"
 #include "launch.h"
 
 namespace {
 
-constexpr int64_t kMaxPos = 0x7fffffffLL;   // positions and rows are int32
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// ceil(a / b) for a >= 0, b > 0, without the overflow of (a + b - 1) / b near INT64_MAX.
-int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
-
-int64_t esize_of(mosaic_dtype_t t) { return t == MOSAIC_F32 ? 4 : (t == MOSAIC_BF16 ? 2 : 0); }
-
-// M * V * esize without int64 overflow; -1 on overflow.
-int64_t checked_bytes(int64_t rows, int64_t V, int64_t esize)
-{
-    if (rows < 0 || V < 0 || esize <= 0)
-        return -1;
-    if (rows != 0 && V > INT64_MAX / rows)
-        return -1;
-    const int64_t n = rows * V;
-    if (n != 0 && esize > INT64_MAX / n)
-        return -1;
-    return n * esize;
-}
+using namespace mosaic::abi;
 
 // Debug/tuning override, read from the environment once per process (the first call
 // that needs it) and again on mosaic_debug_reload_env():
@@ -95,13 +76,15 @@ Tune read_tune()
     return g_env;
 }
 
+}  // namespace
+
 // Debug mode MOSAIC_CHECK_IDX=1 (read with MOSAIC_TUNE): before any compute is
 // enqueued, check on the device that every idx[i] (i < M) lies in [0, L), and wait for
 // the answer.  A 4-byte device flag is allocated on first use for each (device, stream)
 // pair, so checked calls on different streams never share a flag.  Returns MOSAIC_OK
 // (mode off, or all indices valid), MOSAIC_ERR_INVALID_ARG (an index out of range) or
 // MOSAIC_ERR_DEVICE.
-mosaic_status_t check_idx_if_asked(const int32_t *idx, int64_t M, int64_t L, hipStream_t stream)
+mosaic_status_t mosaic::abi::check_idx_if_asked(const int32_t *idx, int64_t M, int64_t L, hipStream_t stream)
 {
     if (!read_tune().check_idx)
         return MOSAIC_OK;
@@ -130,6 +113,8 @@ mosaic_status_t check_idx_if_asked(const int32_t *idx, int64_t M, int64_t L, hip
         return MOSAIC_ERR_DEVICE;
     return host ? MOSAIC_ERR_INVALID_ARG : MOSAIC_OK;
 }
+
+namespace {
 
 bool variant_can_run(int v, int64_t M, int64_t d, mosaic_dtype_t in, mosaic_dtype_t out)
 {

@@ -1,0 +1,333 @@
+// Residual addition with root-mean-square norm, and 8-bit row codes.
+//
+// For a row of d elements, with x the layer's output and r the residual stream:
+//   s = x + r,   y_k = s_k * g_k / sqrt(mean_k(s_k^2) + eps),
+//   amax = max_k |y_k|,  scale = amax / top,  q_k = RNE(y_k * (top / amax)),
+// top = 448 for E4M3 codes and 127 for INT8 codes; a row of zeros has zero codes and
+// scale 0.  Sums, the norm and the scale are fp32; s, y and q are each rounded once, from
+// the unrounded fp32 value of the one before (rounding s to bf16 first would move y by up
+// to half a bf16 step, 2^-9 of its value, for nothing: s is in registers).  The INT8
+// quantization of plain rows is the same kernel without the norm.
+//
+// Rows are gathered through a list of row ids where one is given: the LM head needs the
+// final norm of the masked rows only.
+//
+// One pass: a row's elements stay in registers from the loads to the last store, so each
+// input is read once and each output written once, and HBM is what bounds the kernel.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "launch.h"
+#include "row_ops.h"
+
+namespace mosaic {
+namespace {
+
+using namespace rows;
+
+// |x| as MaxBitsOp takes it
+__device__ __forceinline__ float abs_bits(float x)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
+}
+
+// Codes of VEC values already multiplied by top / amax (|y| <= top up to fp32 rounding), in
+// the low bytes of w[].  INT8: adding 1.5 * 2^23 leaves the nearest even integer in the
+// sum's low bits.  E4M3: v_cvt_pk_fp8_f32 rounds to nearest even, and 448 (1 + 2^-23) is
+// still 448.
+template <int VEC>
+__device__ __forceinline__ void make_codes(const float (&y)[VEC], bool int8, uint32_t (&w)[(VEC + 3) / 4])
+{
+#pragma clang fp contract(off)   // y * inv rounds before the addition
+    if (int8) {
+        uint32_t b[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            b[i] = __builtin_bit_cast(uint32_t, y[i] + 12582912.0f);
+        if constexpr (VEC == 1) {
+            w[0] = b[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
+                const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
+                w[i] = lo | (hi << 16);
+            }
+        }
+    } else {
+        if constexpr (VEC == 1) {
+            w[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[0], 0, false);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+                w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], p, true);
+            }
+        }
+    }
+}
+
+// Power of two that keeps top / amax inside fp32 for the smallest rows (1 for all others).
+__device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
+
+// One row per WPR waves, a thread holding CH chunks of VEC elements (d <= 64 WPR CH VEC).
+// NORM off: y = x (plain quantization).
+template <bool BF16, bool NORM, int VEC, int WPR, int CH>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(const RowsNorm a)
+{
+    constexpr int RPB = WPR == 1 ? 4 : 1;   // rows per workgroup
+    constexpr int STEP = 64 * WPR * VEC;
+    __shared__ float red[WPR];
+    const int t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t n = row_count(a.count, a.rows);
+    for (int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? threadIdx.x >> 6 : 0); row < n;
+         row += (int64_t)gridDim.x * RPB) {
+        const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
+        const bool inside = src >= 0 && src < a.nsrc;   // a row id outside gives a row of NaN
+        float v[CH][VEC];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = c * STEP + t * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                v[c][i] = 0.0f;
+            if (k < a.d) {
+                if (inside) {
+                    load<BF16, VEC>(a.X, src * a.ldx + k, v[c]);
+                    if (a.R) {
+                        float r[VEC];
+                        load<BF16, VEC>(a.R, src * a.ldr + k, r);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            v[c][i] += r[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        v[c][i] = __builtin_nanf("");
+                }
+            }
+        }
+        if constexpr (NORM) {
+            if (a.sum) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int k = c * STEP + t * VEC;
+                    if (k < a.d)
+                        store<BF16, VEC>(a.sum, row * a.ldsum + k, v[c]);
+                }
+            }
+            float ss = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    ss += v[c][i] * v[c][i];
+            ss = block_reduce<WPR>(ss, AddOp{}, red);
+            float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+            if (__builtin_isinf(ss)) {
+                // the squares of finite values passed fp32's range: take them 2^-80 smaller
+                // (2^128 and d < 2^31 terms then stay inside), where eps no longer counts
+                constexpr float down = 0x1p-80f;
+                float s2 = 0.0f;
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        s2 += (v[c][i] * down) * (v[c][i] * down);
+                s2 = block_reduce<WPR>(s2, AddOp{}, red);
+                rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int k = c * STEP + t * VEC;
+                if (k < a.d) {
+                    float g[VEC];
+                    if (a.gain_bf16)
+                        load<true, VEC>(a.gain, k, g);
+                    else
+                        load<false, VEC>(a.gain, k, g);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        v[c][i] = v[c][i] * rstd * g[i];
+                    if (a.out)
+                        store<BF16, VEC>(a.out, row * a.d + k, v[c]);
+                }
+            }
+            if (!a.q)
+                continue;
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                amax = MaxBitsOp{}(amax, abs_bits(v[c][i]));
+        amax = block_reduce<WPR>(amax, MaxBitsOp{}, red);
+        const float top = a.code_int8 ? 127.0f : 448.0f;
+        // a row with a NaN or an infinity has zero codes and that scale, so that what is
+        // computed from it is not finite either
+        const bool fine = amax > 0.0f && amax < __builtin_inff();
+        const float up = code_lift(amax), inv = fine ? top / (amax * up) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = c * STEP + t * VEC;
+            if (k < a.d) {
+                float y[VEC];
+                uint32_t w[(VEC + 3) / 4];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    y[i] = fine ? v[c][i] * up * inv : 0.0f;
+                make_codes<VEC>(y, a.code_int8, w);
+                if constexpr (VEC == 8)
+                    *(u32x2_t *)(a.q + row * a.d + k) = u32x2_t{w[0], w[1]};
+                else
+                    a.q[row * a.d + k] = (uint8_t)w[0];
+            }
+        }
+        if (t == 0)
+            a.scale[row] = amax / top;
+    }
+}
+
+// Rows too long for the registers: the row is read again for each of the three passes (sum
+// of squares, maximum, results), from L2 after the first.  `sum` is written in the last pass,
+// each element by the thread that has read it for the last time, so that it may be X or R.
+template <bool BF16, bool NORM>
+__global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
+{
+    __shared__ float red[16];
+    const int64_t n = row_count(a.count, a.rows);
+    for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+        const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
+        const bool inside = src >= 0 && src < a.nsrc;
+        auto element = [&](int k) {
+            if (!inside)
+                return __builtin_nanf("");
+            float x[1];
+            load<BF16, 1>(a.X, src * a.ldx + k, x);
+            if (NORM && a.R) {
+                float r[1];
+                load<BF16, 1>(a.R, src * a.ldr + k, r);
+                x[0] += r[0];
+            }
+            return x[0];
+        };
+        float rstd = 1.0f;
+        if constexpr (NORM) {
+            float ss = 0.0f;
+            for (int k = threadIdx.x; k < a.d; k += 1024) {
+                const float x = element(k);
+                ss += x * x;
+            }
+            ss = block_reduce<16>(ss, AddOp{}, red);
+            rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+            if (__builtin_isinf(ss)) {   // as in rows_norm_kernel
+                constexpr float down = 0x1p-80f;
+                float s2 = 0.0f;
+                for (int k = threadIdx.x; k < a.d; k += 1024) {
+                    const float x = element(k) * down;
+                    s2 += x * x;
+                }
+                s2 = block_reduce<16>(s2, AddOp{}, red);
+                rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
+            }
+        }
+        auto normed = [&](float x, int k) {
+            if constexpr (!NORM)
+                return x;
+            float g[1];
+            if (a.gain_bf16)
+                load<true, 1>(a.gain, k, g);
+            else
+                load<false, 1>(a.gain, k, g);
+            return x * rstd * g[0];
+        };
+        float amax = 0.0f;
+        if (a.q) {
+            for (int k = threadIdx.x; k < a.d; k += 1024)
+                amax = MaxBitsOp{}(amax, abs_bits(normed(element(k), k)));
+            amax = block_reduce<16>(amax, MaxBitsOp{}, red);
+        }
+        const float top = a.code_int8 ? 127.0f : 448.0f;
+        const bool fine = amax > 0.0f && amax < __builtin_inff();
+        const float up = code_lift(amax), inv = fine ? top / (amax * up) : 0.0f;
+        for (int k = threadIdx.x; k < a.d; k += 1024) {
+            const float x[1] = {element(k)};
+            const float y[1] = {normed(x[0], k)};
+            if (NORM && a.sum)
+                store<BF16, 1>(a.sum, row * a.ldsum + k, x);
+            if (NORM && a.out)
+                store<BF16, 1>(a.out, row * a.d + k, y);
+            if (a.q) {
+                const float z[1] = {fine ? y[0] * up * inv : 0.0f};
+                uint32_t w[1];
+                make_codes<1>(z, a.code_int8, w);
+                a.q[row * a.d + k] = (uint8_t)w[0];
+            }
+        }
+        if (a.q && threadIdx.x == 0)
+            a.scale[row] = amax / top;
+    }
+}
+
+// Workgroups of a launch: one for each row (or four), and no more than 2^20, over which the
+// kernels walk: a launch holds at most 2^32 - 1 threads.
+unsigned grid_of(int64_t rows, int per_block)
+{
+    return (unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 1 << 20);
+}
+
+template <bool BF16, bool NORM, int VEC, int WPR, int CH>
+void run(const RowsNorm &a, hipStream_t stream)
+{
+    hipLaunchKernelGGL((rows_norm_kernel<BF16, NORM, VEC, WPR, CH>), dim3(grid_of(a.rows, WPR == 1 ? 4 : 1)),
+                       dim3(WPR == 1 ? 256 : 64 * WPR), 0, stream, a);
+}
+
+template <bool BF16, bool NORM>
+void pick(const RowsNorm &a, hipStream_t stream)
+{
+    const int64_t es = BF16 ? 2 : 4;
+    auto ok = [&](const void *p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); };
+    // whole 8-element chunks at 16-byte (codes: 8-byte) places
+    const bool vec = a.d % 8 == 0 && ok(a.X, a.ldx) && ok(a.R, a.ldr) && ok(a.sum, a.ldsum) && ok(a.out, a.d) &&
+                     ((uintptr_t)a.q & 7) == 0 && ((uintptr_t)a.gain & 15) == 0;
+    if (vec) {
+        if (a.d <= 512)
+            return run<BF16, NORM, 8, 1, 1>(a, stream);
+        if (a.d <= 1024)
+            return run<BF16, NORM, 8, 1, 2>(a, stream);
+        if (a.d <= 2048)
+            return run<BF16, NORM, 8, 4, 1>(a, stream);
+        if (a.d <= 4096)
+            return run<BF16, NORM, 8, 4, 2>(a, stream);
+        if (a.d <= 8192)
+            return run<BF16, NORM, 8, 16, 1>(a, stream);
+        if (a.d <= 16384)
+            return run<BF16, NORM, 8, 16, 2>(a, stream);
+    } else {
+        if (a.d <= 512)
+            return run<BF16, NORM, 1, 1, 8>(a, stream);
+        if (a.d <= 2048)
+            return run<BF16, NORM, 1, 4, 8>(a, stream);
+        if (a.d <= 8192)
+            return run<BF16, NORM, 1, 16, 8>(a, stream);
+    }
+    hipLaunchKernelGGL((rows_norm_long_kernel<BF16, NORM>), dim3(grid_of(a.rows, 1)), dim3(1024), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_rows_norm(const RowsNorm &a, bool in_bf16, bool norm, hipStream_t stream)
+{
+    if (in_bf16)
+        norm ? pick<true, true>(a, stream) : pick<true, false>(a, stream);
+    else
+        norm ? pick<false, true>(a, stream) : pick<false, false>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace mosaic

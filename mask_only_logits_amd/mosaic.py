@@ -10,6 +10,7 @@ PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -23,6 +24,8 @@ MOSAIC_ERR_UNSUPPORTED = 2
 MOSAIC_ERR_DEVICE = 3
 MOSAIC_F32 = 0
 MOSAIC_BF16 = 1
+MOSAIC_E4M3 = 0
+MOSAIC_INT8 = 1
 MOSAIC_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 # Every symbol include/mosaic.h declares.
@@ -45,6 +48,14 @@ EXPORTS = (
     "mosaic_quantize_rows_fp8",
     "mosaic_logits_fp8_workspace_bytes",
     "mosaic_masked_logits_fp8",
+    "mosaic_add_rmsnorm",
+    "mosaic_quantize_rows_int8",
+    "mosaic_quantized_logits",
+    "mosaic_logits_int8_workspace_bytes",
+    "mosaic_masked_logits_int8",
+    "mosaic_distill_topk",
+    "mosaic_distill_topk_workspace_bytes",
+    "mosaic_distill_topk_grad",
     "mosaic_debug_reload_env",
 )
 
@@ -97,6 +108,23 @@ def _load() -> ctypes.CDLL:
     lib.mosaic_logits_fp8_workspace_bytes.argtypes = [i64, i64, i64]
     lib.mosaic_masked_logits_fp8.restype = st
     lib.mosaic_masked_logits_fp8.argtypes = [p, i64, i64, p, i64, p, p, i64, p, i64, st, p, i64, p]
+    f32 = ctypes.c_float
+    lib.mosaic_add_rmsnorm.restype = st
+    lib.mosaic_add_rmsnorm.argtypes = [p, i64, p, i64, i64, i64, st, p, st, f32, p, p, i64, p, i64, p, st, p, p, p]
+    lib.mosaic_quantize_rows_int8.restype = st
+    lib.mosaic_quantize_rows_int8.argtypes = [p, i64, i64, st, p, i64, p, p, p]
+    lib.mosaic_quantized_logits.restype = st
+    lib.mosaic_quantized_logits.argtypes = [st, p, p, i64, p, p, p, i64, i64, p, st, p]
+    lib.mosaic_logits_int8_workspace_bytes.restype = i64
+    lib.mosaic_logits_int8_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.mosaic_masked_logits_int8.restype = st
+    lib.mosaic_masked_logits_int8.argtypes = [p, i64, i64, st, p, i64, p, p, i64, p, i64, st, p, i64, p]
+    lib.mosaic_distill_topk.restype = st
+    lib.mosaic_distill_topk.argtypes = [p, i64, i64, i64, st, p, st, p, i64, f32, p, p, p, p, p, i64, p, i64, p]
+    lib.mosaic_distill_topk_workspace_bytes.restype = i64
+    lib.mosaic_distill_topk_workspace_bytes.argtypes = [i64, i64]
+    lib.mosaic_distill_topk_grad.restype = st
+    lib.mosaic_distill_topk_grad.argtypes = [p, i64, i64, i64, st, p, st, p, i64, f32, p, p, p, p, i64, p]
     lib.mosaic_debug_reload_env.restype = None
     lib.mosaic_debug_reload_env.argtypes = []
     lib.mosaic_lazy_chunk_rows.restype = st
@@ -137,6 +165,51 @@ def _stream(stream) -> int | None:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _dev_rows(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype: torch.dtype | None = None):
+    """(pointer, row stride in elements) of a [>= rows, cols] device tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr() if t.numel() else None, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype: torch.dtype):
+    """Pointer of a contiguous device tensor with at least n elements."""
+    ptr = _dev(t, name, dtype)
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{name} has fewer than {n} entries")
+    return ptr
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, like: torch.Tensor, *others):
+    """Context in which a call allocates and launches: the tensors' device (one for all of
+    them) and the stream the kernels go to, so that what the call allocates belongs to it."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        raise ValueError("the tensors must be device tensors")
+    for t in others:
+        if t is not None and t.device != like.device:
+            raise ValueError(f"tensors on {like.device} and {t.device}")
+    if stream is None:
+        return _HERE if like.device.index == torch.cuda.current_device() else torch.cuda.device(like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+    if stream.device != like.device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {like.device}")
+    return torch.cuda.stream(stream)
 
 
 def _check(status: int, where: str):
@@ -475,3 +548,207 @@ def mosaic_masked_logits_fp8(H: torch.Tensor, idx: torch.Tensor, Wq: torch.Tenso
                                         _dev(workspace, "workspace", torch.uint8), workspace.numel(),
                                         _stream(stream)), "mosaic_masked_logits_fp8")
     return out
+
+
+def mosaic_add_rmsnorm(X: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                       row_idx: torch.Tensor | None = None, count: torch.Tensor | None = None,
+                       rows: int | None = None, store_sum: bool = False, sum_out: torch.Tensor | None = None,
+                       store_out: bool = True, out: torch.Tensor | None = None, code: int | None = None,
+                       q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """s = X + residual and y = s * gain / sqrt(mean(s^2) + eps) of rows of X [n, d] (bf16 or
+    fp32; the rows row_idx names, or all): returns (sum_out, out, q, scale), None for what is
+    not asked for.
+
+    sum_out [rows, d] holds s (with `store_sum`, or where it is given; without row_idx it may
+    be X or residual itself), out [rows, d] holds y (unless store_out is False), and with
+    code = MOSAIC_INT8 (q int8) or MOSAIC_E4M3 (q uint8) q [rows, d] and scale [rows] hold y's
+    codes.  X, residual and sum_out may have any row stride.  count: an int32 device tensor
+    with the number of rows (clamped to rows); rows past it are not written."""
+    if X.dim() != 2:
+        raise ValueError("X must be [n, d]")
+    n, d = X.shape
+    if rows is None:
+        rows = n if row_idx is None else row_idx.numel()
+    if row_idx is not None and rows > row_idx.numel():
+        raise ValueError("rows exceeds the length of row_idx")
+    if gain.numel() != d:
+        raise ValueError("gain must have d entries")
+    q_type = None if code is None else {MOSAIC_E4M3: torch.uint8, MOSAIC_INT8: torch.int8}.get(code)
+    if code is not None and q_type is None:
+        raise ValueError(f"unknown code {code}")
+    if code is None and (q is not None or scale is not None):
+        raise ValueError("q and scale need a code")
+    with _on(stream, X, gain, residual, row_idx, count, sum_out, out, q, scale):
+        if store_sum and sum_out is None:
+            sum_out = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+        if store_out and out is None:
+            out = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+        if code is not None:
+            q = torch.empty((rows, d), dtype=q_type, device=X.device) if q is None else q
+            scale = torch.empty(rows, dtype=torch.float32, device=X.device) if scale is None else scale
+        x, ldx = _dev_rows(X, "X", n, d)
+        r, ldr = _dev_rows(residual, "residual", n, d, X.dtype)
+        s, lds = _dev_rows(sum_out, "sum_out", rows, d, X.dtype)
+        _check(lib.mosaic_add_rmsnorm(
+            x, ldx, r, ldr, n, d, _dtype_code(X.dtype), _dev(gain, "gain"), _dtype_code(gain.dtype), eps,
+            _vector(row_idx, "row_idx", rows, torch.int32), _vector(count, "count", 1, torch.int32), rows, s, lds,
+            _vector(out, "out", rows * d, X.dtype), code or 0, _vector(q, "q", rows * d, q_type),
+            _vector(scale, "scale", rows, torch.float32), _stream(None)), "mosaic_add_rmsnorm")
+    return sum_out, out, q, scale
+
+
+def mosaic_quantize_rows_int8(X: torch.Tensor, row_idx: torch.Tensor | None = None, rows: int | None = None,
+                              q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """Per-row INT8 quantization of X [n, d] (bf16 or fp32): returns (codes int8 [rows, d],
+    scales float32 [rows]); rows = len(row_idx) (gathered rows) or n."""
+    if X.dim() != 2:
+        raise ValueError("X must be [n, d]")
+    n, d = X.shape
+    if rows is None:
+        rows = n if row_idx is None else row_idx.numel()
+    with _on(stream, X, row_idx, q, scale):
+        q = torch.empty((rows, d), dtype=torch.int8, device=X.device) if q is None else q
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device) if scale is None else scale
+        _check(lib.mosaic_quantize_rows_int8(
+            _dev(X, "X"), n, d, _dtype_code(X.dtype), _vector(row_idx, "row_idx", rows, torch.int32), rows,
+            _vector(q, "q", rows * d, torch.int8), _vector(scale, "scale", rows, torch.float32), _stream(None)),
+            "mosaic_quantize_rows_int8")
+    return q, scale
+
+
+def mosaic_quantized_logits(Hq: torch.Tensor, h_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                            M: int | None = None, count: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                            stream=None) -> torch.Tensor:
+    """logits[i, v] = (Hq[i] . Wq[v]) * h_scale[i] * w_scale[v] of 8-bit codes Hq [M, d] and
+    Wq [V, d]: INT8 (int8 tensors, exact sums, bf16 or fp32 logits) or E4M3 (uint8 tensors,
+    bf16 logits, d % 128 == 0).  count: an int32 device tensor with the number of rows
+    (clamped to M; INT8 only); rows past it are not written."""
+    if Hq.dim() != 2 or Wq.dim() != 2 or Hq.shape[1] != Wq.shape[1]:
+        raise ValueError("Hq must be [M, d] and Wq [V, d]")
+    code = {torch.int8: MOSAIC_INT8, torch.uint8: MOSAIC_E4M3}.get(Hq.dtype)
+    if code is None:
+        raise TypeError(f"Hq must be int8 (INT8 codes) or uint8 (E4M3 codes), got {Hq.dtype}")
+    d, V = Hq.shape[1], Wq.shape[0]
+    M = Hq.shape[0] if M is None else int(M)
+    if M > Hq.shape[0]:
+        raise ValueError("M exceeds the rows of Hq")
+    with _on(stream, Hq, h_scale, Wq, w_scale, count, out):
+        if out is None:
+            out = torch.empty((M, V), dtype=out_dtype or torch.bfloat16, device=Hq.device)
+        _check(lib.mosaic_quantized_logits(
+            code, _dev(Hq, "Hq"), _vector(h_scale, "h_scale", M, torch.float32), M,
+            _vector(count, "count", 1, torch.int32), _dev(Wq, "Wq", Hq.dtype),
+            _vector(w_scale, "w_scale", V, torch.float32), V, d, _vector(out, "out", M * V, out.dtype),
+            _dtype_code(out.dtype), _stream(None)), "mosaic_quantized_logits")
+    return out
+
+
+def mosaic_logits_int8_workspace_bytes(M: int, chunk_rows: int, d: int) -> int:
+    """Workspace bytes mosaic_masked_logits_int8 needs for M rows in chunks of chunk_rows."""
+    n = int(lib.mosaic_logits_int8_workspace_bytes(int(M), int(chunk_rows), int(d)))
+    if n < 0:
+        raise ValueError("workspace size overflows")
+    return n
+
+
+def mosaic_masked_logits_int8(H: torch.Tensor, idx: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                              M: int | None = None, out: torch.Tensor | None = None, chunk_rows: int = 0,
+                              out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """Logits [M, V] (bf16 or fp32) of the INT8 LM head: H[idx[:M]] (bf16 or fp32) quantized
+    per row on the fly, times the pre-quantized W (Wq int8 [V, d], w_scale float32 [V])."""
+    if H.dim() != 2 or Wq.dim() != 2 or H.shape[1] != Wq.shape[1]:
+        raise ValueError("H must be [L, d] and Wq [V, d]")
+    L, d = H.shape
+    V = Wq.shape[0]
+    M = idx.numel() if M is None else int(M)
+    if M > idx.numel():
+        raise ValueError("M exceeds the length of idx")
+    with _on(stream, H, idx, Wq, w_scale, out, workspace):
+        if out is None:
+            out = torch.empty((M, V), dtype=out_dtype or torch.bfloat16, device=H.device)
+        if workspace is None:
+            workspace = torch.empty(max(16, mosaic_logits_int8_workspace_bytes(M, chunk_rows, d)),
+                                    dtype=torch.uint8, device=H.device)
+        _check(lib.mosaic_masked_logits_int8(
+            _dev(H, "H"), L, d, _dtype_code(H.dtype), _dev(idx, "idx", torch.int32), M, _dev(Wq, "Wq", torch.int8),
+            _vector(w_scale, "w_scale", V, torch.float32), V, _vector(out, "out", M * V, out.dtype),
+            int(chunk_rows), _dtype_code(out.dtype), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+            _stream(None)), "mosaic_masked_logits_int8")
+    return out
+
+
+def _teacher(M: int, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor):
+    """(pointer, dtype code, ids pointer, K) of a teacher's top logits [M, K]."""
+    if teacher_logits.dim() != 2 or teacher_logits.shape != teacher_ids.shape or teacher_logits.shape[0] < M:
+        raise ValueError("teacher_logits and teacher_ids must be [M, K]")
+    return (_dev(teacher_logits, "teacher_logits"), _dtype_code(teacher_logits.dtype),
+            _dev(teacher_ids, "teacher_ids", torch.int32), teacher_logits.shape[1])
+
+
+def mosaic_distill_topk_workspace_bytes(M: int, V: int) -> int:
+    """Workspace bytes mosaic_distill_topk needs for M rows over V vocabulary entries."""
+    n = int(lib.mosaic_distill_topk_workspace_bytes(int(M), int(V)))
+    if n < 0:
+        raise ValueError("negative size")
+    return n
+
+
+def mosaic_distill_topk(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor,
+                        temperature: float = 1.0, count: torch.Tensor | None = None,
+                        loss: torch.Tensor | None = None, stats: torch.Tensor | None = None,
+                        with_grad: bool = False, grad_loss: torch.Tensor | None = None,
+                        grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Per row i of logits [M, V] (bf16 or fp32, any row stride): the loss T^2 KL(p || q)
+    of q = softmax(logits[i] / T) against the teacher's top logits teacher_logits[i] [K] at the
+    vocabulary entries teacher_ids[i] (int32; entries outside [0, V) are absent), with
+    p = softmax(teacher_logits[i] / T).  Returns (loss float32 [M], stats float32 [M, 2],
+    grad): stats is what mosaic_distill_topk_grad takes, and grad, with `with_grad` (or where
+    it is given; it may be logits itself), is the gradient times grad_loss [M] (default 1),
+    else None.  count: an int32 device tensor with the number of rows (clamped to M)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    with _on(stream, logits, teacher_logits, teacher_ids, count, loss, stats, grad_loss, grad, workspace):
+        dev = logits.device
+        loss = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
+        stats = torch.empty((M, 2), dtype=torch.float32, device=dev) if stats is None else stats
+        if with_grad and grad is None:
+            grad = torch.empty((M, V), dtype=logits.dtype, device=dev)
+        if workspace is None:
+            need = mosaic_distill_topk_workspace_bytes(M, V)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        z, ldz = _dev_rows(logits, "logits", M, V)
+        g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
+        top, top_type, ids, K = _teacher(M, teacher_logits, teacher_ids)
+        _check(lib.mosaic_distill_topk(
+            z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
+            _vector(count, "count", 1, torch.int32), _vector(loss, "loss", M, torch.float32),
+            _vector(stats, "stats", 2 * M, torch.float32), _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg,
+            _dev(workspace, "workspace", torch.uint8), 0 if workspace is None else workspace.numel(),
+            _stream(None)), "mosaic_distill_topk")
+    return loss, stats, grad
+
+
+def mosaic_distill_topk_grad(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor,
+                             stats: torch.Tensor, grad_loss: torch.Tensor | None = None, temperature: float = 1.0,
+                             count: torch.Tensor | None = None, grad: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """The gradient of mosaic_distill_topk's loss with respect to logits, times grad_loss [M]
+    (default 1), from the stats it returned for the same arguments.  grad (allocated if
+    absent) may be logits itself."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    with _on(stream, logits, teacher_logits, teacher_ids, stats, grad_loss, count, grad):
+        if grad is None:
+            grad = torch.empty((M, V), dtype=logits.dtype, device=logits.device)
+        z, ldz = _dev_rows(logits, "logits", M, V)
+        g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
+        top, top_type, ids, K = _teacher(M, teacher_logits, teacher_ids)
+        _check(lib.mosaic_distill_topk_grad(
+            z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
+            _vector(count, "count", 1, torch.int32), _vector(stats, "stats", 2 * M, torch.float32),
+            _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg, _stream(None)), "mosaic_distill_topk_grad")
+    return grad
