@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "row_ops.h"
@@ -46,7 +47,7 @@ __device__ __forceinline__ void store4(void *out, int64_t off, const float (&x)[
 // Any shape and alignment.  64 x 64 outputs per workgroup of four waves, 32 x 32 each; K in
 // steps of 64 codes, staged through registers into LDS (rows of 64 + 16 bytes, so that the
 // 16-byte fragment reads spread over the banks); codes past d, V or the rows are zeros.
-template <bool OUT_BF16, bool ALIGNED>
+template <bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_int8_any_kernel(const int8_t *__restrict__ Hq,
                                                             const float *__restrict__ hs,
                                                             const int32_t *__restrict__ count, int32_t max_rows,
@@ -71,8 +72,10 @@ __global__ __launch_bounds__(256) void gemm_int8_any_kernel(const int8_t *__rest
         i32x4_t r = {0, 0, 0, 0};
         if (!ok || k >= d)
             return r;
-        if constexpr (ALIGNED)   // d % 16 == 0 and 16-byte aligned rows: whole or nothing
-            return *(const i32x4_t *)(p + k);
+        if (k + 16 <= d) {
+            __builtin_memcpy(&r, p + k, 16);   // rows may start at any byte
+            return r;
+        }
 #pragma unroll
         for (int b = 0; b < 16; ++b)
             if (k + b < d)
@@ -140,22 +143,559 @@ __global__ __launch_bounds__(256) void gemm_int8_any_kernel(const int8_t *__rest
     }
 }
 
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier without the fence of __syncthreads(), which would wait for the requests
+// in flight.
+__device__ __forceinline__ void bar()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What a request past the end of a row reads (rows whose d is no multiple of the K tile).
+__device__ __attribute__((aligned(16))) const int8_t kZeroCodes[16] = {};
+
+// 256 x 256 outputs per workgroup of eight waves, walked persistently.  K tiles of 128 codes
+// are rows of 128 bytes, as the bf16 kernel's K tiles of 64 elements are, and
+// v_mfma_i32_16x16x64_i8 takes the 16 bytes per lane and the cycles of
+// v_mfma_f32_16x16x32_bf16 at twice the products, so the pipeline is that kernel's: requests
+// straight to LDS by waves 0-3 (one per SIMD), three W stages and two H stages (160 KiB),
+// XOR-swizzled 16-byte chunks, the A fragments single-buffered, the tile order that keeps the
+// XCDs side by side on the vocabulary.
+//  * The tile's row scales (256 of W, 256 of H) are requested into the W stage that the K
+//    loop's last step but one frees, one step ahead of their use; the ring of W stages starts
+//    behind that stage in the next tile, whose third K tile is the first to reach it.
+//  * Epilogue: int32 -> fp32, times both scales, rounded; lanes trade words so that each
+//    store instruction writes whole 128-byte lines.
+//  * TAIL: d is a multiple of 16 only; chunks past the row's end are read from kZeroCodes.
+template <bool OUT_BF16, bool TAIL>
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2))) void
+gemm_int8_kernel(const int8_t *__restrict__ Hq, const float *__restrict__ hs, const int32_t *__restrict__ rows_dev,
+                 int32_t max_rows, const int8_t *__restrict__ Wq, const float *__restrict__ ws, int32_t V, int32_t d,
+                 void *__restrict__ out, int64_t ldo, int32_t group_m)
+{
+    constexpr int NW = 8, DMAW = 4, BV = 256, BM = 256, BK = 128, WST = 3, HST = 2;
+    constexpr int CHUNKS = BK / 16, RPI = 64 / CHUNKS;          // rows per request instruction
+    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, H_BASE = WST * W_TILE;
+    constexpr int WV = BV / 2, WM = BM / (NW / 2), AV = WV / 16, AM = WM / 16;
+    constexpr int LW = BV / RPI / DMAW, LH = BM / RPI / DMAW;   // requests per requesting wave
+    static_assert(H_BASE + HST * H_TILE <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(1024))) char smem[H_BASE + HST * H_TILE];
+
+    const int rows = (int)rows::row_count(rows_dev, max_rows);
+    const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, ntiles = nvt * nmt;
+    const int nk = (d + BK - 1) / BK;
+
+    // Tile list of this workgroup: in a full super-group of 8 * group_m row tiles, XCD x takes
+    // row tiles x, x + 8, ... of every vocabulary tile; the rest goes to the XCDs in eight
+    // contiguous runs.
+    const int per_xcd = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int per_group = group_m * nvt, sg = 8 * group_m, nfull = nmt / sg;
+    const int full_tiles = nfull * per_group;
+    const int rtiles = ntiles - 8 * full_tiles, q8 = rtiles >> 3, rem = rtiles & 7;
+    const int start = xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8;
+    const int count = full_tiles + q8 + (xcd < rem ? 1 : 0);
+    const int n_my = slot < count ? (count - slot + per_xcd - 1) / per_xcd : 0;
+    if (n_my == 0)
+        return;
+    auto tile_coords = [&](int i, int &m0, int &v0) __attribute__((always_inline)) {
+        const int tx = slot + i * per_xcd;
+        if (tx < full_tiles) {
+            const int s = tx / per_group, t = 8 * (tx - s * per_group) + xcd;
+            m0 = (s * sg + t % sg) * BM;
+            v0 = (t / sg) * BV;
+            return;
+        }
+        const int t = start + tx - full_tiles, g = t / per_group;
+        const int first_m = nfull * sg + g * group_m, gsz = min(nmt - first_m, group_m);
+        const int local = t - g * per_group;
+        m0 = (first_m + local % gsz) * BM;
+        v0 = (local / gsz) * BV;
+    };
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wv = wave & 1, wm = wave >> 1, dwave = wave % DMAW;
+    auto swz = [](int r) { return (r >> 1) & 7; };
+
+    // Requests: lane i of instruction j fills tile row (dwave * L + j) * RPI + i / CHUNKS, whose
+    // logical chunk (i % CHUNKS) ^ swz(row) goes to physical chunk i % CHUNKS.  Rows past V /
+    // rows re-read the last valid row; their results are never stored.
+    auto tile_row = [&](int j) { return (dwave * LW + j) * RPI + lane / CHUNKS; };
+    auto chunk_of = [&](int j) { return ((lane % CHUNKS) ^ swz(tile_row(j))) * 16; };
+    const int8_t *wbase, *hbase;
+    uint32_t woff[LW], hoff[LH];
+    auto make_src = [&](int m0, int v0) __attribute__((always_inline)) {
+        wbase = Wq + (int64_t)v0 * d;
+        hbase = Hq + (int64_t)m0 * d;
+#pragma unroll
+        for (int j = 0; j < LW; ++j)
+            woff[j] = (uint32_t)min(tile_row(j), V - 1 - v0) * (uint32_t)d + (uint32_t)chunk_of(j);
+#pragma unroll
+        for (int j = 0; j < LH; ++j)
+            hoff[j] = (uint32_t)min(tile_row(j), rows - 1 - m0) * (uint32_t)d + (uint32_t)chunk_of(j);
+    };
+    auto request = [&](const int8_t *base, uint32_t off, int kb, int j, int lds) __attribute__((always_inline)) {
+        const int8_t *src = base + kb + off;
+        if constexpr (TAIL)
+            src = kb + chunk_of(j) < d ? src : kZeroCodes;
+        __builtin_amdgcn_global_load_lds((const void *)src, (lds_void_t *)(smem + lds), 16, 0, 0);
+    };
+    auto issue_w = [&](int rw, int kt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < LW; ++j)
+            request(wbase, woff[j], kt * BK, j, rw + (dwave * LW + j) * 1024);
+    };
+    auto issue_h = [&](int rh, int kt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < LH; ++j)
+            request(hbase, hoff[j], kt * BK, j, rh + (dwave * LH + j) * 1024);
+    };
+    // row scales: 256 of W, then 256 of H, indices clamped to the last valid row
+    auto issue_scales = [&](int at, int m0, int v0) __attribute__((always_inline)) {
+        const int r = dwave * 64 + lane;
+        __builtin_amdgcn_global_load_lds((const void *)(ws + min(v0 + r, V - 1)), (lds_void_t *)(smem + at + dwave * 256),
+                                         4, 0, 0);
+        __builtin_amdgcn_global_load_lds((const void *)(hs + min(m0 + r, rows - 1)),
+                                         (lds_void_t *)(smem + at + BV * 4 + dwave * 256), 4, 0, 0);
+    };
+    auto next_w = [](int rw) { return rw + W_TILE == H_BASE ? 0 : rw + W_TILE; };
+    auto next_h = [](int rh) { return rh + H_TILE == H_BASE + HST * H_TILE ? H_BASE : rh + H_TILE; };
+
+    i32x4_t acc[AV][AM];
+    auto zero_acc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < AV; ++a)
+#pragma unroll
+            for (int b = 0; b < AM; ++b)
+                acc[a][b] = i32x4_t{0, 0, 0, 0};
+    };
+    zero_acc();
+
+    // Fragments: lane (r16, qd) reads row r16 of a 16-row block, logical chunk 4 s + qd of
+    // sub-step s; blocks start at multiples of 16 rows, so a row's swizzle is the lane's.
+    const int r16 = lane & 15, qd = lane >> 4;
+    const int lane_chunk = (qd ^ swz(r16)) * 16;
+    const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = (wm * WM + r16) * BK + lane_chunk;
+    i32x4_t af[AV], bf[2][AM];
+    // MFMAs on B buffer `cur` while sub-step s of the stages at rw (W) and rh (H) is read: the B
+    // fragments first, each A fragment after its row's MFMAs, the last one before them, so
+    // that the wave's last read is not followed by the step's wait.  Odd rows take the B
+    // blocks in reverse: consecutive MFMAs share an operand, which takes less power.
+    auto mma_load = [&](int rw, int rh, int s, int cur) __attribute__((always_inline)) {
+        const int ab = (a_addr + rw) ^ (64 * s), bb = (b_addr + rh) ^ (64 * s);
+#pragma unroll
+        for (int b = 0; b < AM; ++b)
+            bf[cur ^ 1][b] = *(const i32x4_t *)(smem + bb + b * 16 * BK);
+#pragma unroll
+        for (int a = 0; a < AV; ++a) {
+            i32x4_t nxt;
+            if (a == AV - 1)
+                nxt = *(const i32x4_t *)(smem + ab + a * 16 * BK);
+#pragma unroll
+            for (int c = 0; c < AM; ++c) {
+                const int b = (a & 1) ? AM - 1 - c : c;
+                acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[a], bf[cur][b], acc[a][b], 0, 0, 0);
+            }
+            af[a] = a == AV - 1 ? nxt : *(const i32x4_t *)(smem + ab + a * 16 * BK);
+        }
+    };
+    // Instruction order of a sub-step: each request beside an MFMA, then the fragment reads
+    // spread over the MFMAs.
+    auto interleave = [&](int nreq) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+            if (i < nreq) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < AM; ++b) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        const int used = nreq + AM;
+#pragma unroll
+        for (int a = 0; a < AV; ++a) {
+            if (a == AV - 1)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+            for (int c = 0; c < AM; ++c)
+                if (a * AM + c >= used)
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (a < AV - 1)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    };
+
+    int w0 = 0;   // W stage of the current tile's K tile 0
+    // a tile's first two K tiles, in the order the waits count on
+    auto prologue = [&]() __attribute__((always_inline)) {
+        issue_h(H_BASE, 0);
+        issue_w(w0 * W_TILE, 0);
+        if (nk > 1) {
+            issue_h(H_BASE + H_TILE, 1);
+            issue_w((w0 + 1) % WST * W_TILE, 1);
+        }
+    };
+
+    const bool vec_ok = ((uintptr_t)out & 15) == 0 && ldo % (OUT_BF16 ? 8 : 4) == 0;
+    // one lane's N = 8 (bf16) or 4 (fp32) results of row `row` from vocabulary entry v on
+    auto store_words = [&](int row, int v, const uint32_t (&w)[4]) __attribute__((always_inline)) {
+        constexpr int N = OUT_BF16 ? 8 : 4;
+        if (row >= rows)
+            return;
+        char *o = (char *)out + ((int64_t)row * ldo + v) * (OUT_BF16 ? 2 : 4);
+        if (vec_ok && v + N <= V) {
+            *(i32x4_t *)o = i32x4_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (v + e < V) {
+                if constexpr (OUT_BF16)
+                    ((uint16_t *)o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else
+                    ((uint32_t *)o)[e] = w[e];
+            }
+        }
+    };
+    // Lanes r16 and r16 ^ 8 trade words (row rotate by 8, the bank mask picks the receiving
+    // half), so that x holds rows 0-7 of both operands and y rows 8-15.
+    auto trade = [&](uint32_t (&x)[4], uint32_t (&y)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int a = (int)x[e], b = (int)y[e];
+            x[e] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xf, 0xc, false);
+            y[e] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xf, 0x3, false);
+        }
+    };
+    // Lane (r16, qd) holds entries 4 qd .. 4 qd + 3 of each 16-entry block for row r16 of each
+    // 16-row block.
+    auto epilogue = [&](const float *sc, int m0, int v0) __attribute__((always_inline)) {
+        float h[AM];
+#pragma unroll
+        for (int b = 0; b < AM; ++b)
+            h[b] = sc[BV + wm * WM + b * 16 + r16];
+#pragma unroll
+        for (int q = 0; q < AV / 4; ++q) {
+            f32x4_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = *(const f32x4_t *)(sc + wv * WV + (4 * q + i) * 16 + 4 * qd);
+#pragma unroll
+            for (int b = 0; b < AM; ++b) {
+                const int row = m0 + wm * WM + b * 16 + (r16 & 7);
+                float x[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[i][e] = (float)acc[4 * q + i][b][e] * h[b] * w[i][e];
+                if constexpr (OUT_BF16) {
+                    // neighbouring blocks: permlane16_swap gives a lane eight entries of one
+                    uint32_t p[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const auto s0 = __builtin_amdgcn_permlane16_swap(rows::pack_bf16(x[2 * i][0], x[2 * i][1]),
+                                                                         rows::pack_bf16(x[2 * i + 1][0], x[2 * i + 1][1]),
+                                                                         false, false);
+                        const auto s1 = __builtin_amdgcn_permlane16_swap(rows::pack_bf16(x[2 * i][2], x[2 * i][3]),
+                                                                         rows::pack_bf16(x[2 * i + 1][2], x[2 * i + 1][3]),
+                                                                         false, false);
+                        p[i][0] = s0[0];
+                        p[i][1] = s1[0];
+                        p[i][2] = s0[1];
+                        p[i][3] = s1[1];
+                    }
+                    trade(p[0], p[1]);
+                    const int v = v0 + wv * WV + (4 * q + 2 * (r16 >> 3) + (qd & 1)) * 16 + 4 * (qd & 2);
+                    store_words(row, v, p[0]);
+                    store_words(row + 8, v, p[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        uint32_t p[2][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[0][e] = __builtin_bit_cast(uint32_t, x[i][e]);
+                            p[1][e] = __builtin_bit_cast(uint32_t, x[i + 1][e]);
+                        }
+                        trade(p[0], p[1]);
+                        const int v = v0 + wv * WV + (4 * q + i + (r16 >> 3)) * 16 + 4 * qd;
+                        store_words(row, v, p[0]);
+                        store_words(row + 8, v, p[1]);
+                    }
+                }
+            }
+        }
+    };
+
+    auto main_loop = [&](auto dma_tag) __attribute__((always_inline)) {
+        constexpr bool DMA_ON = decltype(dma_tag)::value;
+        int m0, v0;
+        tile_coords(0, m0, v0);
+        if constexpr (DMA_ON) {
+            make_src(m0, v0);
+            prologue();
+        }
+        for (int i = 0; i < n_my; ++i) {
+            // K tile 0 has landed; K tile 1 may still be in flight
+            if (nk > 1)
+                wait_vm<LW + LH>();
+            else
+                wait_vm<0>();
+            bar();
+            int rw = w0 * W_TILE, rh = H_BASE, kt = 0;
+            int sc_at = next_w(next_w(rw));   // one K tile: the stage it does not use
+            if constexpr (DMA_ON) {
+                if (nk == 1)
+                    issue_scales(sc_at, m0, v0);
+            }
+#pragma unroll
+            for (int a = 0; a < AV; ++a)
+                af[a] = *(const i32x4_t *)(smem + a_addr + rw + a * 16 * BK);
+#pragma unroll
+            for (int b = 0; b < AM; ++b)
+                bf[0][b] = *(const i32x4_t *)(smem + b_addr + rh + b * 16 * BK);
+            for (; kt + 2 < nk; ++kt) {
+                // W's rows of K tile kt + 2 go to the stage the last barrier freed; the wait
+                // leaves them in flight and needs the rest, K tile kt + 1
+                if constexpr (DMA_ON)
+                    issue_w(next_w(next_w(rw)), kt + 2);
+                mma_load(rw, rh, 1, 0);
+                interleave(DMA_ON ? LW : 0);
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vm<LW>();
+                bar();
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (DMA_ON)
+                    issue_h(rh, kt + 2);
+                rw = next_w(rw);
+                rh = next_h(rh);
+                mma_load(rw, rh, 0, 1);
+                interleave(DMA_ON ? LH : 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            for (; kt < nk; ++kt) {
+                mma_load(rw, rh, 1, 0);
+                if (kt + 1 < nk) {
+                    wait_vm<0>();
+                    bar();
+                    sc_at = rw;   // K tile nk - 2: its stage is free
+                    if constexpr (DMA_ON)
+                        issue_scales(sc_at, m0, v0);
+                    rw = next_w(rw);
+                    rh = next_h(rh);
+                }
+                mma_load(rw, rh, 0, 1);   // after the last K tile its reads are unused
+            }
+            // The scales have landed, and every wave's last fragments are in registers.  The
+            // stores go first, then the next tile's requests: its first wait then leaves its
+            // second K tile in flight instead of waiting for it behind these stores.
+            wait_vm<0>();
+            bar();
+            epilogue((const float *)(smem + sc_at), m0, v0);
+            zero_acc();
+            w0 = (sc_at / W_TILE + 1) % WST;
+            if (i + 1 < n_my) {
+                tile_coords(i + 1, m0, v0);
+                if constexpr (DMA_ON) {
+                    make_src(m0, v0);
+                    prologue();
+                }
+            }
+        }
+    };
+    if (wave < DMAW)
+        main_loop(std::true_type{});
+    else
+        main_loop(std::false_type{});
+}
+
+// Small tiles: few rows, or too few 256 x 256 tiles to fill the chip.  BM x BV outputs per
+// workgroup of four waves, WGM of them side by side along the rows; K tiles of 128 codes
+// requested straight to LDS, NSTAGE - 1 of them ahead, in a ring with one barrier per step.
+// Several workgroups share a CU, so one's start and end lie under the others' streams.
+// STREAM: W is read once (one row tile): its requests take the streaming cache policy.
+template <int BM, int BV, int WGM, int NSTAGE, bool STREAM, bool OUT_BF16>
+__global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__restrict__ Hq,
+                                                              const float *__restrict__ hs,
+                                                              const int32_t *__restrict__ rows_dev, int32_t max_rows,
+                                                              const int8_t *__restrict__ Wq,
+                                                              const float *__restrict__ ws, int32_t V, int32_t d,
+                                                              void *__restrict__ out, int64_t ldo)
+{
+    constexpr int BK = 128, CHUNKS = BK / 16, RPI = 64 / CHUNKS;
+    constexpr int WGV = 4 / WGM, WM = BM / WGM, WV = BV / WGV, AM = WM / 16, AV = WV / 16;
+    constexpr int W_TILE = BV * BK, STAGE = W_TILE + BM * BK;
+    constexpr int LW = BV / RPI / 4, LH = BM / RPI / 4, T = LW + LH;   // requests per wave and K tile
+    static_assert(LW >= 1 && LH >= 1 && NSTAGE >= 3 && (NSTAGE - 2) * T < 64, "requests");
+    constexpr int kPolicy = STREAM ? 2 : 0;   // NT: streaming
+    __shared__ __attribute__((aligned(1024))) char smem[NSTAGE * STAGE];
+
+    const int rows = (int)rows::row_count(rows_dev, max_rows);
+    const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, nblk = nvt * nmt;
+    const int b = blockIdx.x;
+    if (b >= nblk)
+        return;
+    // the workgroups of one XCD take a contiguous run of tiles, the row tiles of a vocabulary
+    // tile one after another, so that they share its W rows in that XCD's L2
+    const int q8 = nblk >> 3, rem = nblk & 7, xcd = b & 7, slot = b >> 3;
+    const int t = (xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8) + slot;
+    const int m0 = t % nmt * BM, v0 = t / nmt * BV;
+    const int nk = (d + BK - 1) / BK;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wv = wave % WGV, wm = wave / WGV;
+    auto swz = [](int r) { return (r >> 1) & 7; };
+    const int8_t *src[T];
+    int chunk[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+        const int r = (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS;
+        chunk[j] = ((lane % CHUNKS) ^ swz(r)) * 16;
+        src[j] = j < LW ? Wq + (int64_t)min(v0 + r, V - 1) * d : Hq + (int64_t)min(m0 + r, rows - 1) * d;
+        src[j] += chunk[j];
+    }
+    auto issue = [&](int stage, int kt) __attribute__((always_inline)) {
+        const int kb = kt * BK;
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            const int8_t *p = kb + chunk[j] < d ? src[j] + kb : kZeroCodes;
+            const int at = stage * STAGE + (j < LW ? (wave * LW + j) * 1024 : W_TILE + (wave * LH + j - LW) * 1024);
+            if (j < LW)
+                __builtin_amdgcn_global_load_lds((const void *)p, (lds_void_t *)(smem + at), 16, 0, kPolicy);
+            else
+                __builtin_amdgcn_global_load_lds((const void *)p, (lds_void_t *)(smem + at), 16, 0, 0);
+        }
+    };
+    i32x4_t acc[AV][AM];
+#pragma unroll
+    for (int a = 0; a < AV; ++a)
+#pragma unroll
+        for (int m = 0; m < AM; ++m)
+            acc[a][m] = i32x4_t{0, 0, 0, 0};
+    const int r16 = lane & 15, qd = lane >> 4;
+    const int lane_chunk = (qd ^ swz(r16)) * 16;
+    const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = W_TILE + (wm * WM + r16) * BK + lane_chunk;
+
+#pragma unroll
+    for (int s = 0; s < NSTAGE - 1; ++s)
+        if (s < nk)
+            issue(s, s);
+    int rd = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        // K tile kt has landed; the younger ones (NSTAGE - 2, fewer at the end) may not have
+        if (kt + NSTAGE - 1 <= nk)
+            wait_vm<(NSTAGE - 2) * T>();
+        else
+            wait_vm<0>();
+        bar();   // every wave's part of it, and every wave is done with the stage read before
+        if (kt + NSTAGE - 1 < nk)
+            issue(rd == 0 ? NSTAGE - 1 : rd - 1, kt + NSTAGE - 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            i32x4_t af[AV], bf[AM];
+#pragma unroll
+            for (int a = 0; a < AV; ++a)
+                af[a] = *(const i32x4_t *)(smem + rd * STAGE + ((a_addr + a * 16 * BK) ^ (64 * s)));
+#pragma unroll
+            for (int m = 0; m < AM; ++m)
+                bf[m] = *(const i32x4_t *)(smem + rd * STAGE + ((b_addr + m * 16 * BK) ^ (64 * s)));
+#pragma unroll
+            for (int a = 0; a < AV; ++a)
+#pragma unroll
+                for (int m = 0; m < AM; ++m)
+                    acc[a][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[a], bf[m], acc[a][m], 0, 0, 0);
+        }
+        rd = rd + 1 == NSTAGE ? 0 : rd + 1;
+    }
+    const bool vec = ((uintptr_t)out & 15) == 0 && (ldo & 3) == 0;
+#pragma unroll
+    for (int a = 0; a < AV; ++a) {
+        const int v = v0 + wv * WV + a * 16 + qd * 4;
+        if (v >= V)
+            continue;
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = ws[min(v + e, V - 1)];
+#pragma unroll
+        for (int m = 0; m < AM; ++m) {
+            const int row = m0 + wm * WM + m * 16 + r16;
+            if (row >= rows)
+                continue;
+            const float h = hs[row];
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = (float)acc[a][m][e] * h * w[e];
+            store4<OUT_BF16>(out, (int64_t)row * ldo + v, x, v, V, vec);
+        }
+    }
+}
+
 }  // namespace
 
+// Which form runs, from the sizes and the alignment alone (times of one launch on an MI355X,
+// bf16 output; the forms give the same bits):
+//  * codes that are not 16-byte aligned rows (d % 16 != 0): gemm_int8_any_kernel.
+//  * at most 32 rows, at most 64 rows: W is streamed once past a row tile of 32 or 64 rows.
+//    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 147 us with the 256 x 256 form; 64 rows:
+//    107 against 146 us.  Vocabulary tiles of 128 entries, or of 64 where that gives less than
+//    one workgroup per CU.
+//  * more rows: 256 x 256 tiles where there are enough to fill a good part of the chip, else
+//    64 x 64.  300 x 30000 x 2048 (236 tiles): 32 against 45 us; 1000 x 10000 x 1024 (160):
+//    21 against 30 us; 1024 x 4096 x 4096 (64): 40 against 34 us; 200 x 8192 x 4096 (32): 44
+//    against 19 us.  The two meet near 80 tiles on 256 CUs.
 hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *count, int64_t rows, const int8_t *Wq,
                             const float *ws, int64_t V, int64_t d, void *out, bool out_bf16, int64_t ldo,
                             hipStream_t stream)
 {
-    const bool aligned = d % 16 == 0 && ((uintptr_t)Hq & 15) == 0 && ((uintptr_t)Wq & 15) == 0;
-    const dim3 grid((unsigned)(((V + 63) / 64) * ((rows + 63) / 64)));
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, Hq, hs, count, (int32_t)rows, Wq, ws, (int32_t)V,
-                           (int32_t)d, out, ldo);
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess)
+        (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    auto tiles = [&](int64_t bm, int64_t bv) { return ((V + bv - 1) / bv) * ((rows + bm - 1) / bm); };
+    auto go = [&](auto kernel, int64_t grid, int threads, auto... more) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, Hq, hs, count, (int32_t)rows, Wq,
+                           ws, (int32_t)V, (int32_t)d, out, ldo, more...);
+    };
+    auto pick = [&](auto bf16_tag) {
+        constexpr bool B = decltype(bf16_tag)::value;
+        if (d % 16 != 0 || ((uintptr_t)Hq & 15) || ((uintptr_t)Wq & 15))
+            return go(gemm_int8_any_kernel<B>, tiles(64, 64), 256);
+        if (rows <= 32 && tiles(32, 128) >= cus)
+            return go(gemm_int8_small_kernel<32, 128, 1, 4, true, B>, tiles(32, 128), 256);
+        if (rows <= 32)
+            return go(gemm_int8_small_kernel<32, 64, 1, 4, true, B>, tiles(32, 64), 256);
+        if (rows <= 64 && tiles(64, 128) >= cus)
+            return go(gemm_int8_small_kernel<64, 128, 1, 3, true, B>, tiles(64, 128), 256);
+        if (tiles(256, 256) * 16 < cus * 5)
+            return go(gemm_int8_small_kernel<64, 64, 2, 4, false, B>, tiles(64, 64), 256);
+        // one persistent workgroup per CU, a multiple of the eight XCDs
+        const int64_t grid = std::min<int64_t>(std::max(8, cus / 8 * 8), (tiles(256, 256) + 7) / 8 * 8);
+        if (d % 128 == 0)
+            go(gemm_int8_kernel<B, false>, grid, 512, kDefaultGroupM);
+        else
+            go(gemm_int8_kernel<B, true>, grid, 512, kDefaultGroupM);
     };
     if (out_bf16)
-        aligned ? go(gemm_int8_any_kernel<true, true>) : go(gemm_int8_any_kernel<true, false>);
+        pick(std::true_type{});
     else
-        aligned ? go(gemm_int8_any_kernel<false, true>) : go(gemm_int8_any_kernel<false, false>);
+        pick(std::false_type{});
     return hipGetLastError();
 }
 
