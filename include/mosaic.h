@@ -422,20 +422,21 @@ mosaic_status_t mosaic_masked_logits_int8(const void *H, int64_t L, int64_t d, m
  *                   gradient too, in the same call.  It may be logits itself (same pointer
  *                   and stride); no other overlap is allowed.
  *   grad_loss       NULL (1) or float[M], the gradient with respect to loss.
- *   workspace       >= mosaic_distill_topk_workspace_bytes(M, V) bytes, 16-byte aligned
- *                   (NULL if that is 0); calls that overlap in time need one each.
+ *   workspace       >= mosaic_distill_topk_workspace_bytes(M, V, K) bytes, 16-byte
+ *                   aligned (NULL if that is 0); calls that overlap in time need one each.
  * Rows >= n of every output are not written.  M == 0: OK, nothing enqueued.  V == 0 with M >
  * 0, a NULL required pointer, misalignment, strides below V or a short workspace:
- * INVALID_ARG.  M or V of 2^31 and more: UNSUPPORTED. */
+ * INVALID_ARG.  M of 2^31 and more, V of more than 2^30: UNSUPPORTED. */
 mosaic_status_t mosaic_distill_topk(const void *logits, int64_t ldz, int64_t M, int64_t V, mosaic_dtype_t dtype,
                                     const void *teacher_logits, mosaic_dtype_t teacher_dtype,
                                     const int32_t *teacher_ids, int64_t K, float temperature, const int32_t *count,
                                     float *loss, float *stats, const float *grad_loss, void *grad, int64_t ldg,
                                     void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Workspace bytes of mosaic_distill_topk for M rows over V vocabulary entries (0 where every
- * row has a workgroup of its own), or -1 on a negative size. */
-int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V);
+/* Workspace bytes of mosaic_distill_topk for M rows over V vocabulary entries and K teacher
+ * logits (0 where every row has a workgroup of its own), or -1 on a negative size or K >
+ * 1024. */
+int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V, int64_t K);
 
 /* The gradient alone, from the stats that mosaic_distill_topk left for the same logits and
  * teacher: for a backward pass that comes later.  Arguments and errors as there (grad

@@ -15,6 +15,13 @@
 //
 // HBM bounds both directions: the loss reads the logits once, the gradient reads and writes
 // them.
+//  * distill_row_kernel: a workgroup per row.  Loss and gradient together keep the row in
+//    registers between the two, so the logits are read once.
+//  * distill_part_kernel, distill_split_kernel: rows split over several workgroups, for few
+//    rows; the first leaves a maximum and a sum of each part, the second joins them.  The
+//    second also computes the gradient alone, from the kept statistics.
+// The gradient's bulk T g q_v is written first, without regard to the teacher; then the few
+// entries that the teacher names are written again with their p taken off.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,209 +36,547 @@ namespace {
 using namespace rows;
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kInf = __builtin_inff();
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// -inf stands for nothing seen yet, and (-inf) - (-inf) would be NaN
+__device__ __forceinline__ float ref_of(float m) { return m == -kInf ? 0.0f : m; }
 
 // Running maximum and sum of exp((z - max) / T) of a set of logits; c = log2(e) / T.
 struct MaxSum {
-    float m = -__builtin_inff(), s = 0.0f;
+    float m = -kInf, s = 0.0f;
 
-    // -inf stands for nothing seen yet, and (-inf) - (-inf) would be NaN
-    __device__ __forceinline__ static float ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
-
-    template <int N>
-    __device__ __forceinline__ void add(const float (&z)[N], float c)
+    __device__ __forceinline__ void add(const float (&z)[8], float c)
     {
-        float mx = z[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i)
-            mx = fmaxf(mx, z[i]);
+        float mx = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
         if (mx > m) {
-            s *= exp2f((m - mx) * c);
+            s *= fast_exp2((m - mx) * c);
             m = mx;
         }
-        const float r = ref(m);
+        const float r = ref_of(m);
+        float e[8];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            s += exp2f((z[i] - r) * c);
+        for (int i = 0; i < 8; ++i)
+            e[i] = fast_exp2((z[i] - r) * c);
+        s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
     }
-
     __device__ __forceinline__ void join(float m2, float s2, float c)
     {
-        const float mx = fmaxf(m, m2), r = ref(mx);
-        s = s * exp2f((m - r) * c) + s2 * exp2f((m2 - r) * c);
+        const float mx = fmaxf(m, m2), r = ref_of(mx);
+        s = s * fast_exp2((m - r) * c) + s2 * fast_exp2((m2 - r) * c);
         m = mx;
     }
-};
-
-// The teacher's side of one row, in LDS.
-struct Teacher {
-    int32_t id[kDistillMaxK];
-    float p[kDistillMaxK];      // 0 for an absent entry
-    float z[kDistillMaxK];      // the student's logit at the entry
-    float red[16];
-};
-
-// Fills t from the row's K entries (every thread takes part; ends with a barrier).  Returns
-// sum_j p_j log p_j, and whether any entry is present.
-template <bool BF16, int NW>
-__device__ __forceinline__ float load_teacher(const Distill &a, int64_t row, Teacher &t, bool &present)
-{
-    const float c = kLog2e / a.temperature;
-    float mx = -__builtin_inff();
-    int any = 0;
-    for (int j = threadIdx.x; j < a.K; j += 64 * NW) {
-        const int32_t id = a.ids[row * a.K + j];
-        float x[1];
-        if (a.top_bf16)
-            load<true, 1>(a.top, row * a.K + j, x);
-        else
-            load<false, 1>(a.top, row * a.K + j, x);
-        const bool here = id >= 0 && id < a.V && x[0] != -__builtin_inff();
-        float z[1] = {0.0f};
-        if (here)
-            load<BF16, 1>(a.Z, row * a.ldz + id, z);
-        t.id[j] = here ? id : -1;
-        t.p[j] = x[0];
-        t.z[j] = z[0];
-        mx = here ? fmaxf(mx, x[0]) : mx;
-        any |= here;
+    __device__ __forceinline__ void join_wave(float c)
+    {
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1)
+            join(__shfl_xor(m, o, 64), __shfl_xor(s, o, 64), c);
     }
-    mx = block_reduce<NW>(mx, MaxOp{}, t.red);
-    present = __syncthreads_or(any);
+};
+
+// The teacher's side of one row, in LDS (dynamic: 32 + 3 K + table words).
+struct Teacher {
+    float *part;        // [2][16] maxima and sums of the waves
+    float *p;           // [K], 0 for an absent entry
+    float *z;           // [K] the student's logits at the entries
+    int32_t *id;        // [K], -1 for an absent entry
+    int32_t *table;     // set of the ids: open addressing, a power of two >= 2 K slots
+    int slots;
+    int32_t *flags;     // present, repeated
+    float *entropy;     // sum_j p_j log p_j
+
+    __device__ __forceinline__ Teacher(int32_t *lds, int K, int n_slots)
+    {
+        part = (float *)lds;
+        flags = lds + 32;
+        entropy = (float *)(lds + 34);
+        p = (float *)(lds + 36);
+        z = p + K;
+        id = (int32_t *)(z + K);
+        table = id + K;
+        slots = n_slots;
+    }
+};
+
+// Slots of the id set, and the LDS bytes of a Teacher.
+int table_slots(int K)
+{
+    int n = 64;
+    while (n < 2 * K)
+        n *= 2;
+    return n;
+}
+size_t teacher_bytes(int K) { return (size_t)(36 + 3 * K + table_slots(K)) * 4; }
+
+// Fills t from the row's K entries; run by one wave, visible to the others after a barrier.
+// The student's logits at the entries come from z_at (in the order of the entries) where it
+// is given, else from the logits of the row, those with lo <= c_j < hi only.
+template <bool BF16>
+__device__ __forceinline__ void load_teacher(const Distill &a, int64_t row, const Teacher &t, const float *z_at, int lo,
+                                             int hi)
+{
+    const int lane = threadIdx.x & 63;
+    const float c = kLog2e / a.temperature;
+    for (int i = lane; i < t.slots; i += 64)
+        t.table[i] = -1;
+    float mx = -kInf;
+    bool any = false;
+    for (int j = lane; j < a.K; j += 64) {
+        const int32_t id = a.ids[row * a.K + j];
+        const float x = load1(a.top, row * a.K + j, a.top_bf16);
+        const bool here = id >= 0 && id < a.V && x != -kInf;
+        float z = 0.0f;
+        if (here && id >= lo && id < hi)
+            z = z_at ? z_at[j] : load1(a.Z, row * a.ldz + id, BF16);
+        t.id[j] = here ? id : -1;
+        t.p[j] = x;
+        t.z[j] = z;
+        mx = here ? fmaxf(mx, x) : mx;
+        any = any || here;
+    }
+    mx = wave_reduce(mx, MaxOp{});
+    const bool present = __any(any);
     float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += 64 * NW) {
-        const float e = t.id[j] >= 0 ? exp2f((t.p[j] - mx) * c) : 0.0f;
+    for (int j = lane; j < a.K; j += 64) {
+        const float e = t.id[j] >= 0 ? fast_exp2((t.p[j] - mx) * c) : 0.0f;
         t.p[j] = e;
         sum += e;
     }
-    sum = block_reduce<NW>(sum, AddOp{}, t.red);
+    sum = wave_reduce(sum, AddOp{});
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");   // the cleared table, before other lanes' entries
+    __builtin_amdgcn_wave_barrier();
     float h = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += 64 * NW) {
+    bool repeated = false;
+    for (int j = lane; j < a.K; j += 64) {
         const float p = present ? t.p[j] / sum : 0.0f;
         t.p[j] = p;
         h += p != 0.0f ? p * logf(p) : 0.0f;
-    }
-    return block_reduce<NW>(h, AddOp{}, t.red);
-}
-
-// The row's loss from its statistics, in every thread.
-template <int NW>
-__device__ __forceinline__ float row_loss(const Distill &a, Teacher &t, float entropy, float m, float l)
-{
-    const float T = a.temperature, inv = 1.0f / T;
-    float x = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += 64 * NW)
-        x += t.p[j] != 0.0f ? t.p[j] * ((t.z[j] - m) * inv - l) : 0.0f;
-    x = block_reduce<NW>(x, AddOp{}, t.red);
-    return T * T * (entropy - x);
-}
-
-// Gradient of one row from its statistics.  The bulk is written first, T g q_v everywhere;
-// then the entries the teacher names are written again with their p taken off.
-template <bool BF16, int VEC, int NW>
-__device__ __forceinline__ void row_grad(const Distill &a, Teacher &t, int64_t row, bool present, float m, float l)
-{
-    const float c = kLog2e / a.temperature, l2 = l * kLog2e;
-    const float g = a.temperature * (a.grad_loss ? a.grad_loss[row] : 1.0f);
-    for (int64_t v = threadIdx.x * VEC; v < a.V; v += 64 * NW * VEC) {
-        float z[VEC];
-        if (present) {
-            load<BF16, VEC>(a.Z, row * a.ldz + v, z);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                z[i] = g * exp2f((z[i] - m) * c - l2);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                z[i] = 0.0f;
-        }
-        store<BF16, VEC>(a.grad, row * a.ldg + v, z);
-    }
-    // every wave's stores have reached memory before any is overwritten
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    for (int j = threadIdx.x; j < a.K; j += 64 * NW) {
         const int32_t id = t.id[j];
         if (id < 0)
             continue;
-        float p = 0.0f;
-        bool first = true;
-        for (int i = 0; i < a.K; ++i) {
-            if (t.id[i] == id) {
-                first = first && i >= j;
-                p += t.p[i];
+        // at most K of >= 2 K slots are taken, so a free one is found
+        int s = (int)(((uint32_t)id * 2654435761u) >> 16) & (t.slots - 1);
+        for (;;) {
+            const int32_t old = atomicCAS(&t.table[s], -1, id);
+            if (old == -1 || old == id) {
+                repeated = repeated || old == id;
+                break;
             }
-        }
-        if (first) {   // an entry named twice is written once, with both shares
-            const float x[1] = {g * (exp2f((t.z[j] - m) * c - l2) - p)};
-            store<BF16, 1>(a.grad, row * a.ldg + id, x);
+            s = (s + 1) & (t.slots - 1);
         }
     }
-    __syncthreads();   // the teacher's arrays are refilled for the next row
+    h = wave_reduce(h, AddOp{});
+    repeated = __any(repeated);
+    if (lane == 0) {
+        t.flags[0] = present;
+        t.flags[1] = repeated;
+        *t.entropy = h;
+    }
 }
 
-// One row per workgroup.
-template <bool BF16, int VEC, int NW, bool LOSS>
-__global__ __launch_bounds__(64 * NW) void distill_row_kernel(const Distill a)
+// The row's loss from its statistics, in every lane of the calling wave.
+__device__ __forceinline__ float row_loss(const Distill &a, const Teacher &t, float m, float l)
 {
-    __shared__ Teacher t;
+    const float T = a.temperature, inv = 1.0f / T;
+    float x = 0.0f;
+    for (int j = threadIdx.x & 63; j < a.K; j += 64)
+        x += t.p[j] != 0.0f ? t.p[j] * ((t.z[j] - m) * inv - l) : 0.0f;
+    return T * T * (*t.entropy - wave_reduce(x, AddOp{}));
+}
+
+// Writes the gradient at the teacher's entries with lo <= c_j < hi again, with p taken off; the
+// bulk has been written before the last barrier.  g: T times the row's upstream gradient.
+template <bool BF16, int NT>
+__device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, int64_t row, int lo, int hi, float g,
+                                            float m, float l)
+{
+    const float c = kLog2e / a.temperature, l2 = l * kLog2e;
+    const bool repeated = t.flags[1];
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const int32_t id = t.id[j];
+        if (id < lo || id >= hi)   // absent ones are -1
+            continue;
+        float p = t.p[j];
+        if (repeated) {            // an entry named again is written once, by the first, with all shares
+            bool first = true;
+            p = 0.0f;
+            for (int i = 0; i < a.K; ++i) {
+                if (t.id[i] == id) {
+                    first = first && i >= j;
+                    p += t.p[i];
+                }
+            }
+            if (!first)
+                continue;
+        }
+        store1<BF16>(a.grad, row * a.ldg + id, g * (fast_exp2((t.z[j] - m) * c - l2) - p));
+    }
+}
+
+// eight logits to eight gradients T g q_v (0 in a row without teacher entries)
+__device__ __forceinline__ void grad8(float (&z)[8], float g, float m, float c, float l2, bool present = true)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        z[i] = present ? g * fast_exp2((z[i] - m) * c - l2) : 0.0f;
+}
+
+// running maxima and sums over chunks held in registers
+template <bool BF16>
+__device__ __forceinline__ void max8(Raw8<BF16> &r, float (&mx)[2])
+{
+    float z[8];
+    r.opaque();
+    r.get(z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        mx[0] = fmaxf(mx[0], z[2 * e]);
+        mx[1] = fmaxf(mx[1], z[2 * e + 1]);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void sum8(Raw8<BF16> &r, float ref, float c, float (&s)[2])
+{
+    float z[8];
+    r.opaque();
+    r.get(z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        s[0] += fast_exp2((z[2 * e] - ref) * c);
+        s[1] += fast_exp2((z[2 * e + 1] - ref) * c);
+    }
+}
+
+__device__ __forceinline__ float upstream(const Distill &a, int64_t row)
+{
+    return a.temperature * (a.grad_loss ? a.grad_loss[row] : 1.0f);
+}
+
+// Chunks of eight logits of [lo, hi), lo a multiple of eight: chunk i of this thread's is
+// lo / 8 + threadIdx.x + i * NT.  UN loads are issued before their values are used.
+template <bool BF16, int NT, typename F>
+__device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo, int hi, F f)
+{
+    constexpr int UN = BF16 ? 4 : 2;
+    const int64_t base = row * a.ldz;
+    const int full = lo + ((hi - lo) & ~7);
+    for (int v = lo + threadIdx.x * 8; v < full; v += UN * NT * 8) {
+        Raw8<BF16> r[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+            if (v + i * NT * 8 < full)
+                r[i].load(a.Z, base + v + i * NT * 8);
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            if (v + i * NT * 8 < full) {
+                float z[8];
+                r[i].get(z);
+                f(z, v + i * NT * 8, 8);
+            }
+        }
+    }
+    if (full < hi && threadIdx.x == NT - 1) {
+        Raw8<BF16> r;
+        r.fill(-kInf);
+        r.load_part(a.Z, base + full, hi - full);
+        float z[8];
+        r.get(z);
+        f(z, full, hi - full);
+    }
+}
+
+// Gradient bulk of the part [lo, hi) of a row, then the teacher's entries in it.
+template <bool BF16, int NT>
+__device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, int64_t row, int lo, int hi, float m,
+                                          float l)
+{
+    const float c = kLog2e / a.temperature, l2 = l * kLog2e, g = upstream(a, row);
+    if (t.flags[0])
+        for_chunks<BF16, NT>(a, row, lo, hi, [&](float (&z)[8], int v, int n) {
+            grad8(z, g, m, c, l2);
+            store_upto<BF16>(a.grad, row * a.ldg + v, z, n);
+        });
+    else
+        for (int v = lo + threadIdx.x * 8; v < hi; v += NT * 8) {
+            const float z[8] = {};
+            store_upto<BF16>(a.grad, row * a.ldg + v, z, hi - v);
+        }
+    __syncthreads();   // orders the two writes of an entry
+    fix_entries<BF16, NT>(a, t, row, lo, hi, g, m, l);
+}
+
+// Joins the waves' (m, s) of a workgroup: m and l of the row in every thread.  Its barrier also
+// publishes the teacher.
+template <int NT>
+__device__ __forceinline__ void join_block(MaxSum x, const Teacher &t, float c, float &m, float &l)
+{
+    x.join_wave(c);
+    if constexpr (NT == 64) {
+        __syncthreads();
+    } else {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            t.part[wave] = x.m;
+            t.part[16 + wave] = x.s;
+        }
+        __syncthreads();
+        x = MaxSum{t.part[0], t.part[16]};
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w)
+            x.join(t.part[w], t.part[16 + w], c);
+    }
+    m = x.m;
+    l = logf(x.s);
+}
+
+// One row per workgroup.  R > 0: the row stays in registers, R chunks of eight logits per
+// thread (V <= 8 NT R), and is read once; R = 0: a gradient reads it again.
+template <bool BF16, int NT, int R>
+__global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int slots)
+{
+    extern __shared__ int32_t lds[];
+    const Teacher t(lds, a.K, slots);
     const float c = kLog2e / a.temperature;
     const int64_t n = row_count(a.count, a.rows);
+    const int V = a.V, full = V & ~7;
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        bool present;
-        const float entropy = load_teacher<BF16, NW>(a, row, t, present);
-        float m, l;
-        if constexpr (LOSS) {
-            MaxSum x;
-            for (int64_t v = threadIdx.x * VEC; v < a.V; v += 64 * NW * VEC) {
-                float z[VEC];
-                load<BF16, VEC>(a.Z, row * a.ldz + v, z);
-                x.add(z, c);
+        MaxSum x;
+        Raw8<BF16> r[R > 0 ? R : 1], rest;   // whole chunks, and the last, shorter one
+        if (threadIdx.x < 64)
+            load_teacher<BF16>(a, row, t, nullptr, 0, V);
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int v = (i * NT + threadIdx.x) * 8;
+                r[i].fill(-kInf);
+                if (v < full)
+                    r[i].load(a.Z, row * a.ldz + v);
             }
-            m = block_reduce<NW>(x.m, MaxOp{}, t.red);
-            l = logf(block_reduce<NW>(x.s * exp2f((x.m - MaxSum::ref(m)) * c), AddOp{}, t.red));
-            const float loss = row_loss<NW>(a, t, entropy, m, l);
+            rest.fill(-kInf);
+            if (full < V && threadIdx.x == NT - 1)
+                rest.load_part(a.Z, row * a.ldz + full, V - full);
+            float mx[2] = {-kInf, -kInf};
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                max8(r[i], mx);
+            max8(rest, mx);
+            x.m = fmaxf(mx[0], mx[1]);
+            const float ref = ref_of(x.m);
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                sum8(r[i], ref, c, s);
+            if (full < V)
+                sum8(rest, ref, c, s);
+            x.s = s[0] + s[1];
+        } else {
+            for_chunks<BF16, NT>(a, row, 0, V, [&](float (&z)[8], int, int) { x.add(z, c); });
+        }
+        float m, l;
+        join_block<NT>(x, t, c, m, l);
+        const bool present = t.flags[0];
+        if (threadIdx.x < 64) {
+            const float loss = row_loss(a, t, m, l);
             if (threadIdx.x == 0) {
                 a.loss[row] = present ? loss : 0.0f;
                 a.stats[2 * row] = m;
                 a.stats[2 * row + 1] = l;
             }
+        }
+        if (a.grad) {
+            if constexpr (R > 0) {
+                const float l2 = l * kLog2e, g = upstream(a, row);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int v = (i * NT + threadIdx.x) * 8;
+                    if (v < full) {
+                        float z[8];
+                        r[i].opaque();
+                        r[i].get(z);
+                        grad8(z, g, m, c, l2, present);
+                        store8<BF16>(a.grad, row * a.ldg + v, z);
+                    }
+                }
+                if (full < V && threadIdx.x == NT - 1) {
+                    float z[8];
+                    rest.get(z);
+                    grad8(z, g, m, c, l2, present);
+                    store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
+                }
+                __syncthreads();   // orders the two writes of an entry
+                fix_entries<BF16, NT>(a, t, row, 0, V, g, m, l);
+            } else {
+                part_grad<BF16, NT>(a, t, row, 0, V, m, l);
+            }
+        }
+        __syncthreads();   // the teacher's arrays are refilled for the next row
+    }
+}
+
+// Part s of a row's `parts`: logits [lo, hi), multiples of eight but for the last.
+__device__ __forceinline__ void part_range(int V, int parts, int s, int &lo, int &hi)
+{
+    const int chunks = (V + 7) / 8, each = (chunks + parts - 1) / parts;
+    lo = min(s * each, chunks) * 8;
+    hi = min(min((s + 1) * each, chunks) * 8, V);
+    lo = min(lo, hi);
+}
+
+constexpr int kSplitThreads = 256;
+
+// (maximum, sum) of each part of each row into partials[row][part][2], and the student's
+// logits at the teacher's entries into z_at[row][K] (the gradient may overwrite them).
+template <bool BF16>
+__global__ __launch_bounds__(kSplitThreads) void distill_part_kernel(const Distill a, int parts,
+                                                                     float *__restrict__ z_at)
+{
+    __shared__ float red[8];
+    const float c = kLog2e / a.temperature;
+    const int64_t row = blockIdx.x / parts;
+    const int s = blockIdx.x % parts;
+    if (row >= row_count(a.count, a.rows))
+        return;
+    int lo, hi;
+    part_range(a.V, parts, s, lo, hi);
+    MaxSum x;
+    for_chunks<BF16, kSplitThreads>(a, row, lo, hi, [&](float (&z)[8], int, int) { x.add(z, c); });
+    x.join_wave(c);
+    if ((threadIdx.x & 63) == 0) {
+        red[threadIdx.x >> 6] = x.m;
+        red[4 + (threadIdx.x >> 6)] = x.s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 4; ++w)
+            x.join(red[w], red[4 + w], c);
+        a.partials[2 * blockIdx.x] = x.m;
+        a.partials[2 * blockIdx.x + 1] = x.s;
+    }
+    if (s == parts - 1)
+        for (int j = threadIdx.x; j < a.K; j += kSplitThreads) {
+            const int32_t id = a.ids[row * a.K + j];
+            z_at[row * a.K + j] = id >= 0 && id < a.V ? load1(a.Z, row * a.ldz + id, BF16) : 0.0f;
+        }
+}
+
+// Gradient of part blockIdx.x % cuts of a row.  parts > 0: the statistics are joined from the
+// row's partials, and the workgroup of the first part writes them and the loss; parts = 0:
+// they are given.
+template <bool BF16>
+__global__ __launch_bounds__(kSplitThreads) void distill_split_kernel(const Distill a, int slots, int parts, int cuts,
+                                                                      const float *__restrict__ z_at)
+{
+    extern __shared__ int32_t lds[];
+    const Teacher t(lds, a.K, slots);
+    const float c = kLog2e / a.temperature;
+    const int64_t n = row_count(a.count, a.rows);
+    for (int64_t b = blockIdx.x; b < n * cuts; b += gridDim.x) {
+        const int64_t row = b / cuts;
+        const int s = (int)(b % cuts);
+        int lo, hi;
+        part_range(a.V, cuts, s, lo, hi);
+        if (threadIdx.x < 64)
+            load_teacher<BF16>(a, row, t, z_at ? z_at + row * a.K : nullptr, z_at ? 0 : lo, z_at ? a.V : hi);
+        float m, l;
+        if (parts > 0) {
+            MaxSum x;
+            const int i = threadIdx.x & 63;   // parts <= 64
+            if (i < parts)
+                x = MaxSum{a.partials[2 * (row * parts + i)], a.partials[2 * (row * parts + i) + 1]};
+            x.join_wave(c);
+            m = x.m;
+            l = logf(x.s);
         } else {
             m = a.stats[2 * row];
             l = a.stats[2 * row + 1];
         }
+        __syncthreads();   // the teacher is there
+        if (parts > 0 && s == 0 && threadIdx.x < 64) {
+            const float loss = row_loss(a, t, m, l);
+            if (threadIdx.x == 0) {
+                a.loss[row] = t.flags[0] ? loss : 0.0f;
+                a.stats[2 * row] = m;
+                a.stats[2 * row + 1] = l;
+            }
+        }
         if (a.grad)
-            row_grad<BF16, VEC, NW>(a, t, row, present, m, l);
-        else
-            __syncthreads();
+            part_grad<BF16, kSplitThreads>(a, t, row, lo, hi, m, l);
+        __syncthreads();   // the teacher's arrays are refilled for the next row
     }
 }
 
-template <bool BF16, bool LOSS>
+// Parts of a row in the split form: about 2048 workgroups, of 4096 logits at least each.
+int parts_of(int64_t rows, int64_t V)
+{
+    return (int)std::max<int64_t>(1, std::min<int64_t>({64, 2048 / std::max<int64_t>(rows, 1), V / 4096}));
+}
+
+// Few rows of many logits go over several workgroups each.
+bool is_split(int64_t rows, int64_t V, bool grad) { return rows <= (grad ? 128 : 1024) && V >= 16384; }
+
+template <bool BF16>
 hipError_t run(const Distill &a, hipStream_t stream)
 {
-    const int64_t es = BF16 ? 2 : 4;
-    auto ok = [&](const void *p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); };
-    const bool vec = a.V % 8 == 0 && ok(a.Z, a.ldz) && ok(a.grad, a.ldg);
+    const int slots = table_slots(a.K);
+    const size_t lds = teacher_bytes(a.K);
+    if (is_split(a.rows, a.V, a.grad)) {
+        const int parts = parts_of(a.rows, a.V), cuts = a.grad ? parts : 1;
+        float *z_at = a.partials + 2 * a.rows * parts;
+        hipLaunchKernelGGL(distill_part_kernel<BF16>, dim3((unsigned)(a.rows * parts)), dim3(kSplitThreads), 0,
+                           stream, a, parts, z_at);
+        hipLaunchKernelGGL(distill_split_kernel<BF16>, dim3((unsigned)(a.rows * cuts)), dim3(kSplitThreads), lds,
+                           stream, a, slots, parts, cuts, z_at);
+        return hipGetLastError();
+    }
     const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20));
-    if (vec)
-        hipLaunchKernelGGL((distill_row_kernel<BF16, 8, 16, LOSS>), grid, dim3(1024), 0, stream, a);
+    auto go = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, stream, a, slots);
+    };
+    constexpr int W = BF16 ? 1 : 2;   // fp32 rows take twice the registers
+    if (a.V <= 64 * 8 * 4)
+        go(distill_row_kernel<BF16, 64, 4>, 64);
+    else if (a.V <= 256 * 8 * 8)
+        go(distill_row_kernel<BF16, 256, 8>, 256);
+    else if (!a.grad)
+        go(distill_row_kernel<BF16, 256, 0>, 256);
+    else if (a.V <= 1024 * 8 * 8)
+        go(distill_row_kernel<BF16, 1024, 8>, 1024);
+    else if (a.V <= 1024 * 8 * 16 / W)
+        go(distill_row_kernel<BF16, 1024, 16 / W>, 1024);
+    else if (a.V <= 1024 * 8 * 20 / W)
+        go(distill_row_kernel<BF16, 1024, 20 / W>, 1024);
     else
-        hipLaunchKernelGGL((distill_row_kernel<BF16, 1, 16, LOSS>), grid, dim3(1024), 0, stream, a);
+        go(distill_row_kernel<BF16, 1024, 0>, 1024);
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t run_grad(const Distill &a, hipStream_t stream)
+{
+    const int cuts = parts_of(a.rows, a.V);
+    hipLaunchKernelGGL(distill_split_kernel<BF16>, dim3((unsigned)std::min<int64_t>(a.rows * cuts, 1 << 20)),
+                       dim3(kSplitThreads), teacher_bytes(a.K), stream, a, table_slots(a.K), 0, cuts,
+                       (const float *)nullptr);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t distill_workspace_bytes(int64_t, int64_t) { return 0; }
+int64_t distill_workspace_bytes(int64_t rows, int64_t V, int64_t K)
+{
+    return is_split(rows, V, false) ? 4 * rows * (2 * parts_of(rows, V) + K) : 0;
+}
 
 hipError_t launch_distill(const Distill &a, bool z_bf16, hipStream_t stream)
 {
-    return z_bf16 ? run<true, true>(a, stream) : run<false, true>(a, stream);
+    return z_bf16 ? run<true>(a, stream) : run<false>(a, stream);
 }
 
 hipError_t launch_distill_grad(const Distill &a, bool z_bf16, hipStream_t stream)
 {
-    return z_bf16 ? run<true, false>(a, stream) : run<false, false>(a, stream);
+    return z_bf16 ? run_grad<true>(a, stream) : run_grad<false>(a, stream);
 }
 
 }  // namespace mosaic

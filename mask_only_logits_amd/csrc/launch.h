@@ -136,8 +136,9 @@ struct Distill {
     float *partials = nullptr;          // workspace of the split form
 };
 constexpr int kDistillMaxK = 1024;
-// Workspace bytes of launch_distill for `rows` rows (0: none needed).
-int64_t distill_workspace_bytes(int64_t rows, int64_t V);
+constexpr int64_t kDistillMaxV = (int64_t)1 << 30;
+// Workspace bytes of launch_distill (0: none needed).
+int64_t distill_workspace_bytes(int64_t rows, int64_t V, int64_t K);
 // loss and stats, and grad where it is given.
 hipError_t launch_distill(const Distill &a, bool z_bf16, hipStream_t stream);
 // grad from the stats.

@@ -196,9 +196,9 @@ mosaic_status_t mosaic_masked_logits_int8(const void *H, int64_t L, int64_t d, m
     return MOSAIC_OK;
 }
 
-int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V)
+int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V, int64_t K)
 {
-    return M < 0 || V < 0 ? -1 : mosaic::distill_workspace_bytes(M, V);
+    return M < 0 || V < 0 || K < 0 || K > mosaic::kDistillMaxK ? -1 : mosaic::distill_workspace_bytes(M, V, K);
 }
 
 // What both distillation entry points check of the arguments they share, and `a` filled from
@@ -222,7 +222,7 @@ static mosaic_status_t distill_args(const void *logits, int64_t ldz, int64_t M, 
         return MOSAIC_ERR_INVALID_ARG;
     if (grad == logits && ldg != ldz)
         return MOSAIC_ERR_INVALID_ARG;
-    if (M > kMaxPos || V > kMaxPos || K > mosaic::kDistillMaxK)
+    if (M > kMaxPos || V > mosaic::kDistillMaxV || K > mosaic::kDistillMaxK)
         return MOSAIC_ERR_UNSUPPORTED;
     a.Z = logits;
     a.ldz = ldz;
@@ -251,7 +251,7 @@ mosaic_status_t mosaic_distill_topk(const void *logits, int64_t ldz, int64_t M, 
                                            temperature, count, grad_loss, grad, ldg, a);
     if (s != MOSAIC_OK || a.rows == 0)
         return s;
-    const int64_t need = mosaic::distill_workspace_bytes(M, V);
+    const int64_t need = mosaic::distill_workspace_bytes(M, V, K);
     if (!loss || !stats || !aligned_to(loss, 4) || !aligned_to(stats, 8) || !aligned16(workspace) ||
         workspace_bytes < need || (need > 0 && !workspace))
         return MOSAIC_ERR_INVALID_ARG;

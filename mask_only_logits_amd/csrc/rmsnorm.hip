@@ -33,52 +33,74 @@ __device__ __forceinline__ float abs_bits(float x)
     return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
 }
 
-// Codes of VEC values already multiplied by top / amax (|y| <= top up to fp32 rounding), in
-// the low bytes of w[].  INT8: adding 1.5 * 2^23 leaves the nearest even integer in the
-// sum's low bits.  E4M3: v_cvt_pk_fp8_f32 rounds to nearest even, and 448 (1 + 2^-23) is
-// still 448.
-template <int VEC>
-__device__ __forceinline__ void make_codes(const float (&y)[VEC], bool int8, uint32_t (&w)[(VEC + 3) / 4])
+// Codes of eight values already multiplied by top / amax (|y| <= top up to fp32 rounding).
+// INT8: adding 1.5 * 2^23 leaves the nearest even integer in the sum's low bits.  E4M3:
+// v_cvt_pk_fp8_f32 rounds to nearest even, and 448 (1 + 2^-23) is still 448.
+__device__ __forceinline__ u32x2_t make_codes(const float (&y)[8], bool int8)
 {
 #pragma clang fp contract(off)   // y * inv rounds before the addition
+    u32x2_t w;
     if (int8) {
-        uint32_t b[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            b[i] = __builtin_bit_cast(uint32_t, y[i] + 12582912.0f);
-        if constexpr (VEC == 1) {
-            w[0] = b[0];
-        } else {
+        for (int i = 0; i < 2; ++i) {
+            uint32_t b[4];
 #pragma unroll
-            for (int i = 0; i < VEC / 4; ++i) {
-                const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
-                const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
-                w[i] = lo | (hi << 16);
-            }
+            for (int e = 0; e < 4; ++e)
+                b[e] = __builtin_bit_cast(uint32_t, y[4 * i + e] + 12582912.0f);
+            const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+            w[i] = lo | (hi << 16);
         }
     } else {
-        if constexpr (VEC == 1) {
-            w[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[0], 0, false);
-        } else {
 #pragma unroll
-            for (int i = 0; i < VEC / 4; ++i) {
-                const int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
-                w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], p, true);
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+            w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], p, true);
         }
     }
+    return w;
+}
+
+typedef u32x2_t u32x2_any __attribute__((aligned(1)));
+
+// The first n of eight codes.
+__device__ __forceinline__ void store_codes(uint8_t *q, const u32x2_t &w, int n)
+{
+    if (n >= 8) {
+        *(u32x2_any *)q = w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n)
+            q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+}
+
+// The elements k .. k + 7 of a row that lie before d, zeros behind them.
+template <bool BF16>
+__device__ __forceinline__ void load_upto(const void *p, int64_t off, int k, int d, float (&x)[8])
+{
+    Raw8<BF16> r;
+    if (k + 8 <= d) {
+        r.load(p, off + k);
+    } else {
+        r.fill(0.0f);
+        if (k < d)
+            r.load_part(p, off + k, d - k);
+    }
+    r.get(x);
 }
 
 // Power of two that keeps top / amax inside fp32 for the smallest rows (1 for all others).
 __device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
 
-// One row per WPR waves, a thread holding CH chunks of VEC elements (d <= 64 WPR CH VEC).
+// One row per WPR waves, a thread holding CH chunks of eight elements (d <= 512 WPR CH).
 // NORM off: y = x (plain quantization).
-template <bool BF16, bool NORM, int VEC, int WPR, int CH>
+template <bool BF16, bool NORM, int WPR, int CH>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(const RowsNorm a)
 {
     constexpr int RPB = WPR == 1 ? 4 : 1;   // rows per workgroup
-    constexpr int STEP = 64 * WPR * VEC;
+    constexpr int STEP = 512 * WPR;
     __shared__ float red[WPR];
     const int t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t n = row_count(a.count, a.rows);
@@ -86,44 +108,39 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
          row += (int64_t)gridDim.x * RPB) {
         const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
         const bool inside = src >= 0 && src < a.nsrc;   // a row id outside gives a row of NaN
-        float v[CH][VEC];
+        float v[CH][8];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = c * STEP + t * VEC;
+            const int k = c * STEP + t * 8;
+            if (inside) {
+                load_upto<BF16>(a.X, src * a.ldx, k, a.d, v[c]);
+                if (NORM && a.R) {
+                    float r[8];
+                    load_upto<BF16>(a.R, src * a.ldr, k, a.d, r);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                v[c][i] = 0.0f;
-            if (k < a.d) {
-                if (inside) {
-                    load<BF16, VEC>(a.X, src * a.ldx + k, v[c]);
-                    if (a.R) {
-                        float r[VEC];
-                        load<BF16, VEC>(a.R, src * a.ldr + k, r);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            v[c][i] += r[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        v[c][i] = __builtin_nanf("");
+                    for (int i = 0; i < 8; ++i)
+                        v[c][i] += r[i];
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[c][i] = __builtin_nanf("");
             }
         }
         if constexpr (NORM) {
             if (a.sum) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const int k = c * STEP + t * VEC;
+                    const int k = c * STEP + t * 8;
                     if (k < a.d)
-                        store<BF16, VEC>(a.sum, row * a.ldsum + k, v[c]);
+                        store_upto<BF16>(a.sum, row * a.ldsum + k, v[c], a.d - k);
                 }
             }
             float ss = 0.0f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
+                for (int i = 0; i < 8; ++i)
                     ss += v[c][i] * v[c][i];
             ss = block_reduce<WPR>(ss, AddOp{}, red);
             float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
@@ -135,25 +152,25 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
+                    for (int i = 0; i < 8; ++i)
                         s2 += (v[c][i] * down) * (v[c][i] * down);
                 s2 = block_reduce<WPR>(s2, AddOp{}, red);
                 rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const int k = c * STEP + t * VEC;
+                const int k = c * STEP + t * 8;
                 if (k < a.d) {
-                    float g[VEC];
+                    float g[8];
                     if (a.gain_bf16)
-                        load<true, VEC>(a.gain, k, g);
+                        load_upto<true>(a.gain, 0, k, a.d, g);
                     else
-                        load<false, VEC>(a.gain, k, g);
+                        load_upto<false>(a.gain, 0, k, a.d, g);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
+                    for (int i = 0; i < 8; ++i)
                         v[c][i] = v[c][i] * rstd * g[i];
                     if (a.out)
-                        store<BF16, VEC>(a.out, row * a.d + k, v[c]);
+                        store_upto<BF16>(a.out, row * a.d + k, v[c], a.d - k);
                 }
             }
             if (!a.q)
@@ -163,7 +180,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
+            for (int i = 0; i < 8; ++i)
                 amax = MaxBitsOp{}(amax, abs_bits(v[c][i]));
         amax = block_reduce<WPR>(amax, MaxBitsOp{}, red);
         const float top = a.code_int8 ? 127.0f : 448.0f;
@@ -173,18 +190,13 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
         const float up = code_lift(amax), inv = fine ? top / (amax * up) : 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = c * STEP + t * VEC;
+            const int k = c * STEP + t * 8;
             if (k < a.d) {
-                float y[VEC];
-                uint32_t w[(VEC + 3) / 4];
+                float y[8];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
+                for (int i = 0; i < 8; ++i)
                     y[i] = fine ? v[c][i] * up * inv : 0.0f;
-                make_codes<VEC>(y, a.code_int8, w);
-                if constexpr (VEC == 8)
-                    *(u32x2_t *)(a.q + row * a.d + k) = u32x2_t{w[0], w[1]};
-                else
-                    a.q[row * a.d + k] = (uint8_t)w[0];
+                store_codes(a.q + row * a.d + k, make_codes(y, a.code_int8), a.d - k);
             }
         }
         if (t == 0)
@@ -206,14 +218,8 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
         auto element = [&](int k) {
             if (!inside)
                 return __builtin_nanf("");
-            float x[1];
-            load<BF16, 1>(a.X, src * a.ldx + k, x);
-            if (NORM && a.R) {
-                float r[1];
-                load<BF16, 1>(a.R, src * a.ldr + k, r);
-                x[0] += r[0];
-            }
-            return x[0];
+            const float x = load1(a.X, src * a.ldx + k, BF16);
+            return NORM && a.R ? x + load1(a.R, src * a.ldr + k, BF16) : x;
         };
         float rstd = 1.0f;
         if constexpr (NORM) {
@@ -235,16 +241,7 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
                 rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
             }
         }
-        auto normed = [&](float x, int k) {
-            if constexpr (!NORM)
-                return x;
-            float g[1];
-            if (a.gain_bf16)
-                load<true, 1>(a.gain, k, g);
-            else
-                load<false, 1>(a.gain, k, g);
-            return x * rstd * g[0];
-        };
+        auto normed = [&](float x, int k) { return NORM ? x * rstd * load1(a.gain, k, a.gain_bf16) : x; };
         float amax = 0.0f;
         if (a.q) {
             for (int k = threadIdx.x; k < a.d; k += 1024)
@@ -255,17 +252,14 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
         const bool fine = amax > 0.0f && amax < __builtin_inff();
         const float up = code_lift(amax), inv = fine ? top / (amax * up) : 0.0f;
         for (int k = threadIdx.x; k < a.d; k += 1024) {
-            const float x[1] = {element(k)};
-            const float y[1] = {normed(x[0], k)};
+            const float x = element(k), y = normed(x, k);
             if (NORM && a.sum)
-                store<BF16, 1>(a.sum, row * a.ldsum + k, x);
+                store1<BF16>(a.sum, row * a.ldsum + k, x);
             if (NORM && a.out)
-                store<BF16, 1>(a.out, row * a.d + k, y);
+                store1<BF16>(a.out, row * a.d + k, y);
             if (a.q) {
-                const float z[1] = {fine ? y[0] * up * inv : 0.0f};
-                uint32_t w[1];
-                make_codes<1>(z, a.code_int8, w);
-                a.q[row * a.d + k] = (uint8_t)w[0];
+                float z[8] = {fine ? y * up * inv : 0.0f};
+                a.q[row * a.d + k] = (uint8_t)make_codes(z, a.code_int8)[0];
             }
         }
         if (a.q && threadIdx.x == 0)
@@ -280,42 +274,28 @@ unsigned grid_of(int64_t rows, int per_block)
     return (unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 1 << 20);
 }
 
-template <bool BF16, bool NORM, int VEC, int WPR, int CH>
+template <bool BF16, bool NORM, int WPR, int CH>
 void run(const RowsNorm &a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((rows_norm_kernel<BF16, NORM, VEC, WPR, CH>), dim3(grid_of(a.rows, WPR == 1 ? 4 : 1)),
+    hipLaunchKernelGGL((rows_norm_kernel<BF16, NORM, WPR, CH>), dim3(grid_of(a.rows, WPR == 1 ? 4 : 1)),
                        dim3(WPR == 1 ? 256 : 64 * WPR), 0, stream, a);
 }
 
 template <bool BF16, bool NORM>
 void pick(const RowsNorm &a, hipStream_t stream)
 {
-    const int64_t es = BF16 ? 2 : 4;
-    auto ok = [&](const void *p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); };
-    // whole 8-element chunks at 16-byte (codes: 8-byte) places
-    const bool vec = a.d % 8 == 0 && ok(a.X, a.ldx) && ok(a.R, a.ldr) && ok(a.sum, a.ldsum) && ok(a.out, a.d) &&
-                     ((uintptr_t)a.q & 7) == 0 && ((uintptr_t)a.gain & 15) == 0;
-    if (vec) {
-        if (a.d <= 512)
-            return run<BF16, NORM, 8, 1, 1>(a, stream);
-        if (a.d <= 1024)
-            return run<BF16, NORM, 8, 1, 2>(a, stream);
-        if (a.d <= 2048)
-            return run<BF16, NORM, 8, 4, 1>(a, stream);
-        if (a.d <= 4096)
-            return run<BF16, NORM, 8, 4, 2>(a, stream);
-        if (a.d <= 8192)
-            return run<BF16, NORM, 8, 16, 1>(a, stream);
-        if (a.d <= 16384)
-            return run<BF16, NORM, 8, 16, 2>(a, stream);
-    } else {
-        if (a.d <= 512)
-            return run<BF16, NORM, 1, 1, 8>(a, stream);
-        if (a.d <= 2048)
-            return run<BF16, NORM, 1, 4, 8>(a, stream);
-        if (a.d <= 8192)
-            return run<BF16, NORM, 1, 16, 8>(a, stream);
-    }
+    if (a.d <= 512)
+        return run<BF16, NORM, 1, 1>(a, stream);
+    if (a.d <= 1024)
+        return run<BF16, NORM, 1, 2>(a, stream);
+    if (a.d <= 2048)
+        return run<BF16, NORM, 4, 1>(a, stream);
+    if (a.d <= 4096)
+        return run<BF16, NORM, 4, 2>(a, stream);
+    if (a.d <= 8192)
+        return run<BF16, NORM, 16, 1>(a, stream);
+    if (a.d <= 16384)
+        return run<BF16, NORM, 16, 2>(a, stream);
     hipLaunchKernelGGL((rows_norm_long_kernel<BF16, NORM>), dim3(grid_of(a.rows, 1)), dim3(1024), 0, stream, a);
 }
 

@@ -69,55 +69,109 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
 
-// VEC elements from element offset off: VEC == 8 with 16-byte loads (off a multiple of 8,
-// base 16-byte aligned), VEC == 1 with one element's load.
-template <bool BF16, int VEC>
-__device__ __forceinline__ void load(const void *p, int64_t off, float (&x)[VEC])
-{
-    if constexpr (VEC == 8) {
+// Rows may start at any element, so the vector types are aligned to one: gfx950 takes the
+// same 16-byte loads and stores at any address, at full rate where it is aligned.
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
+// Eight elements as they are stored: 16 bytes (bf16) or 32 (fp32).
+template <bool BF16>
+struct Raw8 {
+    u32x4_t w[BF16 ? 1 : 2];
+
+    __device__ __forceinline__ void load(const void *p, int64_t off)
+    {
         if constexpr (BF16) {
-            const u32x4_t w = *(const u32x4_t *)((const uint16_t *)p + off);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(w[i]);
-                x[2 * i + 1] = bf16_hi(w[i]);
-            }
+            w[0] = *(const u32x4_any *)((const uint16_t *)p + off);
         } else {
-            const f32x4_t a = *(const f32x4_t *)((const float *)p + off);
-            const f32x4_t b = *(const f32x4_t *)((const float *)p + off + 4);
+            w[0] = __builtin_bit_cast(u32x4_t, (f32x4_t) * (const f32x4_any *)((const float *)p + off));
+            w[1] = __builtin_bit_cast(u32x4_t, (f32x4_t) * (const f32x4_any *)((const float *)p + off + 4));
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = a[i];
-                x[4 + i] = b[i];
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
+                x[2 * i] = bf16_lo(w[0][i]);
+                x[2 * i + 1] = bf16_hi(w[0][i]);
+            } else {
+                // (copies: a bit cast of a vector's element itself takes its first one)
+                const uint32_t lo = w[0][i], hi = w[1][i];
+                x[i] = __builtin_bit_cast(float, lo);
+                x[4 + i] = __builtin_bit_cast(float, hi);
             }
         }
+    }
+    __device__ __forceinline__ void fill(float v)
+    {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v), f = BF16 ? (b & 0xffff0000u) | (b >> 16) : b;
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            w[i] = u32x4_t{f, f, f, f};
+    }
+    // Keeps the compiler from carrying the unpacked floats of an earlier use past this point:
+    // rows held in registers are held as they are stored.
+    __device__ __forceinline__ void opaque()
+    {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            asm volatile("" : "+v"(w[i]));
+    }
+    // the first n < 8 elements (n >= 1), the rest left as they are
+    __device__ __forceinline__ void load_part(const void *p, int64_t off, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < 7; ++i) {
+            if (i >= n)
+                continue;
+            if constexpr (BF16) {
+                const uint32_t e = ((const uint16_t *)p)[off + i];
+                w[0][i >> 1] = i & 1 ? (w[0][i >> 1] & 0xffffu) | (e << 16) : (w[0][i >> 1] & 0xffff0000u) | e;
+            } else {
+                w[i >> 2][i & 3] = ((const uint32_t *)p)[off + i];
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float load1(const void *p, int64_t off, bool bf16)
+{
+    return bf16 ? bf16_lo(((const uint16_t *)p)[off]) : ((const float *)p)[off];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store1(void *p, int64_t off, float x)
+{
+    if constexpr (BF16)
+        ((__bf16 *)p)[off] = static_cast<__bf16>(x);
+    else
+        ((float *)p)[off] = x;
+}
+
+// Eight results; bf16 values are rounded to nearest even here.
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int64_t off, const float (&x)[8])
+{
+    if constexpr (BF16) {
+        *(u32x4_any *)((uint16_t *)p + off) = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                      pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     } else {
-        static_assert(VEC == 1, "one element or eight");
-        if constexpr (BF16)
-            x[0] = bf16_lo(((const uint16_t *)p)[off]);
-        else
-            x[0] = ((const float *)p)[off];
+        *(f32x4_any *)((float *)p + off) = f32x4_t{x[0], x[1], x[2], x[3]};
+        *(f32x4_any *)((float *)p + off + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
     }
 }
 
-// The same for a store; bf16 values are rounded to nearest even here.
-template <bool BF16, int VEC>
-__device__ __forceinline__ void store(void *p, int64_t off, const float (&x)[VEC])
+// The first n of eight results.
+template <bool BF16>
+__device__ __forceinline__ void store_upto(void *p, int64_t off, const float (&x)[8], int n)
 {
-    if constexpr (VEC == 8) {
-        if constexpr (BF16) {
-            *(u32x4_t *)((uint16_t *)p + off) = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                        pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-        } else {
-            *(f32x4_t *)((float *)p + off) = f32x4_t{x[0], x[1], x[2], x[3]};
-            *(f32x4_t *)((float *)p + off + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
-        }
-    } else {
-        if constexpr (BF16)
-            ((__bf16 *)p)[off] = static_cast<__bf16>(x[0]);
-        else
-            ((float *)p)[off] = x[0];
-    }
+    if (n >= 8)
+        return store8<BF16>(p, off, x);
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n)
+            store1<BF16>(p, off + i, x[i]);
 }
 
 // rows, or min(max(*count, 0), rows) where a device-side count is given.

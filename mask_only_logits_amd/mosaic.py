@@ -122,7 +122,7 @@ def _load() -> ctypes.CDLL:
     lib.mosaic_distill_topk.restype = st
     lib.mosaic_distill_topk.argtypes = [p, i64, i64, i64, st, p, st, p, i64, f32, p, p, p, p, p, i64, p, i64, p]
     lib.mosaic_distill_topk_workspace_bytes.restype = i64
-    lib.mosaic_distill_topk_workspace_bytes.argtypes = [i64, i64]
+    lib.mosaic_distill_topk_workspace_bytes.argtypes = [i64, i64, i64]
     lib.mosaic_distill_topk_grad.restype = st
     lib.mosaic_distill_topk_grad.argtypes = [p, i64, i64, i64, st, p, st, p, i64, f32, p, p, p, p, i64, p]
     lib.mosaic_debug_reload_env.restype = None
@@ -687,11 +687,12 @@ def _teacher(M: int, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor):
             _dev(teacher_ids, "teacher_ids", torch.int32), teacher_logits.shape[1])
 
 
-def mosaic_distill_topk_workspace_bytes(M: int, V: int) -> int:
-    """Workspace bytes mosaic_distill_topk needs for M rows over V vocabulary entries."""
-    n = int(lib.mosaic_distill_topk_workspace_bytes(int(M), int(V)))
+def mosaic_distill_topk_workspace_bytes(M: int, V: int, K: int) -> int:
+    """Workspace bytes mosaic_distill_topk needs for M rows over V vocabulary entries and K
+    teacher logits."""
+    n = int(lib.mosaic_distill_topk_workspace_bytes(int(M), int(V), int(K)))
     if n < 0:
-        raise ValueError("negative size")
+        raise ValueError("a negative size, or K above 1024")
     return n
 
 
@@ -716,12 +717,12 @@ def mosaic_distill_topk(logits: torch.Tensor, teacher_logits: torch.Tensor, teac
         stats = torch.empty((M, 2), dtype=torch.float32, device=dev) if stats is None else stats
         if with_grad and grad is None:
             grad = torch.empty((M, V), dtype=logits.dtype, device=dev)
-        if workspace is None:
-            need = mosaic_distill_topk_workspace_bytes(M, V)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         z, ldz = _dev_rows(logits, "logits", M, V)
         g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
         top, top_type, ids, K = _teacher(M, teacher_logits, teacher_ids)
+        if workspace is None:
+            need = int(lib.mosaic_distill_topk_workspace_bytes(M, V, K))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
         _check(lib.mosaic_distill_topk(
             z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
             _vector(count, "count", 1, torch.int32), _vector(loss, "loss", M, torch.float32),

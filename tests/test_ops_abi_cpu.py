@@ -138,7 +138,7 @@ SHARED = [
     (dict(z=A16 + 1), INVALID), (dict(grad=B16 + 1), INVALID), (dict(t=A16 + 2), INVALID), (dict(ids=A16 + 2), INVALID),
     (dict(count=A16 + 2), INVALID), (dict(gl=A16 + 2), INVALID), (dict(stats=A16 + 4), INVALID),
     (dict(ldz=2**61, M=2**10), INVALID),
-    (dict(K=1025), UNSUPPORTED), (dict(M=2**31), UNSUPPORTED), (dict(V=2**31, ldz=2**31, ldg=2**31), UNSUPPORTED),
+    (dict(K=1025), UNSUPPORTED), (dict(M=2**31), UNSUPPORTED), (dict(V=2**30 + 1, ldz=2**31, ldg=2**31), UNSUPPORTED),
 ]
 
 
@@ -159,9 +159,11 @@ def test_distill_refusals_of_one(m):
 def test_distill_workspace(m):
     f = m.mosaic_distill_topk_workspace_bytes
     with pytest.raises(ValueError):
-        f(-1, 5)
-    for M, V in ((1, 152064), (20, 152064), (20, 126464), (4096, 126464), (3, 100)):
-        need = f(M, V)
+        f(-1, 5, 5)
+    with pytest.raises(ValueError):
+        f(5, 5, 1025)
+    for M, V in ((1, 152064), (20, 152064), (20, 126464), (700, 126464), (4096, 126464), (3, 100)):
+        need = f(M, V, 4)
         assert need >= 0
         if need:
             assert _distill(m, M=M, V=V, ldz=V, wb=need - 1) == INVALID
