@@ -307,6 +307,21 @@ __device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, in
     fix_entries<BF16, NT>(a, t, row, lo, hi, g, m, l);
 }
 
+// (m, s) of NW waves from the teacher's part array.
+template <int NW>
+__device__ __forceinline__ MaxSum join_parts(const Teacher &t, float c)
+{
+    MaxSum x;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        x.m = fmaxf(x.m, t.part[w]);
+    const float ref = ref_of(x.m);
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        x.s += t.part[16 + w] * fast_exp2((t.part[w] - ref) * c);
+    return x;
+}
+
 // Joins the waves' (m, s) of a workgroup: m and l of the row in every thread.  Its barrier also
 // publishes the teacher.
 template <int NT>
@@ -322,10 +337,7 @@ __device__ __forceinline__ void join_block(MaxSum x, const Teacher &t, float c, 
             t.part[16 + wave] = x.s;
         }
         __syncthreads();
-        x = MaxSum{t.part[0], t.part[16]};
-#pragma unroll
-        for (int w = 1; w < NT / 64; ++w)
-            x.join(t.part[w], t.part[16 + w], c);
+        x = join_parts<NT / 64>(t, c);
     }
     m = x.m;
     l = logf(x.s);
@@ -412,6 +424,119 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
             }
         }
         __syncthreads();   // the teacher's arrays are refilled for the next row
+    }
+}
+
+// Loss and gradient of long rows.  A workgroup of 16 waves has a CU to itself and walks its
+// rows: 15 waves hold the row in registers, R chunks of eight logits per thread (V <= 7680 R),
+// and wave 0 prepares the next row's teacher, writes the loss and mends the entries of the row
+// before.  As soon as a chunk's gradient is stored, its registers take the next row's logits,
+// so that reads and writes run side by side; the one barrier of a row publishes the waves'
+// sums and the teacher, and finds the stores of the row before complete, behind the loads
+// that it waits for anyway.
+template <bool BF16, int R>
+__global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, int slots, int teacher_words)
+{
+    extern __shared__ int32_t lds[];
+    constexpr int ND = 960;
+    const Teacher t0(lds, a.K, slots), t1(lds + teacher_words, a.K, slots);
+    const float c = kLog2e / a.temperature;
+    const int64_t n = row_count(a.count, a.rows);
+    const int V = a.V, full = V & ~7;
+    int64_t row = blockIdx.x;
+    if (row >= n)
+        return;
+    if (threadIdx.x < 64) {
+        load_teacher<BF16>(a, row, t0, nullptr, 0, V);
+        __syncthreads();
+        float pm = 0.0f, pl = 0.0f;
+        for (bool odd = false, first = true;; odd = !odd, first = false) {
+            const Teacher &t = odd ? t1 : t0, &other = odd ? t0 : t1;
+            const MaxSum x = join_parts<15>(t, c);
+            const float m = x.m, l = logf(x.s), loss = row_loss(a, t, m, l);
+            if (threadIdx.x == 0) {
+                a.loss[row] = t.flags[0] ? loss : 0.0f;
+                a.stats[2 * row] = m;
+                a.stats[2 * row + 1] = l;
+            }
+            if (!first)
+                fix_entries<BF16, 64>(a, other, row - gridDim.x, 0, V, upstream(a, row - gridDim.x), pm, pl);
+            pm = m;
+            pl = l;
+            const int64_t next = row + gridDim.x;
+            if (next < n)
+                load_teacher<BF16>(a, next, other, nullptr, 0, V);
+            __syncthreads();
+            if (next >= n) {
+                fix_entries<BF16, 64>(a, t, row, 0, V, upstream(a, row), m, l);
+                return;
+            }
+            row = next;
+        }
+    }
+    const int d = threadIdx.x - 64;
+    const bool has_rest = full < V && d == ND - 1;
+    Raw8<BF16> r[R], rest;   // whole chunks, and the last, shorter one
+    rest.fill(-kInf);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        r[i].fill(-kInf);
+        if ((i * ND + d) * 8 < full)
+            r[i].load(a.Z, row * a.ldz + (i * ND + d) * 8);
+    }
+    if (has_rest)
+        rest.load_part(a.Z, row * a.ldz + full, V - full);
+    for (bool odd = false;; odd = !odd) {
+        const Teacher &t = odd ? t1 : t0;
+        float mx[2] = {-kInf, -kInf};
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            max8(r[i], mx);
+        if (full < V)
+            max8(rest, mx);
+        const float wm = wave_reduce(fmaxf(mx[0], mx[1]), MaxOp{}), ref = ref_of(wm);
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            sum8(r[i], ref, c, s);
+        if (full < V)
+            sum8(rest, ref, c, s);
+        const float ws = wave_reduce(s[0] + s[1], AddOp{});
+        if ((threadIdx.x & 63) == 0) {
+            t.part[(threadIdx.x >> 6) - 1] = wm;
+            t.part[15 + (threadIdx.x >> 6)] = ws;
+        }
+        __syncthreads();
+        const MaxSum x = join_parts<15>(t, c);
+        const float m = x.m, l2 = logf(x.s) * kLog2e, g = upstream(a, row);
+        const bool present = t.flags[0];
+        const int64_t next = row + gridDim.x;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int v = (i * ND + d) * 8;
+            if (v < full) {
+                float z[8];
+                r[i].opaque();
+                r[i].get(z);
+                grad8(z, g, m, c, l2, present);
+                store8<BF16>(a.grad, row * a.ldg + v, z);
+                if (next < n)
+                    r[i].load(a.Z, next * a.ldz + v);
+            }
+        }
+        if (has_rest) {
+            float z[8];
+            rest.get(z);
+            grad8(z, g, m, c, l2, present);
+            store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
+            if (next < n)
+                rest.load_part(a.Z, next * a.ldz + full, V - full);
+        }
+        if (next >= n) {
+            __syncthreads();   // the last row's stores, before its entries are mended
+            return;
+        }
+        row = next;
     }
 }
 
@@ -534,19 +659,29 @@ hipError_t run(const Distill &a, hipStream_t stream)
     auto go = [&](auto kernel, int threads) {
         hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, stream, a, slots);
     };
-    constexpr int W = BF16 ? 1 : 2;   // fp32 rows take twice the registers
+    auto stream_rows = [&](auto kernel) {
+        int dev = 0, cus = 256;
+        if (hipGetDevice(&dev) == hipSuccess)
+            (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, cus)), dim3(1024), 2 * lds, stream, a,
+                           slots, (int)(lds / 4));
+    };
     if (a.V <= 64 * 8 * 4)
         go(distill_row_kernel<BF16, 64, 4>, 64);
     else if (a.V <= 256 * 8 * 8)
         go(distill_row_kernel<BF16, 256, 8>, 256);
     else if (!a.grad)
         go(distill_row_kernel<BF16, 256, 0>, 256);
-    else if (a.V <= 1024 * 8 * 8)
-        go(distill_row_kernel<BF16, 1024, 8>, 1024);
-    else if (a.V <= 1024 * 8 * 16 / W)
-        go(distill_row_kernel<BF16, 1024, 16 / W>, 1024);
-    else if (a.V <= 1024 * 8 * 20 / W)
-        go(distill_row_kernel<BF16, 1024, 20 / W>, 1024);
+    else if (a.V <= 7680 * 5)
+        stream_rows(distill_stream_kernel<BF16, 5>);
+    else if (a.V <= 7680 * 9)
+        stream_rows(distill_stream_kernel<BF16, 9>);
+    else if (BF16 && a.V <= 7680 * 13)
+        stream_rows(distill_stream_kernel<BF16, BF16 ? 13 : 9>);
+    else if (BF16 && a.V <= 7680 * 17)
+        stream_rows(distill_stream_kernel<BF16, BF16 ? 17 : 9>);
+    else if (BF16 && a.V <= 7680 * 20)
+        stream_rows(distill_stream_kernel<BF16, BF16 ? 20 : 9>);
     else
         go(distill_row_kernel<BF16, 1024, 0>, 1024);
     return hipGetLastError();
