@@ -40,31 +40,48 @@ constexpr float kInf = __builtin_inff();
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// -inf stands for nothing seen yet, and (-inf) - (-inf) would be NaN
-__device__ __forceinline__ float ref_of(float m) { return m == -kInf ? 0.0f : m; }
+// Exponents of a set of logits against its maximum m: (z - m) / T in powers of two is taken as
+// z * c - k with one rounding, k = m * c rounded, and what k lost, m * c - k, is known
+// exactly (`off`) and put right once per sum: a third fewer operations than subtracting
+// first.  Where |m| c reaches 2^60 (logits of the type's lowest value) every other logit is
+// further away than exp can tell from nothing, so c is replaced by a power of two with which
+// m * c is exact and no product overflows.  An empty set (m = -inf) takes k = 0.
+struct Ref {
+    float c, k, off;
 
-// Running maximum and sum of exp((z - max) / T) of a set of logits; c = log2(e) / T.
+    __device__ __forceinline__ Ref(float m, float c0)
+    {
+        c = c0;
+        k = m * c0;
+        off = __builtin_fmaf(m, c0, -k);
+        if (!(fabsf(k) < 0x1p60f)) {
+            const int e = (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255u);
+            if (m == -kInf) {
+                k = off = 0.0f;
+            } else if (e < 255) {
+                c = __builtin_bit_cast(float, (uint32_t)(294 - e) << 23);   // m * c in [2^40, 2^41)
+                k = m * c;
+                off = 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ float exp(float z) const { return fast_exp2(__builtin_fmaf(z, c, -k)); }
+};
+
+// Factor that takes a sum of exp((z - from) / T) to one of exp((z - to) / T).
+__device__ __forceinline__ float rescale(float from, float to, float c)
+{
+    return from == -kInf ? 0.0f : fast_exp2((from - to) * c);
+}
+
+// Maximum and sum of exp((z - max) / T) of a set of logits; c = log2(e) / T.
 struct MaxSum {
     float m = -kInf, s = 0.0f;
 
-    __device__ __forceinline__ void add(const float (&z)[8], float c)
-    {
-        float mx = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
-        if (mx > m) {
-            s *= fast_exp2((m - mx) * c);
-            m = mx;
-        }
-        const float r = ref_of(m);
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            e[i] = fast_exp2((z[i] - r) * c);
-        s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-    }
     __device__ __forceinline__ void join(float m2, float s2, float c)
     {
-        const float mx = fmaxf(m, m2), r = ref_of(mx);
-        s = s * fast_exp2((m - r) * c) + s2 * fast_exp2((m2 - r) * c);
+        const float mx = fmaxf(m, m2);
+        s = s * rescale(m, mx, c) + s2 * rescale(m2, mx, c);
         m = mx;
     }
     __device__ __forceinline__ void join_wave(float c)
@@ -72,6 +89,60 @@ struct MaxSum {
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1)
             join(__shfl_xor(m, o, 64), __shfl_xor(s, o, 64), c);
+    }
+};
+
+__device__ __forceinline__ float max_of(const float (&z)[8])
+{
+    return fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+}
+
+__device__ __forceinline__ float sum_of(const float (&z)[8], const Ref &ref)
+{
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        e[i] = ref.exp(z[i]);
+    return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+}
+
+// The same over a stream of logits.
+struct RunningMaxSum {
+    float m = -kInf, s = 0.0f, c0;
+    Ref ref;
+
+    __device__ __forceinline__ RunningMaxSum(float c) : c0(c), ref(-kInf, c) {}
+    __device__ __forceinline__ void add(const float (&z)[8])
+    {
+        const float mx = max_of(z);
+        if (mx > m) {
+            s = s * fast_exp2(-ref.off) * rescale(m, mx, c0);
+            m = mx;
+            ref = Ref(m, c0);
+            s *= fast_exp2(ref.off);
+        }
+        s += sum_of(z, ref);
+    }
+    __device__ __forceinline__ MaxSum done() const { return MaxSum{m, s * fast_exp2(-ref.off)}; }
+};
+
+// What turns a row's logits into gradients: g q_v = scale * exp2(z_v * c - k), with g = T times
+// the upstream gradient.
+struct RowGrad {
+    Ref ref;
+    float scale, g;
+
+    // s = exp(l) = sum_v exp((z_v - m) / T)
+    __device__ __forceinline__ RowGrad(const Distill &a, int64_t row, const MaxSum &x)
+        : ref(x.m, kLog2e / a.temperature), g(a.temperature * (a.grad_loss ? a.grad_loss[row] : 1.0f))
+    {
+        scale = g * fast_exp2(-ref.off) / x.s;
+    }
+    __device__ __forceinline__ void apply(float (&z)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = scale * ref.exp(z[i]);
     }
 };
 
@@ -185,13 +256,22 @@ __device__ __forceinline__ float row_loss(const Distill &a, const Teacher &t, fl
     return T * T * (*t.entropy - wave_reduce(x, AddOp{}));
 }
 
-// Writes the gradient at the teacher's entries with lo <= c_j < hi again, with p taken off; the
-// bulk has been written before the last barrier.  g: T times the row's upstream gradient.
+// The gradient of a row without teacher entries.
 template <bool BF16, int NT>
-__device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, int64_t row, int lo, int hi, float g,
-                                            float m, float l)
+__device__ __forceinline__ void zero_grad(const Distill &a, int64_t row, int lo, int hi)
 {
-    const float c = kLog2e / a.temperature, l2 = l * kLog2e;
+    for (int v = lo + threadIdx.x * 8; v < hi; v += NT * 8) {
+        const float z[8] = {};
+        store_upto<BF16>(a.grad, row * a.ldg + v, z, hi - v);
+    }
+}
+
+// Writes the gradient at the teacher's entries with lo <= c_j < hi again, with p taken off; the
+// bulk has been written before the last barrier.
+template <bool BF16, int NT>
+__device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, int64_t row, int lo, int hi,
+                                            const RowGrad &f)
+{
     const bool repeated = t.flags[1];
     for (int j = threadIdx.x; j < a.K; j += NT) {
         const int32_t id = t.id[j];
@@ -210,53 +290,46 @@ __device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, 
             if (!first)
                 continue;
         }
-        store1<BF16>(a.grad, row * a.ldg + id, g * (fast_exp2((t.z[j] - m) * c - l2) - p));
+        store1<BF16>(a.grad, row * a.ldg + id, f.scale * f.ref.exp(t.z[j]) - f.g * p);
     }
 }
 
-// eight logits to eight gradients T g q_v (0 in a row without teacher entries)
-__device__ __forceinline__ void grad8(float (&z)[8], float g, float m, float c, float l2, bool present = true)
+// Maximum and sum over chunks held in registers.  The fences keep the compiler from unpacking
+// many chunks at once, for which there are no registers.
+template <bool BF16, int R>
+__device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], float mx)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        z[i] = present ? g * fast_exp2((z[i] - m) * c - l2) : 0.0f;
-}
-
-// running maxima and sums over chunks held in registers
-template <bool BF16>
-__device__ __forceinline__ void max8(Raw8<BF16> &r, float (&mx)[2])
-{
-    float z[8];
-    r.opaque();
-    r.get(z);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        mx[0] = fmaxf(mx[0], z[2 * e]);
-        mx[1] = fmaxf(mx[1], z[2 * e + 1]);
+    for (int i = 0; i < R; ++i) {
+        float z[8];
+        r[i].opaque();
+        r[i].get(z);
+        mx = fmaxf(mx, max_of(z));
+        if (i % 2)
+            __builtin_amdgcn_sched_barrier(0);
     }
+    return mx;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void sum8(Raw8<BF16> &r, float ref, float c, float (&s)[2])
+template <bool BF16, int R>
+__device__ __forceinline__ float held_sum(Raw8<BF16> (&r)[R], const Ref &ref)
 {
-    float z[8];
-    r.opaque();
-    r.get(z);
+    float s = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        s[0] += fast_exp2((z[2 * e] - ref) * c);
-        s[1] += fast_exp2((z[2 * e + 1] - ref) * c);
+    for (int i = 0; i < R; ++i) {
+        float z[8];
+        r[i].opaque();
+        r[i].get(z);
+        s += sum_of(z, ref);
+        if (i % 2)
+            __builtin_amdgcn_sched_barrier(0);
     }
-}
-
-__device__ __forceinline__ float upstream(const Distill &a, int64_t row)
-{
-    return a.temperature * (a.grad_loss ? a.grad_loss[row] : 1.0f);
+    return s;
 }
 
 // Chunks of eight logits of [lo, hi), lo a multiple of eight: chunk i of this thread's is
 // lo / 8 + threadIdx.x + i * NT.  UN loads are issued before their values are used.
-template <bool BF16, int NT, typename F>
+template <bool BF16, int NT, bool STREAM, typename F>
 __device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo, int hi, F f)
 {
     constexpr int UN = BF16 ? 4 : 2;
@@ -267,7 +340,7 @@ __device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo
 #pragma unroll
         for (int i = 0; i < UN; ++i)
             if (v + i * NT * 8 < full)
-                r[i].load(a.Z, base + v + i * NT * 8);
+                r[i].template load<STREAM>(a.Z, base + v + i * NT * 8);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             if (v + i * NT * 8 < full) {
@@ -288,23 +361,20 @@ __device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo
 }
 
 // Gradient bulk of the part [lo, hi) of a row, then the teacher's entries in it.
-template <bool BF16, int NT>
-__device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, int64_t row, int lo, int hi, float m,
-                                          float l)
+template <bool BF16, int NT, bool STREAM>
+__device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, int64_t row, int lo, int hi,
+                                          const MaxSum &x)
 {
-    const float c = kLog2e / a.temperature, l2 = l * kLog2e, g = upstream(a, row);
+    const RowGrad f(a, row, x);
     if (t.flags[0])
-        for_chunks<BF16, NT>(a, row, lo, hi, [&](float (&z)[8], int v, int n) {
-            grad8(z, g, m, c, l2);
-            store_upto<BF16>(a.grad, row * a.ldg + v, z, n);
+        for_chunks<BF16, NT, STREAM>(a, row, lo, hi, [&](float (&z)[8], int v, int n) {
+            f.apply(z);
+            store_upto<BF16, STREAM>(a.grad, row * a.ldg + v, z, n);
         });
     else
-        for (int v = lo + threadIdx.x * 8; v < hi; v += NT * 8) {
-            const float z[8] = {};
-            store_upto<BF16>(a.grad, row * a.ldg + v, z, hi - v);
-        }
+        zero_grad<BF16, NT>(a, row, lo, hi);
     __syncthreads();   // orders the two writes of an entry
-    fix_entries<BF16, NT>(a, t, row, lo, hi, g, m, l);
+    fix_entries<BF16, NT>(a, t, row, lo, hi, f);
 }
 
 // (m, s) of NW waves from the teacher's part array.
@@ -315,32 +385,27 @@ __device__ __forceinline__ MaxSum join_parts(const Teacher &t, float c)
 #pragma unroll
     for (int w = 0; w < NW; ++w)
         x.m = fmaxf(x.m, t.part[w]);
-    const float ref = ref_of(x.m);
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-        x.s += t.part[16 + w] * fast_exp2((t.part[w] - ref) * c);
+        x.s += t.part[16 + w] * rescale(t.part[w], x.m, c);
     return x;
 }
 
-// Joins the waves' (m, s) of a workgroup: m and l of the row in every thread.  Its barrier also
+// Joins the (m, s) of a workgroup's waves, the result in every thread.  Its barrier also
 // publishes the teacher.
 template <int NT>
-__device__ __forceinline__ void join_block(MaxSum x, const Teacher &t, float c, float &m, float &l)
+__device__ __forceinline__ MaxSum join_block(const MaxSum &x, const Teacher &t, float c)
 {
-    x.join_wave(c);
     if constexpr (NT == 64) {
         __syncthreads();
-    } else {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-            t.part[wave] = x.m;
-            t.part[16 + wave] = x.s;
-        }
-        __syncthreads();
-        x = join_parts<NT / 64>(t, c);
+        return x;
     }
-    m = x.m;
-    l = logf(x.s);
+    if ((threadIdx.x & 63) == 0) {
+        t.part[threadIdx.x >> 6] = x.m;
+        t.part[16 + (threadIdx.x >> 6)] = x.s;
+    }
+    __syncthreads();
+    return join_parts<NT / 64>(t, c);
 }
 
 // One row per workgroup.  R > 0: the row stays in registers, R chunks of eight logits per
@@ -353,41 +418,41 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
     const float c = kLog2e / a.temperature;
     const int64_t n = row_count(a.count, a.rows);
     const int V = a.V, full = V & ~7;
+    uint32_t d8 = threadIdx.x * 8;   // a chunk's place: a uniform pointer and this offset
+    constexpr int64_t ES = BF16 ? 2 : 4;
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+        asm volatile("" : "+v"(d8));   // or the places of all chunks stay in registers between rows
         MaxSum x;
         Raw8<BF16> r[R > 0 ? R : 1], rest;   // whole chunks, and the last, shorter one
+        const bool has_rest = full < V && threadIdx.x == NT - 1;
         if (threadIdx.x < 64)
             load_teacher<BF16>(a, row, t, nullptr, 0, V);
         if constexpr (R > 0) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int v = (i * NT + threadIdx.x) * 8;
                 r[i].fill(-kInf);
-                if (v < full)
-                    r[i].load(a.Z, row * a.ldz + v);
+                if (i * NT * 8 + (int)d8 < full)
+                    r[i].load((const char *)a.Z + (row * a.ldz + i * NT * 8) * ES, d8);
             }
             rest.fill(-kInf);
-            if (full < V && threadIdx.x == NT - 1)
+            if (has_rest)
                 rest.load_part(a.Z, row * a.ldz + full, V - full);
-            float mx[2] = {-kInf, -kInf};
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                max8(r[i], mx);
-            max8(rest, mx);
-            x.m = fmaxf(mx[0], mx[1]);
-            const float ref = ref_of(x.m);
-            float s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                sum8(r[i], ref, c, s);
-            if (full < V)
-                sum8(rest, ref, c, s);
-            x.s = s[0] + s[1];
+            float z[8];
+            rest.get(z);
+            x.m = wave_reduce(held_max(r, has_rest ? max_of(z) : -kInf), MaxOp{});
+            const Ref ref(x.m, c);
+            x.s = wave_reduce(held_sum(r, ref) + (has_rest ? sum_of(z, ref) : 0.0f), AddOp{}) * fast_exp2(-ref.off);
         } else {
-            for_chunks<BF16, NT>(a, row, 0, V, [&](float (&z)[8], int, int) { x.add(z, c); });
+            RunningMaxSum run(c);
+            if (a.grad)   // it will be read again
+                for_chunks<BF16, NT, false>(a, row, 0, V, [&](float (&z)[8], int, int) { run.add(z); });
+            else
+                for_chunks<BF16, NT, true>(a, row, 0, V, [&](float (&z)[8], int, int) { run.add(z); });
+            x = run.done();
+            x.join_wave(c);
         }
-        float m, l;
-        join_block<NT>(x, t, c, m, l);
+        x = join_block<NT>(x, t, c);
+        const float m = x.m, l = logf(x.s);
         const bool present = t.flags[0];
         if (threadIdx.x < 64) {
             const float loss = row_loss(a, t, m, l);
@@ -399,28 +464,32 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
         }
         if (a.grad) {
             if constexpr (R > 0) {
-                const float l2 = l * kLog2e, g = upstream(a, row);
+                const RowGrad f(a, row, x);
+                if (!present) {
+                    zero_grad<BF16, NT>(a, row, 0, V);
+                } else {
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int v = (i * NT + threadIdx.x) * 8;
-                    if (v < full) {
+                    for (int i = 0; i < R; ++i) {
+                        if (i * NT * 8 + (int)d8 < full) {
+                            float z[8];
+                            r[i].opaque();
+                            r[i].get(z);
+                            f.apply(z);
+                            store8<BF16>((char *)a.grad + (row * a.ldg + i * NT * 8) * ES, d8, z);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (has_rest) {
                         float z[8];
-                        r[i].opaque();
-                        r[i].get(z);
-                        grad8(z, g, m, c, l2, present);
-                        store8<BF16>(a.grad, row * a.ldg + v, z);
+                        rest.get(z);
+                        f.apply(z);
+                        store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
                     }
                 }
-                if (full < V && threadIdx.x == NT - 1) {
-                    float z[8];
-                    rest.get(z);
-                    grad8(z, g, m, c, l2, present);
-                    store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
-                }
                 __syncthreads();   // orders the two writes of an entry
-                fix_entries<BF16, NT>(a, t, row, 0, V, g, m, l);
+                fix_entries<BF16, NT>(a, t, row, 0, V, f);
             } else {
-                part_grad<BF16, NT>(a, t, row, 0, V, m, l);
+                part_grad<BF16, NT, false>(a, t, row, 0, V, x);
             }
         }
         __syncthreads();   // the teacher's arrays are refilled for the next row
@@ -429,12 +498,13 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
 
 // Loss and gradient of long rows.  A workgroup of 16 waves has a CU to itself and walks its
 // rows: 15 waves hold the row in registers, R chunks of eight logits per thread (V <= 7680 R),
-// and wave 0 prepares the next row's teacher, writes the loss and mends the entries of the row
-// before.  As soon as a chunk's gradient is stored, its registers take the next row's logits,
-// so that reads and writes run side by side; the one barrier of a row publishes the waves'
-// sums and the teacher, and finds the stores of the row before complete, behind the loads
-// that it waits for anyway.
-template <bool BF16, int R>
+// and wave 0 takes the logits behind the last whole chunk, prepares the next row's teacher,
+// writes the loss and mends the entries of the row before.  As soon as a chunk's gradient is
+// stored, its registers take the next row's logits, so that reads and writes run side by side.
+// The one barrier of a row publishes the waves' sums and the teacher, and finds the stores of
+// the row before complete, behind the loads that it waits for anyway.
+// STREAM: streaming cache policy.
+template <bool BF16, int R, bool STREAM>
 __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, int slots, int teacher_words)
 {
     extern __shared__ int32_t lds[];
@@ -446,91 +516,91 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
     int64_t row = blockIdx.x;
     if (row >= n)
         return;
+    // (m, s) of a wave for the join
+    auto leave = [&](const Teacher &t, float m, float s) __attribute__((always_inline)) {
+        if ((threadIdx.x & 63) == 0) {
+            t.part[threadIdx.x >> 6] = m;
+            t.part[16 + (threadIdx.x >> 6)] = s;
+        }
+    };
     if (threadIdx.x < 64) {
-        load_teacher<BF16>(a, row, t0, nullptr, 0, V);
+        const int v = full + threadIdx.x;   // this lane's logit behind the last whole chunk
+        float z = -kInf;
+        auto prepare = [&](int64_t r, const Teacher &t) __attribute__((always_inline)) {
+            if (v < V)
+                z = load1(a.Z, r * a.ldz + v, BF16);
+            load_teacher<BF16>(a, r, t, nullptr, 0, V);
+            const float m = wave_reduce(z, MaxOp{});
+            const Ref ref(m, c);
+            leave(t, m, wave_reduce(ref.exp(z), AddOp{}) * fast_exp2(-ref.off));
+        };
+        prepare(row, t0);
         __syncthreads();
-        float pm = 0.0f, pl = 0.0f;
+        MaxSum before;
         for (bool odd = false, first = true;; odd = !odd, first = false) {
             const Teacher &t = odd ? t1 : t0, &other = odd ? t0 : t1;
-            const MaxSum x = join_parts<15>(t, c);
-            const float m = x.m, l = logf(x.s), loss = row_loss(a, t, m, l);
+            const MaxSum x = join_parts<16>(t, c);
+            const float l = logf(x.s), loss = row_loss(a, t, x.m, l);
             if (threadIdx.x == 0) {
                 a.loss[row] = t.flags[0] ? loss : 0.0f;
-                a.stats[2 * row] = m;
+                a.stats[2 * row] = x.m;
                 a.stats[2 * row + 1] = l;
             }
+            const RowGrad f(a, row, x);
+            if (v < V)
+                store1<BF16>(a.grad, row * a.ldg + v, t.flags[0] ? f.scale * f.ref.exp(z) : 0.0f);
             if (!first)
-                fix_entries<BF16, 64>(a, other, row - gridDim.x, 0, V, upstream(a, row - gridDim.x), pm, pl);
-            pm = m;
-            pl = l;
+                fix_entries<BF16, 64>(a, other, row - gridDim.x, 0, V, RowGrad(a, row - gridDim.x, before));
+            before = x;
             const int64_t next = row + gridDim.x;
             if (next < n)
-                load_teacher<BF16>(a, next, other, nullptr, 0, V);
+                prepare(next, other);
             __syncthreads();
             if (next >= n) {
-                fix_entries<BF16, 64>(a, t, row, 0, V, upstream(a, row), m, l);
+                fix_entries<BF16, 64>(a, t, row, 0, V, f);
                 return;
             }
             row = next;
         }
     }
-    const int d = threadIdx.x - 64;
-    const bool has_rest = full < V && d == ND - 1;
-    Raw8<BF16> r[R], rest;   // whole chunks, and the last, shorter one
-    rest.fill(-kInf);
+    // Chunk i's place: a uniform pointer and the lane's offset.  The offset is hidden from the
+    // compiler once per row, or it keeps the sums of all chunks in registers between rows.
+    uint32_t d8 = (threadIdx.x - 64) * 8;
+    Raw8<BF16> r[R];
+    constexpr int64_t ES = BF16 ? 2 : 4;
+    auto fetch = [&](int i, int64_t from) __attribute__((always_inline)) {
+        if (i * ND * 8 + (int)d8 < full)
+            r[i].template load<STREAM>((const char *)a.Z + (from * a.ldz + i * ND * 8) * ES, d8);
+    };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         r[i].fill(-kInf);
-        if ((i * ND + d) * 8 < full)
-            r[i].load(a.Z, row * a.ldz + (i * ND + d) * 8);
+        fetch(i, row);
     }
-    if (has_rest)
-        rest.load_part(a.Z, row * a.ldz + full, V - full);
     for (bool odd = false;; odd = !odd) {
         const Teacher &t = odd ? t1 : t0;
-        float mx[2] = {-kInf, -kInf};
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            max8(r[i], mx);
-        if (full < V)
-            max8(rest, mx);
-        const float wm = wave_reduce(fmaxf(mx[0], mx[1]), MaxOp{}), ref = ref_of(wm);
-        float s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            sum8(r[i], ref, c, s);
-        if (full < V)
-            sum8(rest, ref, c, s);
-        const float ws = wave_reduce(s[0] + s[1], AddOp{});
-        if ((threadIdx.x & 63) == 0) {
-            t.part[(threadIdx.x >> 6) - 1] = wm;
-            t.part[15 + (threadIdx.x >> 6)] = ws;
-        }
+        asm volatile("" : "+v"(d8));
+        const float m = wave_reduce(held_max(r, -kInf), MaxOp{});
+        const Ref ref(m, c);
+        leave(t, m, wave_reduce(held_sum(r, ref), AddOp{}) * fast_exp2(-ref.off));
         __syncthreads();
-        const MaxSum x = join_parts<15>(t, c);
-        const float m = x.m, l2 = logf(x.s) * kLog2e, g = upstream(a, row);
-        const bool present = t.flags[0];
+        const RowGrad f(a, row, join_parts<16>(t, c));
         const int64_t next = row + gridDim.x;
+        const bool present = t.flags[0];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int v = (i * ND + d) * 8;
-            if (v < full) {
-                float z[8];
-                r[i].opaque();
-                r[i].get(z);
-                grad8(z, g, m, c, l2, present);
-                store8<BF16>(a.grad, row * a.ldg + v, z);
+            if (i * ND * 8 + (int)d8 < full) {
+                float z[8] = {};
+                if (present) {
+                    r[i].opaque();
+                    r[i].get(z);
+                    f.apply(z);
+                }
+                store8<BF16, STREAM>((char *)a.grad + (row * a.ldg + i * ND * 8) * ES, d8, z);
                 if (next < n)
-                    r[i].load(a.Z, next * a.ldz + v);
+                    fetch(i, next);
             }
-        }
-        if (has_rest) {
-            float z[8];
-            rest.get(z);
-            grad8(z, g, m, c, l2, present);
-            store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
-            if (next < n)
-                rest.load_part(a.Z, next * a.ldz + full, V - full);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (next >= n) {
             __syncthreads();   // the last row's stores, before its entries are mended
@@ -549,12 +619,12 @@ __device__ __forceinline__ void part_range(int V, int parts, int s, int &lo, int
     lo = min(lo, hi);
 }
 
-constexpr int kSplitThreads = 256;
+constexpr int kPartThreads = 256;
 
 // (maximum, sum) of each part of each row into partials[row][part][2], and the student's
 // logits at the teacher's entries into z_at[row][K] (the gradient may overwrite them).
 template <bool BF16>
-__global__ __launch_bounds__(kSplitThreads) void distill_part_kernel(const Distill a, int parts,
+__global__ __launch_bounds__(kPartThreads) void distill_part_kernel(const Distill a, int parts,
                                                                      float *__restrict__ z_at)
 {
     __shared__ float red[8];
@@ -565,8 +635,9 @@ __global__ __launch_bounds__(kSplitThreads) void distill_part_kernel(const Disti
         return;
     int lo, hi;
     part_range(a.V, parts, s, lo, hi);
-    MaxSum x;
-    for_chunks<BF16, kSplitThreads>(a, row, lo, hi, [&](float (&z)[8], int, int) { x.add(z, c); });
+    RunningMaxSum run(c);
+    for_chunks<BF16, kPartThreads, false>(a, row, lo, hi, [&](float (&z)[8], int, int) { run.add(z); });
+    MaxSum x = run.done();
     x.join_wave(c);
     if ((threadIdx.x & 63) == 0) {
         red[threadIdx.x >> 6] = x.m;
@@ -580,7 +651,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_part_kernel(const Disti
         a.partials[2 * blockIdx.x + 1] = x.s;
     }
     if (s == parts - 1)
-        for (int j = threadIdx.x; j < a.K; j += kSplitThreads) {
+        for (int j = threadIdx.x; j < a.K; j += kPartThreads) {
             const int32_t id = a.ids[row * a.K + j];
             z_at[row * a.K + j] = id >= 0 && id < a.V ? load1(a.Z, row * a.ldz + id, BF16) : 0.0f;
         }
@@ -589,8 +660,8 @@ __global__ __launch_bounds__(kSplitThreads) void distill_part_kernel(const Disti
 // Gradient of part blockIdx.x % cuts of a row.  parts > 0: the statistics are joined from the
 // row's partials, and the workgroup of the first part writes them and the loss; parts = 0:
 // they are given.
-template <bool BF16>
-__global__ __launch_bounds__(kSplitThreads) void distill_split_kernel(const Distill a, int slots, int parts, int cuts,
+template <bool BF16, int NT, bool STREAM>
+__global__ __launch_bounds__(NT) void distill_split_kernel(const Distill a, int slots, int parts, int cuts,
                                                                       const float *__restrict__ z_at)
 {
     extern __shared__ int32_t lds[];
@@ -604,30 +675,26 @@ __global__ __launch_bounds__(kSplitThreads) void distill_split_kernel(const Dist
         part_range(a.V, cuts, s, lo, hi);
         if (threadIdx.x < 64)
             load_teacher<BF16>(a, row, t, z_at ? z_at + row * a.K : nullptr, z_at ? 0 : lo, z_at ? a.V : hi);
-        float m, l;
+        MaxSum x;
         if (parts > 0) {
-            MaxSum x;
             const int i = threadIdx.x & 63;   // parts <= 64
             if (i < parts)
                 x = MaxSum{a.partials[2 * (row * parts + i)], a.partials[2 * (row * parts + i) + 1]};
             x.join_wave(c);
-            m = x.m;
-            l = logf(x.s);
         } else {
-            m = a.stats[2 * row];
-            l = a.stats[2 * row + 1];
+            x = MaxSum{a.stats[2 * row], expf(a.stats[2 * row + 1])};
         }
         __syncthreads();   // the teacher is there
         if (parts > 0 && s == 0 && threadIdx.x < 64) {
-            const float loss = row_loss(a, t, m, l);
+            const float l = logf(x.s), loss = row_loss(a, t, x.m, l);
             if (threadIdx.x == 0) {
                 a.loss[row] = t.flags[0] ? loss : 0.0f;
-                a.stats[2 * row] = m;
+                a.stats[2 * row] = x.m;
                 a.stats[2 * row + 1] = l;
             }
         }
         if (a.grad)
-            part_grad<BF16, kSplitThreads>(a, t, row, lo, hi, m, l);
+            part_grad<BF16, NT, STREAM>(a, t, row, lo, hi, x);
         __syncthreads();   // the teacher's arrays are refilled for the next row
     }
 }
@@ -638,9 +705,31 @@ int parts_of(int64_t rows, int64_t V)
     return (int)std::max<int64_t>(1, std::min<int64_t>({64, 2048 / std::max<int64_t>(rows, 1), V / 4096}));
 }
 
-// Few rows of many logits go over several workgroups each.
+// Few rows of many logits go over several workgroups each.  20 x 152064 bf16, the loss: 11 us
+// in two launches against 20 us with a workgroup per row; 129 x 126464, loss and gradient: as
+// fast either way.
 bool is_split(int64_t rows, int64_t V, bool grad) { return rows <= (grad ? 128 : 1024) && V >= 16384; }
 
+// Logits that cannot stay in the 256 MB Infinity Cache are read and written with the streaming
+// cache policy: 4096 x 126464 bf16, loss and gradient: 435 against 463 us, the gradient alone
+// 410 against 468 us; but 512 x 126464: 54 against 46 us for the gradient.  The loss alone reads
+// each logit once and always takes it (4096 x 126464: 169 against 189 us, 512: 33 against 35).
+template <bool BF16>
+bool is_large(const Distill &a)
+{
+    return a.rows * a.V >= ((int64_t)256 << 20) / (BF16 ? 2 : 4);
+}
+
+// Which form a row takes, by its length (bf16; fp32 chunks take twice the registers):
+//  * up to 2048 logits: a wave per row.  Up to 8192: a wave per row where there are rows enough
+//    for several waves per SIMD, else four waves (8000 x 8000, loss and gradient: 56 against
+//    60 us; the loss alone 31 against 46 us).
+//  * up to 65536: 4 or 8 waves per row, several rows on a CU.  4000 x 20000: 88 us with 8 waves,
+//    105 us through the stream form, 2000 x 50000: 88 against 97 us.
+//  * longer: the stream form, a row at a time on each CU, up to what its registers hold, 153600
+//    logits (4096 x 126464: 419 us; without the reads of the next row beside the writes of
+//    this one 475 us).
+//  * longer still: the row is read twice.
 template <bool BF16>
 hipError_t run(const Distill &a, hipStream_t stream)
 {
@@ -649,51 +738,71 @@ hipError_t run(const Distill &a, hipStream_t stream)
     if (is_split(a.rows, a.V, a.grad)) {
         const int parts = parts_of(a.rows, a.V), cuts = a.grad ? parts : 1;
         float *z_at = a.partials + 2 * a.rows * parts;
-        hipLaunchKernelGGL(distill_part_kernel<BF16>, dim3((unsigned)(a.rows * parts)), dim3(kSplitThreads), 0,
-                           stream, a, parts, z_at);
-        hipLaunchKernelGGL(distill_split_kernel<BF16>, dim3((unsigned)(a.rows * cuts)), dim3(kSplitThreads), lds,
+        hipLaunchKernelGGL(distill_part_kernel<BF16>, dim3((unsigned)(a.rows * parts)), dim3(kPartThreads), 0, stream,
+                           a, parts, z_at);
+        hipLaunchKernelGGL((distill_split_kernel<BF16, 256, false>), dim3((unsigned)(a.rows * cuts)), dim3(256), lds,
                            stream, a, slots, parts, cuts, z_at);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20));
-    auto go = [&](auto kernel, int threads) {
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, stream, a, slots);
+    auto rows = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(threads), lds, stream, a,
+                           slots);
     };
-    auto stream_rows = [&](auto kernel) {
+    auto rows_per_cu = [&](auto kernel, auto kernel_large) {
         int dev = 0, cus = 256;
         if (hipGetDevice(&dev) == hipSuccess)
             (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, cus)), dim3(1024), 2 * lds, stream, a,
-                           slots, (int)(lds / 4));
+        const dim3 grid((unsigned)std::min<int64_t>(a.rows, cus));
+        if (is_large<BF16>(a))
+            hipLaunchKernelGGL(kernel_large, grid, dim3(1024), 2 * lds, stream, a, slots, (int)(lds / 4));
+        else
+            hipLaunchKernelGGL(kernel, grid, dim3(1024), 2 * lds, stream, a, slots, (int)(lds / 4));
     };
+    const bool many = a.rows >= 2048;
     if (a.V <= 64 * 8 * 4)
-        go(distill_row_kernel<BF16, 64, 4>, 64);
-    else if (a.V <= 256 * 8 * 8)
-        go(distill_row_kernel<BF16, 256, 8>, 256);
+        rows(distill_row_kernel<BF16, 64, 4>, 64);
+    else if (!a.grad && many && a.V <= 16384)
+        rows(distill_row_kernel<BF16, 64, 0>, 64);
     else if (!a.grad)
-        go(distill_row_kernel<BF16, 256, 0>, 256);
-    else if (a.V <= 7680 * 5)
-        stream_rows(distill_stream_kernel<BF16, 5>);
-    else if (a.V <= 7680 * 9)
-        stream_rows(distill_stream_kernel<BF16, 9>);
-    else if (BF16 && a.V <= 7680 * 13)
-        stream_rows(distill_stream_kernel<BF16, BF16 ? 13 : 9>);
+        rows(distill_row_kernel<BF16, 256, 0>, 256);
+    else if (BF16 && many && a.V <= 64 * 8 * 16)
+        rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 4>, 64);
+    else if (a.V <= 256 * 8 * 4)
+        rows(distill_row_kernel<BF16, 256, 4>, 256);
+    else if (a.V <= 256 * 8 * 8)
+        rows(distill_row_kernel<BF16, 256, 8>, 256);
+    else if (a.V <= 512 * 8 * 8)
+        rows(distill_row_kernel<BF16, 512, 8>, 512);
+    else if (BF16 && a.V <= 512 * 8 * 16)
+        rows(distill_row_kernel<BF16, 512, BF16 ? 16 : 8>, 512);
+    else if (a.V <= 7680 * (BF16 ? 13 : 9))
+        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 13 : 9, false>, distill_stream_kernel<BF16, BF16 ? 13 : 9, true>);
     else if (BF16 && a.V <= 7680 * 17)
-        stream_rows(distill_stream_kernel<BF16, BF16 ? 17 : 9>);
+        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 17 : 9, false>, distill_stream_kernel<BF16, BF16 ? 17 : 9, true>);
     else if (BF16 && a.V <= 7680 * 20)
-        stream_rows(distill_stream_kernel<BF16, BF16 ? 20 : 9>);
+        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 20 : 9, false>, distill_stream_kernel<BF16, BF16 ? 20 : 9, true>);
     else
-        go(distill_row_kernel<BF16, 1024, 0>, 1024);
+        rows(distill_row_kernel<BF16, 1024, 0>, 1024);
     return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t run_grad(const Distill &a, hipStream_t stream)
 {
-    const int cuts = parts_of(a.rows, a.V);
-    hipLaunchKernelGGL(distill_split_kernel<BF16>, dim3((unsigned)std::min<int64_t>(a.rows * cuts, 1 << 20)),
-                       dim3(kSplitThreads), teacher_bytes(a.K), stream, a, table_slots(a.K), 0, cuts,
-                       (const float *)nullptr);
+    // Parts of about 24576 logits: the workgroups under way then cover a compact stretch of
+    // memory (4096 x 126464 bf16: 374 us in 4 or 8 parts per row, 410 us in one, 423 us in 16,
+    // where the teacher is prepared too often).
+    const int cuts = std::max<int>(parts_of(a.rows, a.V), a.V / 24576);
+    auto go = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows * cuts, 1 << 20)), dim3(threads),
+                           teacher_bytes(a.K), stream, a, table_slots(a.K), 0, cuts, (const float *)nullptr);
+    };
+    if (a.V <= 4096 && a.rows >= 2048)   // a wave per row: enough rows, of few chunks each
+        go(distill_split_kernel<BF16, 64, false>, 64);
+    else if (is_large<BF16>(a))
+        go(distill_split_kernel<BF16, 256, true>, 256);
+    else
+        go(distill_split_kernel<BF16, 256, false>, 256);
     return hipGetLastError();
 }
 

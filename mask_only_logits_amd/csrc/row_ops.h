@@ -72,20 +72,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // Rows may start at any element, so the vector types are aligned to one: gfx950 takes the
 // same 16-byte loads and stores at any address, at full rate where it is aligned.
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
-typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
+template <bool NT>
+__device__ __forceinline__ u32x4_t get16(const u32x4_any *p)
+{
+    if constexpr (NT)
+        return __builtin_nontemporal_load(p);
+    else
+        return *p;
+}
+
+template <bool NT>
+__device__ __forceinline__ void put16(u32x4_any *p, const u32x4_t &w)
+{
+    if constexpr (NT)
+        __builtin_nontemporal_store(w, p);
+    else
+        *p = w;
+}
 
 // Eight elements as they are stored: 16 bytes (bf16) or 32 (fp32).
 template <bool BF16>
 struct Raw8 {
     u32x4_t w[BF16 ? 1 : 2];
 
+    // NT: with the streaming cache policy, for data that is read once
+    template <bool NT = false>
     __device__ __forceinline__ void load(const void *p, int64_t off)
     {
         if constexpr (BF16) {
-            w[0] = *(const u32x4_any *)((const uint16_t *)p + off);
+            w[0] = get16<NT>((const u32x4_any *)((const uint16_t *)p + off));
         } else {
-            w[0] = __builtin_bit_cast(u32x4_t, (f32x4_t) * (const f32x4_any *)((const float *)p + off));
-            w[1] = __builtin_bit_cast(u32x4_t, (f32x4_t) * (const f32x4_any *)((const float *)p + off + 4));
+            w[0] = get16<NT>((const u32x4_any *)((const float *)p + off));
+            w[1] = get16<NT>((const u32x4_any *)((const float *)p + off + 4));
         }
     }
     __device__ __forceinline__ void get(float (&x)[8]) const
@@ -149,25 +168,29 @@ __device__ __forceinline__ void store1(void *p, int64_t off, float x)
         ((float *)p)[off] = x;
 }
 
-// Eight results; bf16 values are rounded to nearest even here.
-template <bool BF16>
+// Eight results; bf16 values are rounded to nearest even here.  NT: streaming cache policy.
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ void store8(void *p, int64_t off, const float (&x)[8])
 {
     if constexpr (BF16) {
-        *(u32x4_any *)((uint16_t *)p + off) = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                      pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+        put16<NT>((u32x4_any *)((uint16_t *)p + off), u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
     } else {
-        *(f32x4_any *)((float *)p + off) = f32x4_t{x[0], x[1], x[2], x[3]};
-        *(f32x4_any *)((float *)p + off + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
+        u32x4_t w[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, x[i]);
+        put16<NT>((u32x4_any *)((float *)p + off), w[0]);
+        put16<NT>((u32x4_any *)((float *)p + off + 4), w[1]);
     }
 }
 
 // The first n of eight results.
-template <bool BF16>
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ void store_upto(void *p, int64_t off, const float (&x)[8], int n)
 {
     if (n >= 8)
-        return store8<BF16>(p, off, x);
+        return store8<BF16, NT>(p, off, x);
 #pragma unroll
     for (int i = 0; i < 7; ++i)
         if (i < n)
