@@ -167,44 +167,51 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _dev_rows(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype: torch.dtype | None = None):
-    """(pointer, row stride in elements) of a [>= rows, cols] device tensor whose rows are contiguous."""
+def _dev_rows(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype: torch.dtype):
+    """(pointer, row stride in elements) of a [>= rows, cols] tensor whose rows are contiguous."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(shape)}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr() if t.numel() else None, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    return t.data_ptr() or None, ld if shape[0] > 1 else max(ld, cols)
 
 
 def _vector(t: torch.Tensor | None, name: str, n: int, dtype: torch.dtype):
-    """Pointer of a contiguous device tensor with at least n elements."""
-    ptr = _dev(t, name, dtype)
-    if t is not None and t.numel() < n:
+    """Pointer of a contiguous tensor with at least n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
         raise ValueError(f"{name} has fewer than {n} entries")
-    return ptr
+    return t.data_ptr() or None
 
 
 _HERE = contextlib.nullcontext()
+# the handle of a device's current stream, without making a Stream object of it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _on(stream, like: torch.Tensor, *others):
     """Context in which a call allocates and launches: the tensors' device (one for all of
     them) and the stream the kernels go to, so that what the call allocates belongs to it."""
-    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+    device = like.get_device() if isinstance(like, torch.Tensor) else -1
+    if device < 0:
         raise ValueError("the tensors must be device tensors")
     for t in others:
-        if t is not None and t.device != like.device:
-            raise ValueError(f"tensors on {like.device} and {t.device}")
+        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != device):
+            raise ValueError(f"tensors on {like.device} and {getattr(t, 'device', type(t).__name__)}")
     if stream is None:
-        return _HERE if like.device.index == torch.cuda.current_device() else torch.cuda.device(like.device)
+        return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
     if stream.device != like.device:
@@ -578,22 +585,24 @@ def mosaic_add_rmsnorm(X: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, r
         raise ValueError(f"unknown code {code}")
     if code is None and (q is not None or scale is not None):
         raise ValueError("q and scale need a code")
+    dtype = X.dtype
     with _on(stream, X, gain, residual, row_idx, count, sum_out, out, q, scale):
+        device = X.get_device()
         if store_sum and sum_out is None:
-            sum_out = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+            sum_out = X.new_empty((rows, d))
         if store_out and out is None:
-            out = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+            out = X.new_empty((rows, d))
         if code is not None:
-            q = torch.empty((rows, d), dtype=q_type, device=X.device) if q is None else q
-            scale = torch.empty(rows, dtype=torch.float32, device=X.device) if scale is None else scale
-        x, ldx = _dev_rows(X, "X", n, d)
-        r, ldr = _dev_rows(residual, "residual", n, d, X.dtype)
-        s, lds = _dev_rows(sum_out, "sum_out", rows, d, X.dtype)
+            q = X.new_empty((rows, d), dtype=q_type) if q is None else q
+            scale = X.new_empty(rows, dtype=torch.float32) if scale is None else scale
+        x, ldx = _dev_rows(X, "X", n, d, dtype)
+        r, ldr = _dev_rows(residual, "residual", n, d, dtype)
+        s, lds = _dev_rows(sum_out, "sum_out", rows, d, dtype)
         _check(lib.mosaic_add_rmsnorm(
-            x, ldx, r, ldr, n, d, _dtype_code(X.dtype), _dev(gain, "gain"), _dtype_code(gain.dtype), eps,
-            _vector(row_idx, "row_idx", rows, torch.int32), _vector(count, "count", 1, torch.int32), rows, s, lds,
-            _vector(out, "out", rows * d, X.dtype), code or 0, _vector(q, "q", rows * d, q_type),
-            _vector(scale, "scale", rows, torch.float32), _stream(None)), "mosaic_add_rmsnorm")
+            x, ldx, r, ldr, n, d, _dtype_code(dtype), _vector(gain, "gain", d, gain.dtype), _dtype_code(gain.dtype),
+            eps, _vector(row_idx, "row_idx", rows, torch.int32), _vector(count, "count", 1, torch.int32), rows, s, lds,
+            _vector(out, "out", rows * d, dtype), code or 0, _vector(q, "q", rows * d, q_type),
+            _vector(scale, "scale", rows, torch.float32), _raw_stream(device)), "mosaic_add_rmsnorm")
     return sum_out, out, q, scale
 
 
@@ -607,11 +616,12 @@ def mosaic_quantize_rows_int8(X: torch.Tensor, row_idx: torch.Tensor | None = No
     if rows is None:
         rows = n if row_idx is None else row_idx.numel()
     with _on(stream, X, row_idx, q, scale):
-        q = torch.empty((rows, d), dtype=torch.int8, device=X.device) if q is None else q
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device) if scale is None else scale
+        device = X.get_device()
+        q = X.new_empty((rows, d), dtype=torch.int8) if q is None else q
+        scale = X.new_empty(rows, dtype=torch.float32) if scale is None else scale
         _check(lib.mosaic_quantize_rows_int8(
-            _dev(X, "X"), n, d, _dtype_code(X.dtype), _vector(row_idx, "row_idx", rows, torch.int32), rows,
-            _vector(q, "q", rows * d, torch.int8), _vector(scale, "scale", rows, torch.float32), _stream(None)),
+            _vector(X, "X", 0, X.dtype), n, d, _dtype_code(X.dtype), _vector(row_idx, "row_idx", rows, torch.int32), rows,
+            _vector(q, "q", rows * d, torch.int8), _vector(scale, "scale", rows, torch.float32), _raw_stream(device)),
             "mosaic_quantize_rows_int8")
     return q, scale
 
@@ -634,13 +644,14 @@ def mosaic_quantized_logits(Hq: torch.Tensor, h_scale: torch.Tensor, Wq: torch.T
     if M > Hq.shape[0]:
         raise ValueError("M exceeds the rows of Hq")
     with _on(stream, Hq, h_scale, Wq, w_scale, count, out):
+        device = Hq.get_device()
         if out is None:
-            out = torch.empty((M, V), dtype=out_dtype or torch.bfloat16, device=Hq.device)
+            out = Hq.new_empty((M, V), dtype=out_dtype or torch.bfloat16)
         _check(lib.mosaic_quantized_logits(
-            code, _dev(Hq, "Hq"), _vector(h_scale, "h_scale", M, torch.float32), M,
-            _vector(count, "count", 1, torch.int32), _dev(Wq, "Wq", Hq.dtype),
+            code, _vector(Hq, "Hq", 0, Hq.dtype), _vector(h_scale, "h_scale", M, torch.float32), M,
+            _vector(count, "count", 1, torch.int32), _vector(Wq, "Wq", 0, Hq.dtype),
             _vector(w_scale, "w_scale", V, torch.float32), V, d, _vector(out, "out", M * V, out.dtype),
-            _dtype_code(out.dtype), _stream(None)), "mosaic_quantized_logits")
+            _dtype_code(out.dtype), _raw_stream(device)), "mosaic_quantized_logits")
     return out
 
 
@@ -666,25 +677,27 @@ def mosaic_masked_logits_int8(H: torch.Tensor, idx: torch.Tensor, Wq: torch.Tens
     if M > idx.numel():
         raise ValueError("M exceeds the length of idx")
     with _on(stream, H, idx, Wq, w_scale, out, workspace):
+        device = H.get_device()
         if out is None:
-            out = torch.empty((M, V), dtype=out_dtype or torch.bfloat16, device=H.device)
+            out = H.new_empty((M, V), dtype=out_dtype or torch.bfloat16)
         if workspace is None:
-            workspace = torch.empty(max(16, mosaic_logits_int8_workspace_bytes(M, chunk_rows, d)),
-                                    dtype=torch.uint8, device=H.device)
+            workspace = H.new_empty(max(16, mosaic_logits_int8_workspace_bytes(M, chunk_rows, d)), dtype=torch.uint8)
         _check(lib.mosaic_masked_logits_int8(
-            _dev(H, "H"), L, d, _dtype_code(H.dtype), _dev(idx, "idx", torch.int32), M, _dev(Wq, "Wq", torch.int8),
-            _vector(w_scale, "w_scale", V, torch.float32), V, _vector(out, "out", M * V, out.dtype),
-            int(chunk_rows), _dtype_code(out.dtype), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-            _stream(None)), "mosaic_masked_logits_int8")
+            _vector(H, "H", 0, H.dtype), L, d, _dtype_code(H.dtype), _vector(idx, "idx", M, torch.int32), M,
+            _vector(Wq, "Wq", 0, torch.int8), _vector(w_scale, "w_scale", V, torch.float32), V,
+            _vector(out, "out", M * V, out.dtype), int(chunk_rows), _dtype_code(out.dtype),
+            _vector(workspace, "workspace", 0, torch.uint8), workspace.numel(),
+            _raw_stream(device)), "mosaic_masked_logits_int8")
     return out
 
 
 def _teacher(M: int, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor):
     """(pointer, dtype code, ids pointer, K) of a teacher's top logits [M, K]."""
-    if teacher_logits.dim() != 2 or teacher_logits.shape != teacher_ids.shape or teacher_logits.shape[0] < M:
+    shape = teacher_logits.shape
+    if len(shape) != 2 or shape != teacher_ids.shape or shape[0] < M:
         raise ValueError("teacher_logits and teacher_ids must be [M, K]")
-    return (_dev(teacher_logits, "teacher_logits"), _dtype_code(teacher_logits.dtype),
-            _dev(teacher_ids, "teacher_ids", torch.int32), teacher_logits.shape[1])
+    return (_vector(teacher_logits, "teacher_logits", 0, teacher_logits.dtype), _dtype_code(teacher_logits.dtype),
+            _vector(teacher_ids, "teacher_ids", 0, torch.int32), shape[1])
 
 
 def mosaic_distill_topk_workspace_bytes(M: int, V: int, K: int) -> int:
@@ -712,23 +725,23 @@ def mosaic_distill_topk(logits: torch.Tensor, teacher_logits: torch.Tensor, teac
         raise ValueError("logits must be [M, V]")
     M, V = logits.shape
     with _on(stream, logits, teacher_logits, teacher_ids, count, loss, stats, grad_loss, grad, workspace):
-        dev = logits.device
-        loss = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
-        stats = torch.empty((M, 2), dtype=torch.float32, device=dev) if stats is None else stats
+        device = logits.get_device()
+        loss = logits.new_empty(M, dtype=torch.float32) if loss is None else loss
+        stats = logits.new_empty((M, 2), dtype=torch.float32) if stats is None else stats
         if with_grad and grad is None:
-            grad = torch.empty((M, V), dtype=logits.dtype, device=dev)
-        z, ldz = _dev_rows(logits, "logits", M, V)
+            grad = logits.new_empty((M, V))
+        z, ldz = _dev_rows(logits, "logits", M, V, logits.dtype)
         g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
         top, top_type, ids, K = _teacher(M, teacher_logits, teacher_ids)
         if workspace is None:
             need = int(lib.mosaic_distill_topk_workspace_bytes(M, V, K))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+            workspace = logits.new_empty(need, dtype=torch.uint8) if need > 0 else None
         _check(lib.mosaic_distill_topk(
             z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
             _vector(count, "count", 1, torch.int32), _vector(loss, "loss", M, torch.float32),
             _vector(stats, "stats", 2 * M, torch.float32), _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg,
-            _dev(workspace, "workspace", torch.uint8), 0 if workspace is None else workspace.numel(),
-            _stream(None)), "mosaic_distill_topk")
+            _vector(workspace, "workspace", 0, torch.uint8), 0 if workspace is None else workspace.numel(),
+            _raw_stream(device)), "mosaic_distill_topk")
     return loss, stats, grad
 
 
@@ -743,13 +756,14 @@ def mosaic_distill_topk_grad(logits: torch.Tensor, teacher_logits: torch.Tensor,
         raise ValueError("logits must be [M, V]")
     M, V = logits.shape
     with _on(stream, logits, teacher_logits, teacher_ids, stats, grad_loss, count, grad):
+        device = logits.get_device()
         if grad is None:
-            grad = torch.empty((M, V), dtype=logits.dtype, device=logits.device)
-        z, ldz = _dev_rows(logits, "logits", M, V)
+            grad = logits.new_empty((M, V))
+        z, ldz = _dev_rows(logits, "logits", M, V, logits.dtype)
         g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
         top, top_type, ids, K = _teacher(M, teacher_logits, teacher_ids)
         _check(lib.mosaic_distill_topk_grad(
             z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
             _vector(count, "count", 1, torch.int32), _vector(stats, "stats", 2 * M, torch.float32),
-            _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg, _stream(None)), "mosaic_distill_topk_grad")
+            _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg, _raw_stream(device)), "mosaic_distill_topk_grad")
     return grad
