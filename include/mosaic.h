@@ -345,7 +345,8 @@ mosaic_status_t mosaic_masked_logits_fp8(const void *H, int64_t L, int64_t d, co
  * Any d >= 1 and element-aligned pointers; multiples of 8 elements at 16-byte aligned rows
  * take the vector form.  rows == 0: OK, nothing enqueued.  Row strides below d, a NULL
  * required pointer, misalignment, sum aliasing an input with row_idx or another stride, or
- * rows > nsrc without row_idx: INVALID_ARG.  nsrc or d of 2^31 and more: UNSUPPORTED. */
+ * rows > nsrc without row_idx: INVALID_ARG.  nsrc or rows of 2^31 and more, d of more than
+ * 2^30: UNSUPPORTED. */
 mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, int64_t ldr, int64_t nsrc, int64_t d,
                                    mosaic_dtype_t in_dtype, const void *gain, mosaic_dtype_t gain_dtype, float eps,
                                    const int32_t *row_idx, const int32_t *count, int64_t rows, void *sum,
@@ -356,7 +357,7 @@ mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, in
  * scale = amax / 127, q_k = RNE(x_k * (127 / amax)), each fp32 operation rounded to nearest
  * even.  Used once for the weight W (one scale per vocabulary entry, the product's channel).
  * Arguments as there (row_idx values outside [0, nsrc) give rows of zero codes and scale
- * NaN), without alignment or size requirements on d: any d >= 1, X aligned to its elements.
+ * NaN), without its requirements on d and alignment: 1 <= d <= 2^30, X aligned to its elements.
  * rows == 0 or d == 0: OK, nothing enqueued. */
 mosaic_status_t mosaic_quantize_rows_int8(const void *X, int64_t nsrc, int64_t d, mosaic_dtype_t in_dtype,
                                           const int32_t *row_idx, int64_t rows, int8_t *q, float *scale,

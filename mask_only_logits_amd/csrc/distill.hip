@@ -43,9 +43,10 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 // Exponents of a set of logits against its maximum m: (z - m) / T in powers of two is taken as
 // z * c - k with one rounding, k = m * c rounded, and what k lost, m * c - k, is known
 // exactly (`off`) and put right once per sum: a third fewer operations than subtracting
-// first.  Where |m| c reaches 2^60 (logits of the type's lowest value) every other logit is
-// further away than exp can tell from nothing, so c is replaced by a power of two with which
-// m * c is exact and no product overflows.  An empty set (m = -inf) takes k = 0.
+// first.  Where |m| c reaches 2^30 (logits of the type's lowest value, say) what k loses could
+// pass exp's range, but then the next lower fp32 number is 64 powers of two away from m: every
+// logit counts as m or as nothing, so c is replaced by a power of two with which m * c is exact
+// and no product overflows.  An empty set (m = -inf) takes k = 0.
 struct Ref {
     float c, k, off;
 
@@ -54,7 +55,7 @@ struct Ref {
         c = c0;
         k = m * c0;
         off = __builtin_fmaf(m, c0, -k);
-        if (!(fabsf(k) < 0x1p60f)) {
+        if (!(fabsf(k) < 0x1p30f)) {
             const int e = (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255u);
             if (m == -kInf) {
                 k = off = 0.0f;
@@ -189,8 +190,9 @@ __device__ __forceinline__ void load_teacher(const Distill &a, int64_t row, cons
 {
     const int lane = threadIdx.x & 63;
     const float c = kLog2e / a.temperature;
-    for (int i = lane; i < t.slots; i += 64)
-        t.table[i] = -1;
+    if (a.grad)   // only the gradient asks for repeated entries
+        for (int i = lane; i < t.slots; i += 64)
+            t.table[i] = -1;
     float mx = -kInf;
     bool any = false;
     for (int j = lane; j < a.K; j += 64) {
@@ -198,8 +200,10 @@ __device__ __forceinline__ void load_teacher(const Distill &a, int64_t row, cons
         const float x = load1(a.top, row * a.K + j, a.top_bf16);
         const bool here = id >= 0 && id < a.V && x != -kInf;
         float z = 0.0f;
-        if (here && id >= lo && id < hi)
-            z = z_at ? z_at[j] : load1(a.Z, row * a.ldz + id, BF16);
+        if (z_at)
+            z = z_at[j];
+        else if (here && id >= lo && id < hi)
+            z = load1(a.Z, row * a.ldz + id, BF16);
         t.id[j] = here ? id : -1;
         t.p[j] = x;
         t.z[j] = z;
@@ -224,7 +228,7 @@ __device__ __forceinline__ void load_teacher(const Distill &a, int64_t row, cons
         t.p[j] = p;
         h += p != 0.0f ? p * logf(p) : 0.0f;
         const int32_t id = t.id[j];
-        if (id < 0)
+        if (id < 0 || !a.grad)
             continue;
         // at most K of >= 2 K slots are taken, so a free one is found
         int s = (int)(((uint32_t)id * 2654435761u) >> 16) & (t.slots - 1);

@@ -105,7 +105,8 @@ struct RowsNorm {
     uint8_t *q = nullptr;               // [rows, d] or null
     float *scale = nullptr;             // [rows] where q is given
 };
-// rows >= 1, d >= 1; norm off: q and scale of X's rows themselves.
+// 1 <= d <= kNormMaxWidth, rows >= 1; norm off: q and scale of X's rows themselves.
+constexpr int64_t kNormMaxWidth = (int64_t)1 << 30;
 hipError_t launch_rows_norm(const RowsNorm &a, bool in_bf16, bool norm, hipStream_t stream);
 
 // INT8 product (gemm_int8.hip): out[i, v] = (sum_k Hq[i, k] Wq[v, k]) * hs[i] * ws[v] for

@@ -59,7 +59,7 @@ mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, in
         return MOSAIC_ERR_INVALID_ARG;
     if (out && (out == X || out == R || out == sum))
         return MOSAIC_ERR_INVALID_ARG;
-    if (nsrc > kMaxPos || d > kMaxPos || rows > kMaxPos)
+    if (nsrc > kMaxPos || d > mosaic::kNormMaxWidth || rows > kMaxPos)
         return MOSAIC_ERR_UNSUPPORTED;
     mosaic::RowsNorm a;
     a.X = X;
@@ -115,7 +115,7 @@ mosaic_status_t mosaic_quantize_rows_int8(const void *X, int64_t nsrc, int64_t d
         return MOSAIC_ERR_INVALID_ARG;
     if (checked_bytes(nsrc, d, es) < 0 || checked_bytes(rows, d, 1) < 0)
         return MOSAIC_ERR_INVALID_ARG;
-    if (nsrc > kMaxPos || d > kMaxPos || rows > kMaxPos)
+    if (nsrc > kMaxPos || d > mosaic::kNormMaxWidth || rows > kMaxPos)
         return MOSAIC_ERR_UNSUPPORTED;
     return status_of(quantize_int8(X, nsrc, d, in_dtype, row_idx, rows, q, scale, (hipStream_t)stream));
 }

@@ -76,27 +76,36 @@ __device__ __forceinline__ void store_codes(uint8_t *q, const u32x2_t &w, int n)
             q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
 }
 
-// The elements k .. k + 7 of a row that lie before d, zeros behind them.
-template <bool BF16>
-__device__ __forceinline__ void load_upto(const void *p, int64_t off, int k, int d, float (&x)[8])
+// A thread's CH chunks of a row of d elements, chunk c from element c * STEP + t8 on, zeros
+// behind the row's end.  The whole chunks' loads go first, without a branch between them.
+template <bool BF16, int CH, int STEP, bool STREAM = false>
+__device__ __forceinline__ void load_row(const void *p, int64_t off, int t8, int d, Raw8<BF16> (&r)[CH])
 {
-    Raw8<BF16> r;
-    if (k + 8 <= d) {
-        r.load(p, off + k);
-    } else {
-        r.fill(0.0f);
-        if (k < d)
-            r.load_part(p, off + k, d - k);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        r[c].fill(0.0f);
+        if (c * STEP + t8 + 8 <= d)
+            r[c].template load<STREAM>(p, off + c * STEP + t8);
     }
-    r.get(x);
+    if (d & 7) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = c * STEP + t8;
+            if (k < d && k + 8 > d)
+                r[c].load_part(p, off + k, d - k);
+        }
+    }
 }
 
 // Power of two that keeps top / amax inside fp32 for the smallest rows (1 for all others).
 __device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
 
 // One row per WPR waves, a thread holding CH chunks of eight elements (d <= 512 WPR CH).
-// NORM off: y = x (plain quantization).
-template <bool BF16, bool NORM, int WPR, int CH>
+// NORM off: y = x (plain quantization).  STREAM: streaming cache policy.
+// Bound: HBM.  32768 x 4096 bf16 with residual, sum, out and codes moves 1.21 GB in 187 us, 6.4
+// TB/s (a large copy runs at 4.75); 1229 gathered rows to codes alone take 8.5 us, where the
+// chain of row id, row, two reductions and store counts.
+template <bool BF16, bool GAIN_BF16, bool NORM, int WPR, int CH, bool STREAM>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(const RowsNorm a)
 {
     constexpr int RPB = WPR == 1 ? 4 : 1;   // rows per workgroup
@@ -109,22 +118,26 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
         const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
         const bool inside = src >= 0 && src < a.nsrc;   // a row id outside gives a row of NaN
         float v[CH][8];
+        Raw8<BF16> x[CH], r[CH];
+        Raw8<GAIN_BF16> gain[CH];   // taken with the row, not after its reduction
+        if (inside) {
+            load_row<BF16, CH, STEP, STREAM>(a.X, src * a.ldx, t * 8, a.d, x);
+            if (NORM && a.R)
+                load_row<BF16, CH, STEP, STREAM>(a.R, src * a.ldr, t * 8, a.d, r);
+        }
+        if (NORM)
+            load_row<GAIN_BF16, CH, STEP>(a.gain, 0, t * 8, a.d, gain);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = c * STEP + t * 8;
-            if (inside) {
-                load_upto<BF16>(a.X, src * a.ldx, k, a.d, v[c]);
-                if (NORM && a.R) {
-                    float r[8];
-                    load_upto<BF16>(a.R, src * a.ldr, k, a.d, r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[c][i] += r[i];
-                }
-            } else {
+            if (!inside)
+                x[c].fill(__builtin_nanf(""));
+            x[c].get(v[c]);
+            if (NORM && a.R && inside) {
+                float y[8];
+                r[c].get(y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[c][i] = __builtin_nanf("");
+                    v[c][i] += y[i];
             }
         }
         if constexpr (NORM) {
@@ -133,7 +146,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
                 for (int c = 0; c < CH; ++c) {
                     const int k = c * STEP + t * 8;
                     if (k < a.d)
-                        store_upto<BF16>(a.sum, row * a.ldsum + k, v[c], a.d - k);
+                        store_upto<BF16, STREAM>(a.sum, row * a.ldsum + k, v[c], a.d - k);
                 }
             }
             float ss = 0.0f;
@@ -162,15 +175,12 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
                 const int k = c * STEP + t * 8;
                 if (k < a.d) {
                     float g[8];
-                    if (a.gain_bf16)
-                        load_upto<true>(a.gain, 0, k, a.d, g);
-                    else
-                        load_upto<false>(a.gain, 0, k, a.d, g);
+                    gain[c].get(g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         v[c][i] = v[c][i] * rstd * g[i];
                     if (a.out)
-                        store_upto<BF16>(a.out, row * a.d + k, v[c], a.d - k);
+                        store_upto<BF16, STREAM>(a.out, row * a.d + k, v[c], a.d - k);
                 }
             }
             if (!a.q)
@@ -274,13 +284,35 @@ unsigned grid_of(int64_t rows, int per_block)
     return (unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 1 << 20);
 }
 
+// Rows that pass the 256 MB Infinity Cache by far are read and written with the streaming cache
+// policy: bf16, d = 4096, residual, sum, out and codes, 32768 rows (1.2 GB): 187 against 211 us,
+// 16384 rows: 93 against 106 us; 8192 rows (0.3 GB) run alike, and what reads their results
+// next finds them in the cache.  An fp32 chunk is written in two halves of 16 bytes, which that
+// policy would send out as half-filled lines (16384 x 4096: 245 against 190 us).
+bool is_large(const RowsNorm &a)
+{
+    const int64_t streams = 1 + (a.R != nullptr) + (a.sum != nullptr) + (a.out != nullptr);
+    return streams * a.rows * a.d * 2 >= (int64_t)512 << 20;
+}
+
 template <bool BF16, bool NORM, int WPR, int CH>
 void run(const RowsNorm &a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((rows_norm_kernel<BF16, NORM, WPR, CH>), dim3(grid_of(a.rows, WPR == 1 ? 4 : 1)),
-                       dim3(WPR == 1 ? 256 : 64 * WPR), 0, stream, a);
+    const dim3 grid(grid_of(a.rows, WPR == 1 ? 4 : 1)), block(WPR == 1 ? 256 : 64 * WPR);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (NORM && BF16 && is_large(a))
+        a.gain_bf16 ? go(rows_norm_kernel<BF16, true, NORM, WPR, CH, NORM && BF16>)
+                    : go(rows_norm_kernel<BF16, false, NORM, WPR, CH, NORM && BF16>);
+    else
+        a.gain_bf16 || !NORM ? go(rows_norm_kernel<BF16, true, NORM, WPR, CH, false>)
+                             : go(rows_norm_kernel<BF16, !NORM, NORM, WPR, CH, false>);
 }
 
+// Waves per row and chunks per thread, by the row's length: enough waves for short rows to
+// finish soon, few enough that several rows share a CU and one's reductions lie under the
+// others' reads (bf16, residual, sum, out and codes: 16384 x 8192: 182 us with 8 waves, 285 us
+// with 16; 32768 x 4096: 187 us with 4, 238 us with 8; 65536 x 2048, no codes: 169 us with 2 or
+// 4, 173 us with 1).
 template <bool BF16, bool NORM>
 void pick(const RowsNorm &a, hipStream_t stream)
 {
@@ -289,13 +321,13 @@ void pick(const RowsNorm &a, hipStream_t stream)
     if (a.d <= 1024)
         return run<BF16, NORM, 1, 2>(a, stream);
     if (a.d <= 2048)
-        return run<BF16, NORM, 4, 1>(a, stream);
+        return run<BF16, NORM, 2, 2>(a, stream);
     if (a.d <= 4096)
         return run<BF16, NORM, 4, 2>(a, stream);
     if (a.d <= 8192)
-        return run<BF16, NORM, 16, 1>(a, stream);
+        return run<BF16, NORM, 8, 2>(a, stream);
     if (a.d <= 16384)
-        return run<BF16, NORM, 16, 2>(a, stream);
+        return run<BF16, NORM, 8, 4>(a, stream);
     hipLaunchKernelGGL((rows_norm_long_kernel<BF16, NORM>), dim3(grid_of(a.rows, 1)), dim3(1024), 0, stream, a);
 }
 

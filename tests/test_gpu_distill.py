@@ -126,6 +126,19 @@ def test_distill_masked_logits(m, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [300, 9000, 40000, 120000])
+def test_distill_large_magnitudes(m, V, dtype):
+    # logits around +-1e3 .. 1e38: only those next to the maximum count, whatever its size
+    z, t, ids, w = _data(V, 10, V, 6, F32)
+    for row, base in enumerate((1e3, -1e5, 3e7, -1e9, 7e9, -1e12, 1e18, -1e25, 3e38, -3e38)):
+        z[row] = torch.nextafter(torch.full((V,), base, device=DEV), torch.tensor(-3.4e38, device=DEV)) \
+            if dtype == F32 else base * 1.01
+        z[row, ::3] = base
+        z[row, 1::3] = base - 1 - abs(base) * 2.0 ** -6   # well below
+    _check(m, z.to(dtype), t, ids, 0.5, w, "large")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,V", [(3, 70000), (40, 1000), (600, 1001), (300, 9000)])
 def test_distill_strides_and_in_place(m, M, V, dtype):
     z, t, ids, w = _data(M, M, V + 29, 5, dtype)

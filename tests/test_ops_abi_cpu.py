@@ -42,7 +42,7 @@ def _norm(m, X=A16, ldx=64, R=B16, ldr=64, nsrc=100, d=64, i=BF16, gain=A16, g=B
     (dict(out=A16), INVALID), (dict(out=B16), INVALID), (dict(sum=C16), INVALID),
     (dict(nsrc=BIG, ldx=BIG), INVALID), (dict(ldx=2**62, nsrc=2**10), INVALID),
     (dict(nsrc=2**31), UNSUPPORTED), (dict(rows=2**31), UNSUPPORTED),
-    (dict(d=2**31, ldx=2**31, ldr=2**31), UNSUPPORTED),
+    (dict(d=2**30 + 1, ldx=2**31, ldr=2**31), UNSUPPORTED),
 ])
 def test_norm_refusals(m, kw, status):
     assert _norm(m, **kw) == status
@@ -61,7 +61,7 @@ def _quant(m, X=A16, nsrc=100, d=64, i=BF16, idx=A16, rows=10, q=A16, sc=A16):
     (dict(X=None), INVALID), (dict(q=None), INVALID), (dict(sc=None), INVALID), (dict(nsrc=0), INVALID),
     (dict(idx=None, rows=101), INVALID), (dict(X=A16 + 1), INVALID), (dict(sc=A16 + 2), INVALID),
     (dict(idx=A16 + 1), INVALID), (dict(nsrc=BIG, d=8), INVALID),
-    (dict(nsrc=2**31), UNSUPPORTED), (dict(rows=2**31), UNSUPPORTED), (dict(d=2**31), UNSUPPORTED),
+    (dict(nsrc=2**31), UNSUPPORTED), (dict(rows=2**31), UNSUPPORTED), (dict(d=2**30 + 1), UNSUPPORTED),
 ])
 def test_quantize_int8_refusals(m, kw, status):
     assert _quant(m, **kw) == status
