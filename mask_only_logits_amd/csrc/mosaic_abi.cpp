@@ -593,7 +593,7 @@ static int64_t fp8_chunk_bytes(int64_t rows, int64_t d)
     if (codes > INT64_MAX - 15)
         return -1;
     const int64_t aligned = ceil_div(codes, 16) * 16;
-    if (aligned > INT64_MAX - 4 * rows)
+    if (rows > (INT64_MAX - aligned) / 4)
         return -1;
     return aligned + 4 * rows;
 }
