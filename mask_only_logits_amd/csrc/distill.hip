@@ -23,6 +23,7 @@
 // The gradient's bulk T g q_v is written first, without regard to the teacher; then the few
 // entries that the teacher names are written again with their p taken off.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -790,13 +791,35 @@ hipError_t run(const Distill &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Parts of a row for the gradient alone: 12288 to 32768 logits each, so that the workgroups under
+// way cover a compact stretch of memory (4096 x 126464 bf16: 367 us in 4 parts per row, 410 us
+// in one, 423 us in 16, where the teacher is prepared too often).  Of these numbers of parts
+// the one that best fills the last round of workgroups, 8 on a CU, and the last turn of their
+// loops, 4 chunks per thread (1229 rows: 109 us in 8 parts, 117 us in 4, 121 us in 5).
+int cuts_of(int64_t rows, int64_t V)
+{
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess)
+        (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    const double slots = 8.0 * cus, chunks = (double)V / (8 * 256);
+    int best = 1;
+    double most = 0.0;
+    const int64_t lo = std::max<int64_t>(1, (V + 32767) / 32768), hi = std::min<int64_t>(std::max(lo, V / 12288), lo + 63);
+    for (int64_t n = lo; n <= hi; ++n) {
+        const double groups = (double)rows * n / slots, turns = chunks / n / 4.0;
+        const double full = groups / ceil(groups) * (turns / ceil(turns)) - 0.005 * n;
+        if (full > most) {
+            most = full;
+            best = (int)n;
+        }
+    }
+    return std::max((int)lo, best);
+}
+
 template <bool BF16>
 hipError_t run_grad(const Distill &a, hipStream_t stream)
 {
-    // Parts of about 24576 logits: the workgroups under way then cover a compact stretch of
-    // memory (4096 x 126464 bf16: 374 us in 4 or 8 parts per row, 410 us in one, 423 us in 16,
-    // where the teacher is prepared too often).
-    const int cuts = std::max<int>(parts_of(a.rows, a.V), a.V / 24576);
+    const int cuts = std::max(parts_of(a.rows, a.V), cuts_of(a.rows, a.V));
     auto go = [&](auto kernel, int threads) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows * cuts, 1 << 20)), dim3(threads),
                            teacher_bytes(a.K), stream, a, table_slots(a.K), 0, cuts, (const float *)nullptr);

@@ -657,6 +657,8 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 //    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 147 us with the 256 x 256 form; 64 rows:
 //    107 against 146 us.  Vocabulary tiles of 128 entries, or of 64 where that gives less than
 //    one workgroup per CU.
+//  * up to 128 rows whose 64 x 128 tiles fit on the chip at once, two on a CU, take those:
+//    100 x 30000 x 4096: 26 us, 45 us with 256 x 256 tiles, of which half the CUs get none.
 //  * more rows: 256 x 256 tiles where there are enough to fill a good part of the chip, else
 //    64 x 64.  300 x 30000 x 2048 (236 tiles): 32 against 45 us; 1000 x 10000 x 1024 (160):
 //    21 against 30 us; 1024 x 4096 x 4096 (64): 40 against 34 us; 200 x 8192 x 4096 (32): 44
@@ -683,6 +685,8 @@ hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *co
             return go(gemm_int8_small_kernel<32, 64, 1, 4, true, B>, tiles(32, 64), 256);
         if (rows <= 64 && tiles(64, 128) >= cus)
             return go(gemm_int8_small_kernel<64, 128, 1, 3, true, B>, tiles(64, 128), 256);
+        if (rows > 64 && rows <= 128 && tiles(64, 128) >= cus && tiles(64, 128) <= 2 * cus)
+            return go(gemm_int8_small_kernel<64, 128, 1, 3, false, B>, tiles(64, 128), 256);
         if (tiles(256, 256) * 16 < cus * 5)
             return go(gemm_int8_small_kernel<64, 64, 2, 4, false, B>, tiles(64, 64), 256);
         // one persistent workgroup per CU, a multiple of the eight XCDs
