@@ -299,17 +299,20 @@ __device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, 
     }
 }
 
-// Maximum and sum over chunks held in registers.  The fences keep the compiler from unpacking
-// many chunks at once, for which there are no registers.
+// Maximum and sum over chunks held in registers, the first `live` of R (the others lie behind
+// the row's end for every thread).  The fences keep the compiler from unpacking many chunks at
+// once, for which there are no registers.
 template <bool BF16, int R>
-__device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], float mx)
+__device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], int live, float mx)
 {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float z[8];
-        r[i].opaque();
-        r[i].get(z);
-        mx = fmaxf(mx, max_of(z));
+        if (i < live) {
+            float z[8];
+            r[i].opaque();
+            r[i].get(z);
+            mx = fmaxf(mx, max_of(z));
+        }
         if (i % 2)
             __builtin_amdgcn_sched_barrier(0);
     }
@@ -317,15 +320,17 @@ __device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], float mx)
 }
 
 template <bool BF16, int R>
-__device__ __forceinline__ float held_sum(Raw8<BF16> (&r)[R], const Ref &ref)
+__device__ __forceinline__ float held_sum(Raw8<BF16> (&r)[R], int live, const Ref &ref)
 {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float z[8];
-        r[i].opaque();
-        r[i].get(z);
-        s += sum_of(z, ref);
+        if (i < live) {
+            float z[8];
+            r[i].opaque();
+            r[i].get(z);
+            s += sum_of(z, ref);
+        }
         if (i % 2)
             __builtin_amdgcn_sched_barrier(0);
     }
@@ -423,6 +428,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
     const float c = kLog2e / a.temperature;
     const int64_t n = row_count(a.count, a.rows);
     const int V = a.V, full = V & ~7;
+    const int live = (full + NT * 8 - 1) / (NT * 8);
     uint32_t d8 = threadIdx.x * 8;   // a chunk's place: a uniform pointer and this offset
     constexpr int64_t ES = BF16 ? 2 : 4;
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
@@ -444,9 +450,9 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
                 rest.load_part(a.Z, row * a.ldz + full, V - full);
             float z[8];
             rest.get(z);
-            x.m = wave_reduce(held_max(r, has_rest ? max_of(z) : -kInf), MaxOp{});
+            x.m = wave_reduce(held_max(r, live, has_rest ? max_of(z) : -kInf), MaxOp{});
             const Ref ref(x.m, c);
-            x.s = wave_reduce(held_sum(r, ref) + (has_rest ? sum_of(z, ref) : 0.0f), AddOp{}) * fast_exp2(-ref.off);
+            x.s = wave_reduce(held_sum(r, live, ref) + (has_rest ? sum_of(z, ref) : 0.0f), AddOp{}) * fast_exp2(-ref.off);
         } else {
             RunningMaxSum run(c);
             if (a.grad)   // it will be read again
@@ -570,6 +576,7 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
     }
     // Chunk i's place: a uniform pointer and the lane's offset.  The offset is hidden from the
     // compiler once per row, or it keeps the sums of all chunks in registers between rows.
+    const int live = (full + ND * 8 - 1) / (ND * 8);
     uint32_t d8 = (threadIdx.x - 64) * 8;
     Raw8<BF16> r[R];
     constexpr int64_t ES = BF16 ? 2 : 4;
@@ -585,9 +592,9 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
     for (bool odd = false;; odd = !odd) {
         const Teacher &t = odd ? t1 : t0;
         asm volatile("" : "+v"(d8));
-        const float m = wave_reduce(held_max(r, -kInf), MaxOp{});
+        const float m = wave_reduce(held_max(r, live, -kInf), MaxOp{});
         const Ref ref(m, c);
-        leave(t, m, wave_reduce(held_sum(r, ref), AddOp{}) * fast_exp2(-ref.off));
+        leave(t, m, wave_reduce(held_sum(r, live, ref), AddOp{}) * fast_exp2(-ref.off));
         __syncthreads();
         const RowGrad f(a, row, join_parts<16>(t, c));
         const int64_t next = row + gridDim.x;
@@ -729,8 +736,8 @@ bool is_large(const Distill &a)
 //  * up to 2048 logits: a wave per row.  Up to 8192: a wave per row where there are rows enough
 //    for several waves per SIMD, else four waves (8000 x 8000, loss and gradient: 56 against
 //    60 us; the loss alone 31 against 46 us).
-//  * up to 65536: 4 or 8 waves per row, several rows on a CU.  4000 x 20000: 88 us with 8 waves,
-//    105 us through the stream form, 2000 x 50000: 88 against 97 us.
+//  * up to 65536: 4 or 8 waves per row, several rows on a CU.  4000 x 20000: 72 us with 4 waves,
+//    88 us with 8, 105 us through the stream form; 2000 x 50000: 90 us with 8, 97 us there.
 //  * longer: the stream form, a row at a time on each CU, up to what its registers hold, 153600
 //    logits (4096 x 126464: 419 us; without the reads of the next row beside the writes of
 //    this one 475 us).
@@ -776,8 +783,10 @@ hipError_t run(const Distill &a, hipStream_t stream)
         rows(distill_row_kernel<BF16, 256, 4>, 256);
     else if (a.V <= 256 * 8 * 8)
         rows(distill_row_kernel<BF16, 256, 8>, 256);
-    else if (a.V <= 512 * 8 * 8)
-        rows(distill_row_kernel<BF16, 512, 8>, 512);
+    else if (BF16 && a.V <= 256 * 8 * 16)
+        rows(distill_row_kernel<BF16, 256, BF16 ? 16 : 8>, 256);
+    else if (!BF16 && a.V <= 512 * 8 * 8)
+        rows(distill_row_kernel<BF16, BF16 ? 256 : 512, 8>, 512);
     else if (BF16 && a.V <= 512 * 8 * 16)
         rows(distill_row_kernel<BF16, 512, BF16 ? 16 : 8>, 512);
     else if (a.V <= 7680 * (BF16 ? 13 : 9))
