@@ -94,18 +94,26 @@ struct MaxSum {
     }
 };
 
-__device__ __forceinline__ float max_of(const float (&z)[8])
+template <int N>
+__device__ __forceinline__ float max_of(const float (&z)[N])
 {
-    return fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+    float a = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    if constexpr (N == 8)
+        a = fmaxf(a, fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+    return a;
 }
 
-__device__ __forceinline__ float sum_of(const float (&z)[8], const Ref &ref)
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&z)[N], const Ref &ref)
 {
-    float e[8];
+    float e[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
         e[i] = ref.exp(z[i]);
-    return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    float a = (e[0] + e[1]) + (e[2] + e[3]);
+    if constexpr (N == 8)
+        a += (e[4] + e[5]) + (e[6] + e[7]);
+    return a;
 }
 
 // The same over a stream of logits.
@@ -114,7 +122,8 @@ struct RunningMaxSum {
     Ref ref;
 
     __device__ __forceinline__ RunningMaxSum(float c) : c0(c), ref(-kInf, c) {}
-    __device__ __forceinline__ void add(const float (&z)[8])
+    template <int N>
+    __device__ __forceinline__ void add(const float (&z)[N])
     {
         const float mx = max_of(z);
         if (mx > m) {
@@ -140,10 +149,11 @@ struct RowGrad {
     {
         scale = g * fast_exp2(-ref.off) / x.s;
     }
-    __device__ __forceinline__ void apply(float (&z)[8]) const
+    template <int N>
+    __device__ __forceinline__ void apply(float (&z)[N]) const
     {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             z[i] = scale * ref.exp(z[i]);
     }
 };
@@ -265,8 +275,9 @@ __device__ __forceinline__ float row_loss(const Distill &a, const Teacher &t, fl
 template <bool BF16, int NT>
 __device__ __forceinline__ void zero_grad(const Distill &a, int64_t row, int lo, int hi)
 {
-    for (int v = lo + threadIdx.x * 8; v < hi; v += NT * 8) {
-        const float z[8] = {};
+    constexpr int N = kChunk<BF16>;
+    for (int v = lo + threadIdx.x * N; v < hi; v += NT * N) {
+        const float z[N] = {};
         store_upto<BF16>(a.grad, row * a.ldg + v, z, hi - v);
     }
 }
@@ -303,12 +314,12 @@ __device__ __forceinline__ void fix_entries(const Distill &a, const Teacher &t, 
 // the row's end for every thread).  The fences keep the compiler from unpacking many chunks at
 // once, for which there are no registers.
 template <bool BF16, int R>
-__device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], int live, float mx)
+__device__ __forceinline__ float held_max(Raw<BF16> (&r)[R], int live, float mx)
 {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         if (i < live) {
-            float z[8];
+            float z[kChunk<BF16>];
             r[i].opaque();
             r[i].get(z);
             mx = fmaxf(mx, max_of(z));
@@ -320,13 +331,13 @@ __device__ __forceinline__ float held_max(Raw8<BF16> (&r)[R], int live, float mx
 }
 
 template <bool BF16, int R>
-__device__ __forceinline__ float held_sum(Raw8<BF16> (&r)[R], int live, const Ref &ref)
+__device__ __forceinline__ float held_sum(Raw<BF16> (&r)[R], int live, const Ref &ref)
 {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         if (i < live) {
-            float z[8];
+            float z[kChunk<BF16>];
             r[i].opaque();
             r[i].get(z);
             s += sum_of(z, ref);
@@ -337,34 +348,34 @@ __device__ __forceinline__ float held_sum(Raw8<BF16> (&r)[R], int live, const Re
     return s;
 }
 
-// Chunks of eight logits of [lo, hi), lo a multiple of eight: chunk i of this thread's is
-// lo / 8 + threadIdx.x + i * NT.  UN loads are issued before their values are used.
+// Chunks of N logits of [lo, hi), lo a multiple of N: chunk i of this thread's is
+// lo / N + threadIdx.x + i * NT.  UN loads are issued before their values are used.
 template <bool BF16, int NT, bool STREAM, typename F>
 __device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo, int hi, F f)
 {
-    constexpr int UN = BF16 ? 4 : 2;
+    constexpr int UN = 4, N = kChunk<BF16>;
     const int64_t base = row * a.ldz;
-    const int full = lo + ((hi - lo) & ~7);
-    for (int v = lo + threadIdx.x * 8; v < full; v += UN * NT * 8) {
-        Raw8<BF16> r[UN];
+    const int full = lo + (hi - lo) / N * N;
+    for (int v = lo + threadIdx.x * N; v < full; v += UN * NT * N) {
+        Raw<BF16> r[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i)
-            if (v + i * NT * 8 < full)
-                r[i].template load<STREAM>(a.Z, base + v + i * NT * 8);
+            if (v + i * NT * N < full)
+                r[i].template load<STREAM>(a.Z, base + v + i * NT * N);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            if (v + i * NT * 8 < full) {
-                float z[8];
+            if (v + i * NT * N < full) {
+                float z[N];
                 r[i].get(z);
-                f(z, v + i * NT * 8, 8);
+                f(z, v + i * NT * N, N);
             }
         }
     }
     if (full < hi && threadIdx.x == NT - 1) {
-        Raw8<BF16> r;
+        Raw<BF16> r;
         r.fill(-kInf);
         r.load_part(a.Z, base + full, hi - full);
-        float z[8];
+        float z[N];
         r.get(z);
         f(z, full, hi - full);
     }
@@ -377,7 +388,7 @@ __device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, in
 {
     const RowGrad f(a, row, x);
     if (t.flags[0])
-        for_chunks<BF16, NT, STREAM>(a, row, lo, hi, [&](float (&z)[8], int v, int n) {
+        for_chunks<BF16, NT, STREAM>(a, row, lo, hi, [&](auto &z, int v, int n) {
             f.apply(z);
             store_upto<BF16, STREAM>(a.grad, row * a.ldg + v, z, n);
         });
@@ -418,8 +429,8 @@ __device__ __forceinline__ MaxSum join_block(const MaxSum &x, const Teacher &t, 
     return join_parts<NT / 64>(t, c);
 }
 
-// One row per workgroup.  R > 0: the row stays in registers, R chunks of eight logits per
-// thread (V <= 8 NT R), and is read once; R = 0: a gradient reads it again.
+// One row per workgroup.  R > 0: the row stays in registers, R chunks of N logits per
+// thread (V <= N NT R), and is read once; R = 0: a gradient reads it again.
 template <bool BF16, int NT, int R>
 __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int slots)
 {
@@ -427,14 +438,15 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
     const Teacher t(lds, a.K, slots);
     const float c = kLog2e / a.temperature;
     const int64_t n = row_count(a.count, a.rows);
-    const int V = a.V, full = V & ~7;
-    const int live = (full + NT * 8 - 1) / (NT * 8);
-    uint32_t d8 = threadIdx.x * 8;   // a chunk's place: a uniform pointer and this offset
+    constexpr int N = kChunk<BF16>;
+    const int V = a.V, full = V / N * N;
+    const int live = (full + NT * N - 1) / (NT * N);
+    uint32_t d0 = threadIdx.x * N;   // a chunk's place: a uniform pointer and this offset
     constexpr int64_t ES = BF16 ? 2 : 4;
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        asm volatile("" : "+v"(d8));   // or the places of all chunks stay in registers between rows
+        asm volatile("" : "+v"(d0));   // or the places of all chunks stay in registers between rows
         MaxSum x;
-        Raw8<BF16> r[R > 0 ? R : 1], rest;   // whole chunks, and the last, shorter one
+        Raw<BF16> r[R > 0 ? R : 1], rest;   // whole chunks, and the last, shorter one
         const bool has_rest = full < V && threadIdx.x == NT - 1;
         if (threadIdx.x < 64)
             load_teacher<BF16>(a, row, t, nullptr, 0, V);
@@ -442,13 +454,13 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 r[i].fill(-kInf);
-                if (i * NT * 8 + (int)d8 < full)
-                    r[i].load((const char *)a.Z + (row * a.ldz + i * NT * 8) * ES, d8);
+                if (i * NT * N + (int)d0 < full)
+                    r[i].load((const char *)a.Z + (row * a.ldz + i * NT * N) * ES, d0);
             }
             rest.fill(-kInf);
             if (has_rest)
                 rest.load_part(a.Z, row * a.ldz + full, V - full);
-            float z[8];
+            float z[kChunk<BF16>];
             rest.get(z);
             x.m = wave_reduce(held_max(r, live, has_rest ? max_of(z) : -kInf), MaxOp{});
             const Ref ref(x.m, c);
@@ -456,9 +468,9 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
         } else {
             RunningMaxSum run(c);
             if (a.grad)   // it will be read again
-                for_chunks<BF16, NT, false>(a, row, 0, V, [&](float (&z)[8], int, int) { run.add(z); });
+                for_chunks<BF16, NT, false>(a, row, 0, V, [&](auto &z, int, int) { run.add(z); });
             else
-                for_chunks<BF16, NT, true>(a, row, 0, V, [&](float (&z)[8], int, int) { run.add(z); });
+                for_chunks<BF16, NT, true>(a, row, 0, V, [&](auto &z, int, int) { run.add(z); });
             x = run.done();
             x.join_wave(c);
         }
@@ -481,17 +493,17 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
                 } else {
 #pragma unroll
                     for (int i = 0; i < R; ++i) {
-                        if (i * NT * 8 + (int)d8 < full) {
-                            float z[8];
+                        if (i * NT * N + (int)d0 < full) {
+                            float z[kChunk<BF16>];
                             r[i].opaque();
                             r[i].get(z);
                             f.apply(z);
-                            store8<BF16>((char *)a.grad + (row * a.ldg + i * NT * 8) * ES, d8, z);
+                            store<BF16>((char *)a.grad + (row * a.ldg + i * NT * N) * ES, d0, z);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     if (has_rest) {
-                        float z[8];
+                        float z[kChunk<BF16>];
                         rest.get(z);
                         f.apply(z);
                         store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
@@ -508,7 +520,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
 }
 
 // Loss and gradient of long rows.  A workgroup of 16 waves has a CU to itself and walks its
-// rows: 15 waves hold the row in registers, R chunks of eight logits per thread (V <= 7680 R),
+// rows: 15 waves hold the row in registers, R chunks of N logits per thread (V <= 960 N R),
 // and wave 0 takes the logits behind the last whole chunk, prepares the next row's teacher,
 // writes the loss and mends the entries of the row before.  As soon as a chunk's gradient is
 // stored, its registers take the next row's logits, so that reads and writes run side by side.
@@ -519,11 +531,11 @@ template <bool BF16, int R, bool STREAM>
 __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, int slots, int teacher_words)
 {
     extern __shared__ int32_t lds[];
-    constexpr int ND = 960;
+    constexpr int ND = 960, N = kChunk<BF16>;
     const Teacher t0(lds, a.K, slots), t1(lds + teacher_words, a.K, slots);
     const float c = kLog2e / a.temperature;
     const int64_t n = row_count(a.count, a.rows);
-    const int V = a.V, full = V & ~7;
+    const int V = a.V, full = V / N * N;
     int64_t row = blockIdx.x;
     if (row >= n)
         return;
@@ -576,13 +588,13 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
     }
     // Chunk i's place: a uniform pointer and the lane's offset.  The offset is hidden from the
     // compiler once per row, or it keeps the sums of all chunks in registers between rows.
-    const int live = (full + ND * 8 - 1) / (ND * 8);
-    uint32_t d8 = (threadIdx.x - 64) * 8;
-    Raw8<BF16> r[R];
+    const int live = (full + ND * N - 1) / (ND * N);
+    uint32_t d0 = (threadIdx.x - 64) * N;
+    Raw<BF16> r[R];
     constexpr int64_t ES = BF16 ? 2 : 4;
     auto fetch = [&](int i, int64_t from) __attribute__((always_inline)) {
-        if (i * ND * 8 + (int)d8 < full)
-            r[i].template load<STREAM>((const char *)a.Z + (from * a.ldz + i * ND * 8) * ES, d8);
+        if (i * ND * N + (int)d0 < full)
+            r[i].template load<STREAM>((const char *)a.Z + (from * a.ldz + i * ND * N) * ES, d0);
     };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -591,7 +603,7 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
     }
     for (bool odd = false;; odd = !odd) {
         const Teacher &t = odd ? t1 : t0;
-        asm volatile("" : "+v"(d8));
+        asm volatile("" : "+v"(d0));
         const float m = wave_reduce(held_max(r, live, -kInf), MaxOp{});
         const Ref ref(m, c);
         leave(t, m, wave_reduce(held_sum(r, live, ref), AddOp{}) * fast_exp2(-ref.off));
@@ -601,14 +613,14 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
         const bool present = t.flags[0];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            if (i * ND * 8 + (int)d8 < full) {
-                float z[8] = {};
+            if (i * ND * N + (int)d0 < full) {
+                float z[kChunk<BF16>] = {};
                 if (present) {
                     r[i].opaque();
                     r[i].get(z);
                     f.apply(z);
                 }
-                store8<BF16, STREAM>((char *)a.grad + (row * a.ldg + i * ND * 8) * ES, d8, z);
+                store<BF16, STREAM>((char *)a.grad + (row * a.ldg + i * ND * N) * ES, d0, z);
                 if (next < n)
                     fetch(i, next);
             }
@@ -648,7 +660,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_part_kernel(const Distil
     int lo, hi;
     part_range(a.V, parts, s, lo, hi);
     RunningMaxSum run(c);
-    for_chunks<BF16, kPartThreads, false>(a, row, lo, hi, [&](float (&z)[8], int, int) { run.add(z); });
+    for_chunks<BF16, kPartThreads, false>(a, row, lo, hi, [&](auto &z, int, int) { run.add(z); });
     MaxSum x = run.done();
     x.join_wave(c);
     if ((threadIdx.x & 63) == 0) {
@@ -739,7 +751,7 @@ bool is_large(const Distill &a)
 //  * up to 65536: 4 or 8 waves per row, several rows on a CU.  4000 x 20000: 72 us with 4 waves,
 //    88 us with 8, 105 us through the stream form; 2000 x 50000: 90 us with 8, 97 us there.
 //  * longer: the stream form, a row at a time on each CU, up to what its registers hold, 153600
-//    logits (4096 x 126464: 419 us; without the reads of the next row beside the writes of
+//    bf16 logits (4096 x 126464: 419 us; without the reads of the next row beside the writes of
 //    this one 475 us).
 //  * longer still: the row is read twice.
 template <bool BF16>
@@ -771,30 +783,30 @@ hipError_t run(const Distill &a, hipStream_t stream)
             hipLaunchKernelGGL(kernel, grid, dim3(1024), 2 * lds, stream, a, slots, (int)(lds / 4));
     };
     const bool many = a.rows >= 2048;
-    if (a.V <= 64 * 8 * 4)
-        rows(distill_row_kernel<BF16, 64, 4>, 64);
+    constexpr int N = kChunk<BF16>, B = 8 / N;   // B: chunks of the type that eight logits take
+    if (a.V <= 2048)
+        rows(distill_row_kernel<BF16, 64, 4 * B>, 64);
     else if (!a.grad && many && a.V <= 16384)
         rows(distill_row_kernel<BF16, 64, 0>, 64);
     else if (!a.grad)
         rows(distill_row_kernel<BF16, 256, 0>, 256);
-    else if (BF16 && many && a.V <= 64 * 8 * 16)
-        rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 4>, 64);
-    else if (a.V <= 256 * 8 * 4)
-        rows(distill_row_kernel<BF16, 256, 4>, 256);
-    else if (a.V <= 256 * 8 * 8)
-        rows(distill_row_kernel<BF16, 256, 8>, 256);
-    else if (BF16 && a.V <= 256 * 8 * 16)
-        rows(distill_row_kernel<BF16, 256, BF16 ? 16 : 8>, 256);
-    else if (!BF16 && a.V <= 512 * 8 * 8)
-        rows(distill_row_kernel<BF16, BF16 ? 256 : 512, 8>, 512);
-    else if (BF16 && a.V <= 512 * 8 * 16)
-        rows(distill_row_kernel<BF16, 512, BF16 ? 16 : 8>, 512);
-    else if (a.V <= 7680 * (BF16 ? 13 : 9))
-        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 13 : 9, false>, distill_stream_kernel<BF16, BF16 ? 13 : 9, true>);
-    else if (BF16 && a.V <= 7680 * 17)
-        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 17 : 9, false>, distill_stream_kernel<BF16, BF16 ? 17 : 9, true>);
-    else if (BF16 && a.V <= 7680 * 20)
-        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 20 : 9, false>, distill_stream_kernel<BF16, BF16 ? 20 : 9, true>);
+    else if (BF16 && many && a.V <= 8192)
+        rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 8>, 64);
+    else if (a.V <= 8192)
+        rows(distill_row_kernel<BF16, 256, 4 * B>, 256);
+    else if (a.V <= 16384)
+        rows(distill_row_kernel<BF16, 256, 8 * B>, 256);
+    else if (BF16 && a.V <= 32768)
+        rows(distill_row_kernel<BF16, 256, 16>, 256);
+    else if (a.V <= (BF16 ? 65536 : 32768))
+        rows(distill_row_kernel<BF16, 512, 16>, 512);
+    else if (a.V <= 960 * N * (BF16 ? 13 : 18))
+        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 13 : 18, false>,
+                    distill_stream_kernel<BF16, BF16 ? 13 : 18, true>);
+    else if (BF16 && a.V <= 960 * N * 17)
+        rows_per_cu(distill_stream_kernel<BF16, 17, false>, distill_stream_kernel<BF16, 17, true>);
+    else if (a.V <= 960 * N * 20)
+        rows_per_cu(distill_stream_kernel<BF16, 20, false>, distill_stream_kernel<BF16, 20, true>);
     else
         rows(distill_row_kernel<BF16, 1024, 0>, 1024);
     return hipGetLastError();
@@ -805,12 +817,12 @@ hipError_t run(const Distill &a, hipStream_t stream)
 // in one, 423 us in 16, where the teacher is prepared too often).  Of these numbers of parts
 // the one that best fills the last round of workgroups, 8 on a CU, and the last turn of their
 // loops, 4 chunks per thread (1229 rows: 109 us in 8 parts, 117 us in 4, 121 us in 5).
-int cuts_of(int64_t rows, int64_t V)
+int cuts_of(int64_t rows, int64_t V, int chunk)
 {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess)
         (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    const double slots = 8.0 * cus, chunks = (double)V / (8 * 256);
+    const double slots = 8.0 * cus, chunks = (double)V / (chunk * 256);
     int best = 1;
     double most = 0.0;
     const int64_t lo = std::max<int64_t>(1, (V + 32767) / 32768), hi = std::min<int64_t>(std::max(lo, V / 12288), lo + 63);
@@ -828,7 +840,7 @@ int cuts_of(int64_t rows, int64_t V)
 template <bool BF16>
 hipError_t run_grad(const Distill &a, hipStream_t stream)
 {
-    const int cuts = std::max(parts_of(a.rows, a.V), cuts_of(a.rows, a.V));
+    const int cuts = std::max(parts_of(a.rows, a.V), cuts_of(a.rows, a.V, kChunk<BF16>));
     auto go = [&](auto kernel, int threads) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows * cuts, 1 << 20)), dim3(threads),
                            teacher_bytes(a.K), stream, a, table_slots(a.K), 0, cuts, (const float *)nullptr);

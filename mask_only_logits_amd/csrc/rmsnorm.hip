@@ -33,16 +33,16 @@ __device__ __forceinline__ float abs_bits(float x)
     return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
 }
 
-// Codes of eight values already multiplied by top / amax (|y| <= top up to fp32 rounding).
+// Codes of N = 4 or 8 values already multiplied by top / amax (|y| <= top up to fp32 rounding).
 // INT8: adding 1.5 * 2^23 leaves the nearest even integer in the sum's low bits.  E4M3:
 // v_cvt_pk_fp8_f32 rounds to nearest even, and 448 (1 + 2^-23) is still 448.
-__device__ __forceinline__ u32x2_t make_codes(const float (&y)[8], bool int8)
+template <int N>
+__device__ __forceinline__ void make_codes(const float (&y)[N], bool int8, uint32_t (&w)[N / 4])
 {
 #pragma clang fp contract(off)   // y * inv rounds before the addition
-    u32x2_t w;
-    if (int8) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
+        if (int8) {
             uint32_t b[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -50,57 +50,100 @@ __device__ __forceinline__ u32x2_t make_codes(const float (&y)[8], bool int8)
             const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
             const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
             w[i] = lo | (hi << 16);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        } else {
             const int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
             w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], p, true);
         }
     }
-    return w;
 }
 
-typedef u32x2_t u32x2_any __attribute__((aligned(1)));
-
-// The first n of eight codes.
-__device__ __forceinline__ void store_codes(uint8_t *q, const u32x2_t &w, int n)
+// The first n of N codes, at any byte.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t *q, const uint32_t (&w)[N / 4], int n)
 {
-    if (n >= 8) {
-        *(u32x2_any *)q = w;
+    if (n >= N) {
+        __builtin_memcpy(q, w, N);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < N - 1; ++i)
         if (i < n)
             q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
 }
 
-// A thread's CH chunks of a row of d elements, chunk c from element c * STEP + t8 on, zeros
+// A thread's CH chunks of a row of d elements, chunk c from element c * STEP + t0 on, zeros
 // behind the row's end.  The whole chunks' loads go first, without a branch between them.
-template <bool BF16, int CH, int STEP, bool STREAM = false>
-__device__ __forceinline__ void load_row(const void *p, int64_t off, int t8, int d, Raw8<BF16> (&r)[CH])
+template <bool BF16, int CH, int STEP, bool STREAM>
+__device__ __forceinline__ void load_row(const void *p, int64_t off, int t0, int d, Raw<BF16> (&r)[CH])
 {
+    constexpr int N = kChunk<BF16>;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         r[c].fill(0.0f);
-        if (c * STEP + t8 + 8 <= d)
-            r[c].template load<STREAM>(p, off + c * STEP + t8);
+        if (c * STEP + t0 + N <= d)
+            r[c].template load<STREAM>(p, off + c * STEP + t0);
     }
-    if (d & 7) {
+    if (d % N) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = c * STEP + t8;
-            if (k < d && k + 8 > d)
+            const int k = c * STEP + t0;
+            if (k < d && k + N > d)
                 r[c].load_part(p, off + k, d - k);
         }
     }
 }
 
+// The gain's elements beside a chunk of N of the row's, as stored: 8, 16 or 32 bytes.
+template <bool BF16, int N>
+struct Gain {
+    static constexpr int WORDS = N * (BF16 ? 2 : 4) / 4, V = WORDS < 4 ? WORDS : 4;
+    typedef uint32_t vec_t __attribute__((ext_vector_type(V)));
+    typedef vec_t vec_any __attribute__((aligned(2)));
+    vec_t w[WORDS / V];
+
+    __device__ __forceinline__ void load(const void *p, int k, int d)
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / V; ++i) {
+            w[i] = (vec_t)(0u);
+            if (k + N <= d)
+                w[i] = ((const vec_any *)((const char *)p + (int64_t)k * (BF16 ? 2 : 4)))[i];
+        }
+    }
+    // the chunk that the row's end cuts: its first n elements
+    __device__ __forceinline__ void load_part(const void *p, int k, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i) {
+            if (i >= n)
+                continue;
+            if constexpr (BF16)
+                w[i / 2 / V][i / 2 % V] |= (uint32_t)((const uint16_t *)p)[k + i] << (16 * (i % 2));
+            else
+                w[i / V][i % V] = ((const uint32_t *)p)[k + i];
+        }
+    }
+    // keeps the elements packed up to here (as Raw::opaque does)
+    __device__ __forceinline__ void opaque()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / V; ++i)
+            asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t e = BF16 ? w[i / 2 / V][i / 2 % V] : w[i / V % (WORDS / V)][i % V];
+        if constexpr (BF16)
+            return i % 2 ? bf16_hi(e) : bf16_lo(e);
+        else
+            return __builtin_bit_cast(float, e);
+    }
+};
+
 // Power of two that keeps top / amax inside fp32 for the smallest rows (1 for all others).
 __device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
 
-// One row per WPR waves, a thread holding CH chunks of eight elements (d <= 512 WPR CH).
+// One row per WPR waves, a thread holding CH chunks of 16 bytes (d <= 64 WPR CH kChunk).
 // NORM off: y = x (plain quantization).  STREAM: streaming cache policy.
 // Bound: HBM.  32768 x 4096 bf16 with residual, sum, out and codes moves 1.21 GB in 187 us, 6.4
 // TB/s (a large copy runs at 4.75); 1229 gathered rows to codes alone take 8.5 us, where the
@@ -109,7 +152,7 @@ template <bool BF16, bool GAIN_BF16, bool NORM, int WPR, int CH, bool STREAM>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(const RowsNorm a)
 {
     constexpr int RPB = WPR == 1 ? 4 : 1;   // rows per workgroup
-    constexpr int STEP = 512 * WPR;
+    constexpr int N = kChunk<BF16>, STEP = 64 * WPR * N;
     __shared__ float red[WPR];
     const int t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t n = row_count(a.count, a.rows);
@@ -117,26 +160,37 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
          row += (int64_t)gridDim.x * RPB) {
         const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
         const bool inside = src >= 0 && src < a.nsrc;   // a row id outside gives a row of NaN
-        float v[CH][8];
-        Raw8<BF16> x[CH], r[CH];
-        Raw8<GAIN_BF16> gain[CH];   // taken with the row, not after its reduction
+        float v[CH][N];
+        Raw<BF16> x[CH], r[CH];
+        Gain<GAIN_BF16, N> gain[CH];   // taken with the row, not after its reduction
         if (inside) {
-            load_row<BF16, CH, STEP, STREAM>(a.X, src * a.ldx, t * 8, a.d, x);
+            load_row<BF16, CH, STEP, STREAM>(a.X, src * a.ldx, t * N, a.d, x);
             if (NORM && a.R)
-                load_row<BF16, CH, STEP, STREAM>(a.R, src * a.ldr, t * 8, a.d, r);
+                load_row<BF16, CH, STEP, STREAM>(a.R, src * a.ldr, t * N, a.d, r);
         }
-        if (NORM)
-            load_row<GAIN_BF16, CH, STEP>(a.gain, 0, t * 8, a.d, gain);
+        if (NORM) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                gain[c].load(a.gain, c * STEP + t * N, a.d);
+            if (a.d % N) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int k = c * STEP + t * N;
+                    if (k < a.d && k + N > a.d)
+                        gain[c].load_part(a.gain, k, a.d - k);
+                }
+            }
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             if (!inside)
                 x[c].fill(__builtin_nanf(""));
             x[c].get(v[c]);
             if (NORM && a.R && inside) {
-                float y[8];
+                float y[N];
                 r[c].get(y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < N; ++i)
                     v[c][i] += y[i];
             }
         }
@@ -144,7 +198,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
             if (a.sum) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const int k = c * STEP + t * 8;
+                    const int k = c * STEP + t * N;
                     if (k < a.d)
                         store_upto<BF16, STREAM>(a.sum, row * a.ldsum + k, v[c], a.d - k);
                 }
@@ -153,7 +207,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < N; ++i)
                     ss += v[c][i] * v[c][i];
             ss = block_reduce<WPR>(ss, AddOp{}, red);
             float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
@@ -165,20 +219,19 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < N; ++i)
                         s2 += (v[c][i] * down) * (v[c][i] * down);
                 s2 = block_reduce<WPR>(s2, AddOp{}, red);
                 rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const int k = c * STEP + t * 8;
+                const int k = c * STEP + t * N;
+                gain[c].opaque();
                 if (k < a.d) {
-                    float g[8];
-                    gain[c].get(g);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[c][i] = v[c][i] * rstd * g[i];
+                    for (int i = 0; i < N; ++i)
+                        v[c][i] = v[c][i] * rstd * gain[c].get(i);
                     if (a.out)
                         store_upto<BF16, STREAM>(a.out, row * a.d + k, v[c], a.d - k);
                 }
@@ -190,7 +243,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < N; ++i)
                 amax = MaxBitsOp{}(amax, abs_bits(v[c][i]));
         amax = block_reduce<WPR>(amax, MaxBitsOp{}, red);
         const float top = a.code_int8 ? 127.0f : 448.0f;
@@ -200,13 +253,15 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
         const float up = code_lift(amax), inv = fine ? top / (amax * up) : 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = c * STEP + t * 8;
+            const int k = c * STEP + t * N;
             if (k < a.d) {
-                float y[8];
+                float y[N];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < N; ++i)
                     y[i] = fine ? v[c][i] * up * inv : 0.0f;
-                store_codes(a.q + row * a.d + k, make_codes(y, a.code_int8), a.d - k);
+                uint32_t w[N / 4];
+                make_codes(y, a.code_int8, w);
+                store_codes<N>(a.q + row * a.d + k, w, a.d - k);
             }
         }
         if (t == 0)
@@ -268,8 +323,10 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
             if (NORM && a.out)
                 store1<BF16>(a.out, row * a.d + k, y);
             if (a.q) {
-                float z[8] = {fine ? y * up * inv : 0.0f};
-                a.q[row * a.d + k] = (uint8_t)make_codes(z, a.code_int8)[0];
+                const float z[4] = {fine ? y * up * inv : 0.0f};
+                uint32_t w[1];
+                make_codes(z, a.code_int8, w);
+                a.q[row * a.d + k] = (uint8_t)w[0];
             }
         }
         if (a.q && threadIdx.x == 0)
@@ -287,25 +344,26 @@ unsigned grid_of(int64_t rows, int per_block)
 // Rows that pass the 256 MB Infinity Cache by far are read and written with the streaming cache
 // policy: bf16, d = 4096, residual, sum, out and codes, 32768 rows (1.2 GB): 187 against 211 us,
 // 16384 rows: 93 against 106 us; 8192 rows (0.3 GB) run alike, and what reads their results
-// next finds them in the cache.  An fp32 chunk is written in two halves of 16 bytes, which that
-// policy would send out as half-filled lines (16384 x 4096: 245 against 190 us).
-bool is_large(const RowsNorm &a)
+// next finds them in the cache.
+bool is_large(const RowsNorm &a, int64_t esize)
 {
     const int64_t streams = 1 + (a.R != nullptr) + (a.sum != nullptr) + (a.out != nullptr);
-    return streams * a.rows * a.d * 2 >= (int64_t)512 << 20;
+    return streams * a.rows * a.d * esize >= (int64_t)512 << 20;
 }
 
+// CH: chunks of eight elements per thread
 template <bool BF16, bool NORM, int WPR, int CH>
 void run(const RowsNorm &a, hipStream_t stream)
 {
+    constexpr int C = CH * 8 / kChunk<BF16>;
     const dim3 grid(grid_of(a.rows, WPR == 1 ? 4 : 1)), block(WPR == 1 ? 256 : 64 * WPR);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-    if (NORM && BF16 && is_large(a))
-        a.gain_bf16 ? go(rows_norm_kernel<BF16, true, NORM, WPR, CH, NORM && BF16>)
-                    : go(rows_norm_kernel<BF16, false, NORM, WPR, CH, NORM && BF16>);
+    if (NORM && is_large(a, BF16 ? 2 : 4))
+        a.gain_bf16 ? go(rows_norm_kernel<BF16, true, NORM, WPR, C, NORM>)
+                    : go(rows_norm_kernel<BF16, false, NORM, WPR, C, NORM>);
     else
-        a.gain_bf16 || !NORM ? go(rows_norm_kernel<BF16, true, NORM, WPR, CH, false>)
-                             : go(rows_norm_kernel<BF16, !NORM, NORM, WPR, CH, false>);
+        a.gain_bf16 || !NORM ? go(rows_norm_kernel<BF16, true, NORM, WPR, C, false>)
+                             : go(rows_norm_kernel<BF16, !NORM, NORM, WPR, C, false>);
 }
 
 // Waves per row and chunks per thread, by the row's length: enough waves for short rows to

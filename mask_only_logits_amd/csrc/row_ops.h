@@ -1,5 +1,5 @@
 // Device helpers of the row kernels (norm, quantization, distillation): wave and workgroup
-// reductions, 16-byte element loads and stores, and row counts read from device memory.
+// reductions, 16-byte loads and stores of elements, and row counts read from device memory.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -91,64 +91,55 @@ __device__ __forceinline__ void put16(u32x4_any *p, const u32x4_t &w)
         *p = w;
 }
 
-// Eight elements as they are stored: 16 bytes (bf16) or 32 (fp32).
+// Elements of a chunk: what one 16-byte access holds.
 template <bool BF16>
-struct Raw8 {
-    u32x4_t w[BF16 ? 1 : 2];
+constexpr int kChunk = BF16 ? 8 : 4;
+
+// A chunk as it is stored.
+template <bool BF16>
+struct Raw {
+    static constexpr int N = kChunk<BF16>;
+    u32x4_t w;
 
     // NT: with the streaming cache policy, for data that is read once
     template <bool NT = false>
     __device__ __forceinline__ void load(const void *p, int64_t off)
     {
-        if constexpr (BF16) {
-            w[0] = get16<NT>((const u32x4_any *)((const uint16_t *)p + off));
-        } else {
-            w[0] = get16<NT>((const u32x4_any *)((const float *)p + off));
-            w[1] = get16<NT>((const u32x4_any *)((const float *)p + off + 4));
-        }
+        w = get16<NT>((const u32x4_any *)((const char *)p + off * (BF16 ? 2 : 4)));
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const
+    __device__ __forceinline__ void get(float (&x)[N]) const
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            const uint32_t e = w[i];   // (a copy: a bit cast of a vector's element takes its first one)
             if constexpr (BF16) {
-                x[2 * i] = bf16_lo(w[0][i]);
-                x[2 * i + 1] = bf16_hi(w[0][i]);
+                x[2 * i] = bf16_lo(e);
+                x[2 * i + 1] = bf16_hi(e);
             } else {
-                // (copies: a bit cast of a vector's element itself takes its first one)
-                const uint32_t lo = w[0][i], hi = w[1][i];
-                x[i] = __builtin_bit_cast(float, lo);
-                x[4 + i] = __builtin_bit_cast(float, hi);
+                x[i] = __builtin_bit_cast(float, e);
             }
         }
     }
     __device__ __forceinline__ void fill(float v)
     {
         const uint32_t b = __builtin_bit_cast(uint32_t, v), f = BF16 ? (b & 0xffff0000u) | (b >> 16) : b;
-#pragma unroll
-        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
-            w[i] = u32x4_t{f, f, f, f};
+        w = u32x4_t{f, f, f, f};
     }
     // Keeps the compiler from carrying the unpacked floats of an earlier use past this point:
     // rows held in registers are held as they are stored.
-    __device__ __forceinline__ void opaque()
-    {
-#pragma unroll
-        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
-            asm volatile("" : "+v"(w[i]));
-    }
-    // the first n < 8 elements (n >= 1), the rest left as they are
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
+    // the first n < N elements (n >= 1), the rest left as they are
     __device__ __forceinline__ void load_part(const void *p, int64_t off, int n)
     {
 #pragma unroll
-        for (int i = 0; i < 7; ++i) {
+        for (int i = 0; i < N - 1; ++i) {
             if (i >= n)
                 continue;
             if constexpr (BF16) {
                 const uint32_t e = ((const uint16_t *)p)[off + i];
-                w[0][i >> 1] = i & 1 ? (w[0][i >> 1] & 0xffffu) | (e << 16) : (w[0][i >> 1] & 0xffff0000u) | e;
+                w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | (e << 16) : (w[i >> 1] & 0xffff0000u) | e;
             } else {
-                w[i >> 2][i & 3] = ((const uint32_t *)p)[off + i];
+                w[i] = ((const uint32_t *)p)[off + i];
             }
         }
     }
@@ -168,31 +159,29 @@ __device__ __forceinline__ void store1(void *p, int64_t off, float x)
         ((float *)p)[off] = x;
 }
 
-// Eight results; bf16 values are rounded to nearest even here.  NT: streaming cache policy.
+// A chunk of results; bf16 values are rounded to nearest even here.  NT: streaming cache policy.
 template <bool BF16, bool NT = false>
-__device__ __forceinline__ void store8(void *p, int64_t off, const float (&x)[8])
+__device__ __forceinline__ void store(void *p, int64_t off, const float (&x)[kChunk<BF16>])
 {
-    if constexpr (BF16) {
-        put16<NT>((u32x4_any *)((uint16_t *)p + off), u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
-    } else {
-        u32x4_t w[2];
+    u32x4_t w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, x[i]);
-        put16<NT>((u32x4_any *)((float *)p + off), w[0]);
-        put16<NT>((u32x4_any *)((float *)p + off + 4), w[1]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16)
+            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        else
+            w[i] = __builtin_bit_cast(uint32_t, x[i]);
     }
+    put16<NT>((u32x4_any *)((char *)p + off * (BF16 ? 2 : 4)), w);
 }
 
-// The first n of eight results.
+// The first n results of a chunk.
 template <bool BF16, bool NT = false>
-__device__ __forceinline__ void store_upto(void *p, int64_t off, const float (&x)[8], int n)
+__device__ __forceinline__ void store_upto(void *p, int64_t off, const float (&x)[kChunk<BF16>], int n)
 {
-    if (n >= 8)
-        return store8<BF16, NT>(p, off, x);
+    if (n >= kChunk<BF16>)
+        return store<BF16, NT>(p, off, x);
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < kChunk<BF16> - 1; ++i)
         if (i < n)
             store1<BF16>(p, off + i, x[i]);
 }
