@@ -381,6 +381,14 @@ __device__ __forceinline__ void for_chunks(const Distill &a, int64_t row, int lo
     }
 }
 
+// Barrier between the gradient's bulk and the entries written again: every wave's stores have
+// been acknowledged before any wave passes it.
+__device__ __forceinline__ void barrier_after_stores()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    __syncthreads();
+}
+
 // Gradient bulk of the part [lo, hi) of a row, then the teacher's entries in it.
 template <bool BF16, int NT, bool STREAM>
 __device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, int64_t row, int lo, int hi,
@@ -394,7 +402,7 @@ __device__ __forceinline__ void part_grad(const Distill &a, const Teacher &t, in
         });
     else
         zero_grad<BF16, NT>(a, row, lo, hi);
-    __syncthreads();   // orders the two writes of an entry
+    barrier_after_stores();
     fix_entries<BF16, NT>(a, t, row, lo, hi, f);
 }
 
@@ -509,7 +517,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
                         store_upto<BF16>(a.grad, row * a.ldg + full, z, V - full);
                     }
                 }
-                __syncthreads();   // orders the two writes of an entry
+                barrier_after_stores();
                 fix_entries<BF16, NT>(a, t, row, 0, V, f);
             } else {
                 part_grad<BF16, NT, false>(a, t, row, 0, V, x);
@@ -578,7 +586,7 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
             const int64_t next = row + gridDim.x;
             if (next < n)
                 prepare(next, other);
-            __syncthreads();
+            barrier_after_stores();
             if (next >= n) {
                 fix_entries<BF16, 64>(a, t, row, 0, V, f);
                 return;
@@ -607,7 +615,7 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
         const float m = wave_reduce(held_max(r, live, -kInf), MaxOp{});
         const Ref ref(m, c);
         leave(t, m, wave_reduce(held_sum(r, live, ref), AddOp{}) * fast_exp2(-ref.off));
-        __syncthreads();
+        barrier_after_stores();   // of the row before, which wave 0 mends after it
         const RowGrad f(a, row, join_parts<16>(t, c));
         const int64_t next = row + gridDim.x;
         const bool present = t.flags[0];
@@ -627,7 +635,7 @@ __global__ __launch_bounds__(1024) void distill_stream_kernel(const Distill a, i
             __builtin_amdgcn_sched_barrier(0);
         }
         if (next >= n) {
-            __syncthreads();   // the last row's stores, before its entries are mended
+            barrier_after_stores();
             return;
         }
         row = next;
@@ -744,6 +752,10 @@ bool is_large(const Distill &a)
     return a.rows * a.V >= ((int64_t)256 << 20) / (BF16 ? 2 : 4);
 }
 
+// Chunks per thread of the stream form: 20 fill its registers.
+template <bool BF16>
+constexpr int kStreamChunks[3] = {BF16 ? 13 : 10, BF16 ? 17 : 15, 20};
+
 // Which form a row takes, by its length (bf16; fp32 chunks take twice the registers):
 //  * up to 2048 logits: a wave per row.  Up to 8192: a wave per row where there are rows enough
 //    for several waves per SIMD, else four waves (8000 x 8000, loss and gradient: 56 against
@@ -791,7 +803,7 @@ hipError_t run(const Distill &a, hipStream_t stream)
     else if (!a.grad)
         rows(distill_row_kernel<BF16, 256, 0>, 256);
     else if (BF16 && many && a.V <= 8192)
-        rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 8>, 64);
+        rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 4 * B>, 64);
     else if (a.V <= 8192)
         rows(distill_row_kernel<BF16, 256, 4 * B>, 256);
     else if (a.V <= 16384)
@@ -800,13 +812,15 @@ hipError_t run(const Distill &a, hipStream_t stream)
         rows(distill_row_kernel<BF16, 256, 16>, 256);
     else if (a.V <= (BF16 ? 65536 : 32768))
         rows(distill_row_kernel<BF16, 512, 16>, 512);
-    else if (a.V <= 960 * N * (BF16 ? 13 : 18))
-        rows_per_cu(distill_stream_kernel<BF16, BF16 ? 13 : 18, false>,
-                    distill_stream_kernel<BF16, BF16 ? 13 : 18, true>);
-    else if (BF16 && a.V <= 960 * N * 17)
-        rows_per_cu(distill_stream_kernel<BF16, 17, false>, distill_stream_kernel<BF16, 17, true>);
-    else if (a.V <= 960 * N * 20)
-        rows_per_cu(distill_stream_kernel<BF16, 20, false>, distill_stream_kernel<BF16, 20, true>);
+    else if (a.V <= 960 * N * kStreamChunks<BF16>[0])
+        rows_per_cu(distill_stream_kernel<BF16, kStreamChunks<BF16>[0], false>,
+                    distill_stream_kernel<BF16, kStreamChunks<BF16>[0], true>);
+    else if (a.V <= 960 * N * kStreamChunks<BF16>[1])
+        rows_per_cu(distill_stream_kernel<BF16, kStreamChunks<BF16>[1], false>,
+                    distill_stream_kernel<BF16, kStreamChunks<BF16>[1], true>);
+    else if (a.V <= 960 * N * kStreamChunks<BF16>[2])
+        rows_per_cu(distill_stream_kernel<BF16, kStreamChunks<BF16>[2], false>,
+                    distill_stream_kernel<BF16, kStreamChunks<BF16>[2], true>);
     else
         rows(distill_row_kernel<BF16, 1024, 0>, 1024);
     return hipGetLastError();

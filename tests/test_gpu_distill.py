@@ -52,6 +52,36 @@ def test_distill_sizes(m, M, V, K, dtype):
     _check(m, z, t, ids, 1.0, w, "T=1")
 
 
+# row counts and lengths on both sides of each form's limits
+FORMS = [(200, 2047), (200, 2049), (2100, 2048), (2050, 8192), (150, 8191), (140, 8193), (130, 16384), (130, 16385),
+         (130, 32768), (130, 32769), (129, 38401), (129, 57601), (129, 65536), (129, 65537), (129, 76801),
+         (129, 99841), (129, 130561), (129, 153600), (129, 153601), (2049, 4097), (1025, 16400), (300, 126464)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V", FORMS)
+def test_distill_forms(m, M, V, dtype):
+    g = torch.Generator(device=DEV).manual_seed(M + V)
+    z = (2 * torch.randn(M, V, generator=g, device=DEV)).to(dtype)
+    t = 2 * torch.randn(M, 7, generator=g, device=DEV)
+    ids = torch.randint(-1, V, (M, 7), generator=g, dtype=torch.int32, device=DEV)
+    w = torch.rand(M, generator=g, device=DEV)
+    # the plain form on rows at both ends and in between; the others against the two calls' agreement
+    rows = torch.tensor(sorted({0, 1, M // 3, M // 2, M - 2, M - 1}), device=DEV)
+    ref = plain64.distill(z[rows], t[rows], ids[rows], 1.0, w[rows])
+    loss, stats, grad = m.mosaic_distill_topk(z, t, ids, with_grad=True, grad_loss=w)
+    plain64.check_distill(ref, loss[rows], stats[rows], grad[rows], "both")
+    alone, stats2, _ = m.mosaic_distill_topk(z, t, ids)
+    plain64.check_distill(ref, alone[rows], stats2[rows], None, "loss")
+    later = m.mosaic_distill_topk_grad(z, t, ids, stats2, grad_loss=w)
+    plain64.check_distill(ref, None, None, later[rows], "gradient")
+    assert torch.equal(stats[:, 0], stats2[:, 0]) and torch.equal(stats[:, 0], z.float().amax(1))
+    # both carry L_ABS of l's error on each row's q, and a rounding of the result
+    size = float(w.max()) * 2 * (8 * plain64.L_ABS + 2 * plain64.HALF[dtype])
+    assert float((later.float() - grad.float()).abs().max()) <= size
+    assert float((loss - alone).abs().max()) <= 64 * plain64.L_ABS
+
+
 @pytest.mark.parametrize("T", [2.0 ** -20, 0.05, 0.7, 3.0, 100.0, 2.0 ** 20])
 @pytest.mark.parametrize("t_dtype", [BF, F32])
 def test_distill_temperatures(m, T, t_dtype):

@@ -49,6 +49,28 @@ def test_int8_few_rows(m, M, V, d):
         plain64.check_int8_logits(got, hq, hs, wq, ws, "logits")
 
 
+@pytest.mark.parametrize("M,V,d", [
+    (100, 20000, 256), (128, 16500, 144),                        # 64 x 128 tiles, all at once
+    (300, 11000, 128), (300, 11000, 384), (300, 11000, 640),     # 256 x 256 tiles: 1, 3 and 5 K tiles
+    (300, 11001, 16), (300, 11001, 272), (300, 11003, 1040),     # ... that the depth does not fill
+    (600, 30000, 128), (600, 30000, 400),                        # several tiles per workgroup
+    (16484, 600, 128), (16484, 600, 304),                        # row tiles past a full super-group
+])
+def test_int8_large_tiles(m, M, V, d):
+    hq, hs = _codes(M, M, d)
+    wq, ws = _codes(V, V, d)
+    rows = torch.tensor(sorted({0, 1, 63, 64, 255 % M, 256 % M, M // 2, M - 65, M - 2, M - 1}), device=DEV)
+    for out_dtype in (BF, F32):
+        out = torch.full((M + 1, V), 7.0, dtype=out_dtype, device=DEV)
+        got = m.mosaic_quantized_logits(hq, hs, wq, ws, out=out)
+        plain64.check_int8_logits(got[rows], hq[rows], hs[rows], wq, ws, "logits")
+        assert bool((out[M] == 7).all())
+        # every row, against the library's own other form: the same bits
+        for r in range(0, M, max(32, M // 8 // 32 * 32)):
+            part = m.mosaic_quantized_logits(hq[r:r + 32], hs[r:r + 32], wq, ws, out_dtype=out_dtype)
+            assert torch.equal(part, got[r:r + 32][:part.shape[0]])
+
+
 def test_int8_largest_sums(m):
     # every code -128 at the greatest depth: sums of 131071 * 2^14, next to int32's end
     for d in (131071, 130944):
@@ -63,7 +85,7 @@ def test_int8_largest_sums(m):
     assert e.value.status == m.MOSAIC_ERR_UNSUPPORTED
 
 
-@pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100)])
+@pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100), (300, 11000, 256), (90, 17000, 128)])
 def test_int8_device_count(m, M, V, d):
     hq, hs = _codes(1, M, d)
     wq, ws = _codes(2, V, d)
