@@ -331,7 +331,8 @@ mosaic_status_t mosaic_masked_logits_fp8(const void *H, int64_t L, int64_t d, co
  * top = 448 (MOSAIC_E4M3) or 127 (MOSAIC_INT8).  All arithmetic is fp32; sum, out and q are
  * each rounded once, from unrounded fp32 values.  A zero row has zero codes and scale 0.
  *   X, R      [nsrc, d] in in_dtype (F32 or BF16), row strides ldx, ldr >= d elements.
- *   gain      [d] in gain_dtype.  eps > 0 and finite.
+ *   gain      [d] in gain_dtype.  2^-126 <= eps < inf: squares too small for fp32 then do
+ *             not count beside it.
  *   row_idx   NULL or int32[rows], any order, repeats allowed.  A value outside [0, nsrc)
  *             gives a row of NaN (codes zero, scale NaN).
  *   count     NULL (n = rows), or int32* in device memory, read when the kernel starts:

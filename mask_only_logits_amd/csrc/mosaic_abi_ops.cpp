@@ -40,7 +40,7 @@ mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, in
                                    void *stream)
 {
     const int64_t es = esize_of(in_dtype), gs = esize_of(gain_dtype);
-    if (nsrc < 0 || d < 0 || rows < 0 || es == 0 || gs == 0 || !(eps > 0.0f) || !isfinite(eps) ||
+    if (nsrc < 0 || d < 0 || rows < 0 || es == 0 || gs == 0 || !(eps >= 0x1p-126f) || !isfinite(eps) ||
         (q && !known(code)))
         return MOSAIC_ERR_INVALID_ARG;
     if (rows == 0)

@@ -29,7 +29,8 @@ def _norm(m, X=A16, ldx=64, R=B16, ldr=64, nsrc=100, d=64, i=BF16, gain=A16, g=B
 @pytest.mark.parametrize("kw,status", [
     (dict(nsrc=-1), INVALID), (dict(d=-1), INVALID), (dict(rows=-1), INVALID), (dict(d=0), INVALID),
     (dict(nsrc=0), INVALID), (dict(i=2), INVALID), (dict(g=2), INVALID),
-    (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID),
+    (dict(eps=0.0), INVALID), (dict(eps=2.0 ** -127), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID),
     (dict(X=None), INVALID), (dict(gain=None), INVALID), (dict(out=None), INVALID),
     (dict(q=A16), INVALID), (dict(q=A16, sc=A16, code=2), INVALID), (dict(q=A16, sc=A16, code=-1), INVALID),
     (dict(ldx=63), INVALID), (dict(ldr=63), INVALID), (dict(sum=C16 + 4096, lds=63), INVALID),
