@@ -165,6 +165,18 @@ __global__ __launch_bounds__(256) void gemm_int8_any_kernel(const int8_t *__rest
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
+// Requests straight to LDS: 16 bytes per lane, lane i's to lds + 16 i (STREAM: streaming cache
+// policy), or 4.
+template <bool STREAM>
+__device__ __forceinline__ void request(const void *src, void *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 16, 0, STREAM ? 2 : 0);
+}
+__device__ __forceinline__ void request4(const void *src, void *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 4, 0, 0);
+}
+
 // s_waitcnt vmcnt(N) lgkmcnt(0)
 template <int N>
 __device__ __forceinline__ void wait_vm()
@@ -185,7 +197,7 @@ __device__ __forceinline__ void bar()
 // What a request past the end of a row reads (rows whose d is no multiple of the K tile).
 __device__ __attribute__((aligned(16))) const int8_t kZeroCodes[16] = {};
 
-// 256 x 256 outputs per workgroup of eight waves, walked persistently.  K tiles of 128 codes
+// BM x 256 outputs per workgroup of eight waves, BM = 128 or 256, walked persistently.  K tiles of 128 codes
 // are rows of 128 bytes, as the bf16 kernel's K tiles of 64 elements are, and
 // v_mfma_i32_16x16x64_i8 takes the 16 bytes per lane and the cycles of
 // v_mfma_f32_16x16x32_bf16 at twice the products, so the pipeline is that kernel's: requests
@@ -198,16 +210,17 @@ __device__ __attribute__((aligned(16))) const int8_t kZeroCodes[16] = {};
 //  * Epilogue: int32 -> fp32, times both scales, rounded; lanes trade words so that each
 //    store instruction writes whole 128-byte lines.
 //  * TAIL: d is a multiple of 16 only; chunks past the row's end are read from kZeroCodes.
-template <bool OUT_BF16, bool TAIL>
+//  * STREAM: W is read once (one row tile): its requests take the streaming cache policy.
+template <int BM, bool STREAM, bool OUT_BF16, bool TAIL>
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2))) void
 gemm_int8_kernel(const int8_t *__restrict__ Hq, const float *__restrict__ hs, const int32_t *__restrict__ rows_dev,
                  int32_t max_rows, const int8_t *__restrict__ Wq, const float *__restrict__ ws, int32_t V, int32_t d,
                  void *__restrict__ out, int64_t ldo, int32_t group_m)
 {
-    constexpr int NW = 8, DMAW = 4, BV = 256, BM = 256, BK = 128, WST = 3, HST = 2;
+    constexpr int NW = 8, NWV = BM == 128 ? 4 : 2, DMAW = 4, BV = 256, BK = 128, WST = 3, HST = 2;
     constexpr int CHUNKS = BK / 16, RPI = 64 / CHUNKS;          // rows per request instruction
     constexpr int W_TILE = BV * BK, H_TILE = BM * BK, H_BASE = WST * W_TILE;
-    constexpr int WV = BV / 2, WM = BM / (NW / 2), AV = WV / 16, AM = WM / 16;
+    constexpr int WV = BV / NWV, WM = BM / (NW / NWV), AV = WV / 16, AM = WM / 16;
     constexpr int LW = BV / RPI / DMAW, LH = BM / RPI / DMAW;   // requests per requesting wave
     static_assert(H_BASE + HST * H_TILE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem[H_BASE + HST * H_TILE];
@@ -245,14 +258,15 @@ gemm_int8_kernel(const int8_t *__restrict__ Hq, const float *__restrict__ hs, co
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wv = wave & 1, wm = wave >> 1, dwave = wave % DMAW;
+    const int wv = wave % NWV, wm = wave / NWV, dwave = wave % DMAW;
     auto swz = [](int r) { return (r >> 1) & 7; };
 
     // Requests: lane i of instruction j fills tile row (dwave * L + j) * RPI + i / CHUNKS, whose
     // logical chunk (i % CHUNKS) ^ swz(row) goes to physical chunk i % CHUNKS.  Rows past V /
     // rows re-read the last valid row; their results are never stored.
-    auto tile_row = [&](int j) { return (dwave * LW + j) * RPI + lane / CHUNKS; };
-    auto chunk_of = [&](int j) { return ((lane % CHUNKS) ^ swz(tile_row(j))) * 16; };
+    auto tile_row = [&](int j, int per_wave) { return (dwave * per_wave + j) * RPI + lane / CHUNKS; };
+    auto chunk_of = [&](int j) { return ((lane % CHUNKS) ^ swz(tile_row(j, LW))) * 16; };
+    static_assert(LW % 2 == 0 && LH % 2 == 0, "rows of W and of H that one lane requests swizzle alike");
     const int8_t *wbase, *hbase;
     uint32_t woff[LW], hoff[LH];
     auto make_src = [&](int m0, int v0) __attribute__((always_inline)) {
@@ -260,34 +274,32 @@ gemm_int8_kernel(const int8_t *__restrict__ Hq, const float *__restrict__ hs, co
         hbase = Hq + (int64_t)m0 * d;
 #pragma unroll
         for (int j = 0; j < LW; ++j)
-            woff[j] = (uint32_t)min(tile_row(j), V - 1 - v0) * (uint32_t)d + (uint32_t)chunk_of(j);
+            woff[j] = (uint32_t)min(tile_row(j, LW), V - 1 - v0) * (uint32_t)d + (uint32_t)chunk_of(j);
 #pragma unroll
         for (int j = 0; j < LH; ++j)
-            hoff[j] = (uint32_t)min(tile_row(j), rows - 1 - m0) * (uint32_t)d + (uint32_t)chunk_of(j);
+            hoff[j] = (uint32_t)min(tile_row(j, LH), rows - 1 - m0) * (uint32_t)d + (uint32_t)chunk_of(j);
     };
-    auto request = [&](const int8_t *base, uint32_t off, int kb, int j, int lds) __attribute__((always_inline)) {
+    auto source = [&](const int8_t *base, uint32_t off, int kb, int j) __attribute__((always_inline)) {
         const int8_t *src = base + kb + off;
         if constexpr (TAIL)
             src = kb + chunk_of(j) < d ? src : kZeroCodes;
-        __builtin_amdgcn_global_load_lds((const void *)src, (lds_void_t *)(smem + lds), 16, 0, 0);
+        return src;
     };
     auto issue_w = [&](int rw, int kt) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < LW; ++j)
-            request(wbase, woff[j], kt * BK, j, rw + (dwave * LW + j) * 1024);
+            request<STREAM>(source(wbase, woff[j], kt * BK, j), smem + rw + (dwave * LW + j) * 1024);
     };
     auto issue_h = [&](int rh, int kt) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < LH; ++j)
-            request(hbase, hoff[j], kt * BK, j, rh + (dwave * LH + j) * 1024);
+            request<false>(source(hbase, hoff[j], kt * BK, j), smem + rh + (dwave * LH + j) * 1024);
     };
     // row scales: 256 of W, then 256 of H, indices clamped to the last valid row
     auto issue_scales = [&](int at, int m0, int v0) __attribute__((always_inline)) {
         const int r = dwave * 64 + lane;
-        __builtin_amdgcn_global_load_lds((const void *)(ws + min(v0 + r, V - 1)), (lds_void_t *)(smem + at + dwave * 256),
-                                         4, 0, 0);
-        __builtin_amdgcn_global_load_lds((const void *)(hs + min(m0 + r, rows - 1)),
-                                         (lds_void_t *)(smem + at + BV * 4 + dwave * 256), 4, 0, 0);
+        request4(ws + min(v0 + r, V - 1), smem + at + dwave * 256);
+        request4(hs + min(m0 + r, rows - 1), smem + at + BV * 4 + dwave * 256);
     };
     auto next_w = [](int rw) { return rw + W_TILE == H_BASE ? 0 : rw + W_TILE; };
     auto next_h = [](int rh) { return rh + H_TILE == H_BASE + HST * H_TILE ? H_BASE : rh + H_TILE; };
@@ -575,7 +587,6 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
     constexpr int W_TILE = BV * BK, STAGE = W_TILE + BM * BK;
     constexpr int LW = BV / RPI / 4, LH = BM / RPI / 4, T = LW + LH;   // requests per wave and K tile
     static_assert(LW >= 1 && LH >= 1 && NSTAGE >= 3 && (NSTAGE - 2) * T < 64, "requests");
-    constexpr int kPolicy = STREAM ? 2 : 0;   // NT: streaming
     __shared__ __attribute__((aligned(1024))) char smem[NSTAGE * STAGE];
 
     const int rows = (int)rows::row_count(rows_dev, max_rows);
@@ -608,11 +619,11 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 #pragma unroll
         for (int j = 0; j < T; ++j) {
             const int8_t *p = kb + chunk[j] < d ? src[j] + kb : kZeroCodes;
-            const int at = stage * STAGE + (j < LW ? (wave * LW + j) * 1024 : W_TILE + (wave * LH + j - LW) * 1024);
+            char *at = smem + stage * STAGE + (j < LW ? (wave * LW + j) * 1024 : W_TILE + (wave * LH + j - LW) * 1024);
             if (j < LW)
-                __builtin_amdgcn_global_load_lds((const void *)p, (lds_void_t *)(smem + at), 16, 0, kPolicy);
+                request<STREAM>(p, at);
             else
-                __builtin_amdgcn_global_load_lds((const void *)p, (lds_void_t *)(smem + at), 16, 0, 0);
+                request<false>(p, at);
         }
     };
     i32x4_t acc[AV][AM];
@@ -687,15 +698,21 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 // bf16 output; the forms give the same bits):
 //  * codes that are not 16-byte aligned rows (d % 16 != 0): gemm_int8_any_kernel.
 //  * at most 32 rows, at most 64 rows: W is streamed once past a row tile of 32 or 64 rows.
-//    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 147 us with the 256 x 256 form; 64 rows:
-//    107 against 146 us.  Vocabulary tiles of 128 entries, or of 64 where that gives less than
-//    one workgroup per CU.
-//  * up to 128 rows whose 64 x 128 tiles fit on the chip at once, two on a CU, take those:
-//    100 x 30000 x 4096: 26 us, 45 us with 256 x 256 tiles, of which half the CUs get none.
-//  * more rows: 256 x 256 tiles where there are enough to fill a good part of the chip, else
-//    64 x 64.  300 x 30000 x 2048 (236 tiles): 32 against 45 us; 1000 x 10000 x 1024 (160):
-//    21 against 30 us; 1024 x 4096 x 4096 (64): 40 against 34 us; 200 x 8192 x 4096 (32): 44
-//    against 19 us.  The two meet near 80 tiles on 256 CUs.
+//    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 106 us with tiles of 128 rows; 64 rows:
+//    109 against 108 us, but 48 rows 104 against 105, 33 rows 96 against 108.  Vocabulary tiles
+//    of 128 entries, or of 64 where that gives less than one workgroup per CU (64 x 30000 x 4096:
+//    29 against 33 us).
+//  * more rows, but too few 128 x 256 tiles to fill three eighths of the chip: 64 x 64 tiles.
+//    200 x 8192 x 4096 (64 tiles of 128 x 256): 18 against 23 us; 512 x 8192 x 4096 (128 tiles):
+//    33 against 24 us.
+//  * else tiles of 128 or 256 rows, by the rounds that the CUs need for either, a tile of 128
+//    rows at three fifths of one of 256 (it halves the products, but not the codes of W):
+//    128 x 152064 x 3584: 111 against 147 us; 384 x 126464 x 4096: 208 against 223; 192 x 152064 x
+//    3584: 161 against 148; 1229 x 126464 x 4096: 624 against 530.
+//  * one row tile reads W once, with the streaming cache policy: 128 x 152064 x 3584: 111 against
+//    119 us, 256 x 100000 x 2048: 69 against 75.  It holds for a smaller W too where other work
+//    has been through the caches since the last call (20 x 50000 x 4096: 42 against 48 us; right
+//    after a call that left W there, 39 against 32).
 hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *count, int64_t rows, const int8_t *Wq,
                             const float *ws, int64_t V, int64_t d, void *out, bool out_bf16, int64_t ldo,
                             hipStream_t stream)
@@ -718,16 +735,27 @@ hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *co
             return go(gemm_int8_small_kernel<32, 64, 1, 4, true, B>, tiles(32, 64), 256);
         if (rows <= 64 && tiles(64, 128) >= cus)
             return go(gemm_int8_small_kernel<64, 128, 1, 3, true, B>, tiles(64, 128), 256);
-        if (rows > 64 && rows <= 128 && tiles(64, 128) >= cus && tiles(64, 128) <= 2 * cus)
-            return go(gemm_int8_small_kernel<64, 128, 1, 3, false, B>, tiles(64, 128), 256);
-        if (tiles(256, 256) * 16 < cus * 5)
+        if (rows <= 64)
+            return go(gemm_int8_small_kernel<64, 64, 2, 4, true, B>, tiles(64, 64), 256);
+        if (tiles(128, 256) * 8 < cus * 3)
             return go(gemm_int8_small_kernel<64, 64, 2, 4, false, B>, tiles(64, 64), 256);
-        // one persistent workgroup per CU, a multiple of the eight XCDs
-        const int64_t grid = std::min<int64_t>(std::max(8, cus / 8 * 8), (tiles(256, 256) + 7) / 8 * 8);
-        if (d % 128 == 0)
-            go(gemm_int8_kernel<B, false>, grid, 512, kDefaultGroupM);
+        auto large = [&](auto bm_tag) {
+            constexpr int BM = decltype(bm_tag)::value;
+            const int64_t n = tiles(BM, 256);
+            // one persistent workgroup per CU, a multiple of the eight XCDs
+            const int64_t grid = std::min<int64_t>(std::max(8, cus / 8 * 8), (n + 7) / 8 * 8);
+            if (d % 128 != 0)
+                go(gemm_int8_kernel<BM, false, B, true>, grid, 512, kDefaultGroupM);
+            else if (rows <= BM)
+                go(gemm_int8_kernel<BM, true, B, false>, grid, 512, kDefaultGroupM);
+            else
+                go(gemm_int8_kernel<BM, false, B, false>, grid, 512, kDefaultGroupM);
+        };
+        auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
+        if (rounds(tiles(128, 256)) * 3 < rounds(tiles(256, 256)) * 5)
+            large(std::integral_constant<int, 128>{});
         else
-            go(gemm_int8_kernel<B, true>, grid, 512, kDefaultGroupM);
+            large(std::integral_constant<int, 256>{});
     };
     if (out_bf16)
         pick(std::true_type{});

@@ -50,11 +50,17 @@ def test_int8_few_rows(m, M, V, d):
 
 
 @pytest.mark.parametrize("M,V,d", [
-    (100, 20000, 256), (128, 16500, 144),                        # 64 x 128 tiles, all at once
-    (300, 11000, 128), (300, 11000, 384), (300, 11000, 640),     # 256 x 256 tiles: 1, 3 and 5 K tiles
+    (100, 20000, 256), (128, 16500, 144),                        # 64 x 64 tiles
+    (100, 30000, 128), (128, 25000, 384), (65, 80001, 400),      # one row tile of 128 rows, the last with several per CU
+    (300, 11000, 128), (300, 11000, 384), (300, 11000, 640),     # 128 x 256 tiles: 1, 3 and 5 K tiles
     (300, 11001, 16), (300, 11001, 272), (300, 11003, 1040),     # ... that the depth does not fill
-    (600, 30000, 128), (600, 30000, 400),                        # several tiles per workgroup
-    (16484, 600, 128), (16484, 600, 304),                        # row tiles past a full super-group
+    (600, 30000, 128), (600, 30000, 256), (600, 30000, 400),     # ... several tiles per workgroup
+    (8300, 400, 128), (8300, 400, 640),                          # ... row tiles past a full super-group
+    (200, 33000, 128), (200, 33000, 384), (250, 70001, 512),     # one row tile of 256 rows
+    (300, 25600, 128), (300, 25600, 384), (300, 25600, 640),     # 256 x 256 tiles: 1, 3 and 5 K tiles
+    (300, 25601, 16), (300, 25601, 272), (300, 25603, 1040),     # ... that the depth does not fill
+    (1100, 25600, 128), (1100, 25600, 400),                      # ... several tiles per workgroup
+    (16484, 600, 128), (16484, 600, 304),                        # ... row tiles past a full super-group
 ])
 def test_int8_large_tiles(m, M, V, d):
     hq, hs = _codes(M, M, d)
@@ -85,7 +91,8 @@ def test_int8_largest_sums(m):
     assert e.value.status == m.MOSAIC_ERR_UNSUPPORTED
 
 
-@pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100), (300, 11000, 256), (90, 17000, 128)])
+@pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100), (300, 11000, 256), (90, 17000, 128),
+                                   (300, 25600, 256), (120, 25600, 256), (200, 33000, 128)])
 def test_int8_device_count(m, M, V, d):
     hq, hs = _codes(1, M, d)
     wq, ws = _codes(2, V, d)
