@@ -44,121 +44,178 @@ __device__ __forceinline__ void store4(void *out, int64_t off, const float (&x)[
     }
 }
 
-// Any shape and alignment.  64 x 64 outputs per workgroup of four waves, 32 x 32 each; K in
-// steps of 128 codes, fetched two steps ahead into registers with 16-byte loads at any byte
-// address and staged into LDS (rows of 128 + 16 bytes, which spreads the 16-byte fragment
-// reads over the banks); codes past d, V or the rows are zeros.  Bound by the steps' latency:
-// 2 x 13433 x 5656 takes 32 us, and took 47 us when fetched 64 codes and one step ahead.
-template <bool OUT_BF16>
-__global__ __launch_bounds__(256) void gemm_int8_any_kernel(const int8_t *__restrict__ Hq,
-                                                            const float *__restrict__ hs,
-                                                            const int32_t *__restrict__ count, int32_t max_rows,
-                                                            const int8_t *__restrict__ Wq,
-                                                            const float *__restrict__ ws, int32_t V, int32_t d,
-                                                            void *__restrict__ out, int64_t ldo)
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_vm()
 {
-    constexpr int BK = 128, PITCH = BK + 16;
-    __shared__ __attribute__((aligned(16))) char smem[2 * 128 * PITCH];
-    const int rows = (int)rows::row_count(count, max_rows);
-    const int nvt = (V + 63) / 64;
-    const int v0 = (int)(blockIdx.x % nvt) * 64, m0 = (int)(blockIdx.x / nvt) * 64;
-    if (m0 >= rows)
-        return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    // thread t stages 32 codes of W row t / 4 and of H row t / 4, 64 codes apart
-    const int sr = tid >> 2, sk = (tid & 3) * 16;
-    const bool w_ok = v0 + sr < V, h_ok = m0 + sr < rows;
-    const int8_t *wp = Wq + (int64_t)(w_ok ? v0 + sr : 0) * d;
-    const int8_t *hp = Hq + (int64_t)(h_ok ? m0 + sr : 0) * d;
-    auto fetch = [&](const int8_t *p, bool ok, int k) __attribute__((always_inline)) {
-        i32x4_t r = {0, 0, 0, 0};
-        if (!ok || k >= d)
-            return r;
-        if (k + 16 <= d) {
-            __builtin_memcpy(&r, p + k, 16);   // rows may start at any byte
-            return r;
-        }
-#pragma unroll
-        for (int b = 0; b < 15; ++b)
-            if (k + b < d)
-                r[b >> 2] |= (int)((uint32_t)(uint8_t)p[k + b] << (8 * (b & 3)));
+    static_assert(N >= 0 && N < 64, "vmcnt range");   // 63: no wait for loads
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier without the fence of __syncthreads(), which would wait for the requests
+// in flight.
+__device__ __forceinline__ void bar()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The 16 codes of a row p of d codes from k on, k a multiple of 16, zeros behind the row's end;
+// the row may start at any byte.  A chunk that the end cuts is read as the row's last 16 codes
+// and shifted, so that nothing outside the row is read.
+__device__ __forceinline__ i32x4_t row_chunk(const int8_t *p, int k, int d)
+{
+    i32x4_t r = {0, 0, 0, 0};
+    if (k >= d)
         return r;
-    };
-    i32x4_t w[2][2], h[2][2];   // K tiles under way
-    auto fetch_tile = [&](int set, int kt) __attribute__((always_inline)) {
+    if (k + 16 <= d) {
+        __builtin_memcpy(&r, p + k, 16);
+        return r;
+    }
+    uint64_t w[2] = {0, 0};
+    if (d >= 16) {
+        __builtin_memcpy(w, p + d - 16, 16);
+        const int shift = 8 * (k + 16 - d);   // 8 .. 120 bits
+        w[0] = shift < 64 ? (w[0] >> shift) | (w[1] << (64 - shift)) : w[1] >> (shift - 64);
+        w[1] = shift < 64 ? w[1] >> shift : 0;
+    } else {
+#pragma unroll 1
+        for (int b = 0; b < d; ++b) {
+            const uint64_t c = (uint64_t)(uint8_t)p[b] << (8 * (b & 7));
+            w[0] |= b < 8 ? c : 0;
+            w[1] |= b < 8 ? 0 : c;
+        }
+    }
+    __builtin_memcpy(&r, w, 16);
+    return r;
+}
+
+// Any shape and alignment.  BM x BV outputs per workgroup of NW waves, NWV of them side by side
+// along the vocabulary; K in steps of 128 codes, fetched two steps ahead into registers with
+// 16-byte loads at any byte address and staged into LDS (rows of 128 + 16 bytes, which spreads
+// the 16-byte fragment reads over the banks).  Rows past V / rows re-read the last valid row.
+// Bound by the L1, which takes a 16-byte load at an odd address in four parts: 3000 x 32000 x
+// 4095 takes 726 to 777 us (1.05 POP/s; L1 busy 77% of the time, matrix pipes 23%), x 4100: 604
+// us, x 4096 in this form 578 us, in the aligned forms 350 us.
+template <int BM, int BV, int NW, int NWV, bool OUT_BF16>
+__global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__restrict__ Hq,
+                                                                const float *__restrict__ hs,
+                                                                const int32_t *__restrict__ count, int32_t max_rows,
+                                                                const int8_t *__restrict__ Wq,
+                                                                const float *__restrict__ ws, int32_t V, int32_t d,
+                                                                void *__restrict__ out, int64_t ldo, int32_t group_m)
+{
+    constexpr int BK = 128, CHUNKS = BK / 16, PITCH = BK + 16, STAGE = (BV + BM) * PITCH;
+    constexpr int WV = BV / NWV, WM = BM / (NW / NWV), AV = WV / 16, AM = WM / 16;
+    constexpr int RPT = 64 * NW / CHUNKS, LW = BV / RPT, LH = BM / RPT, T = LW + LH;   // rows, chunks at a time
+    __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+    const int rows = (int)rows::row_count(count, max_rows);
+    const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, nblk = nvt * nmt;
+    const int blk = blockIdx.x;
+    if (blk >= nblk)
+        return;
+    // the workgroups of one XCD take a contiguous run of tiles: of group_m row tiles, the row
+    // tiles of a vocabulary tile one after another
+    const int q8 = nblk >> 3, rem = nblk & 7, xcd = blk & 7;
+    const int t = (xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8) + (blk >> 3);
+    const int first_m = t / (group_m * nvt) * group_m, gsz = min(nmt - first_m, group_m);
+    const int local = t - first_m * nvt;
+    const int m0 = (first_m + local % gsz) * BM, v0 = local / gsz * BV;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int sr = tid / CHUNKS, sk = tid % CHUNKS * 16;   // thread's row (+ RPT j) and chunk
+    const int8_t *wbase = Wq + (int64_t)v0 * d, *hbase = Hq + (int64_t)m0 * d;
+    uint32_t off[T];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[set][i] = fetch(wp, w_ok, kt * BK + i * 64 + sk);
-            h[set][i] = fetch(hp, h_ok, kt * BK + i * 64 + sk);
+    for (int j = 0; j < T; ++j)
+        off[j] = (uint32_t)(j < LW ? min(sr + j * RPT, V - 1 - v0) : min(sr + (j - LW) * RPT, rows - 1 - m0)) * (uint32_t)d;
+    i32x4_t x[2][T];   // K tiles under way
+    auto fetch_tile = [&](int set, int kt, auto whole) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            const int8_t *p = (j < LW ? wbase : hbase) + off[j];
+            if constexpr (decltype(whole)::value)
+                __builtin_memcpy(&x[set][j], p + kt * BK + sk, 16);
+            else
+                x[set][j] = row_chunk(p, kt * BK + sk, d);
         }
     };
     auto put_tile = [&](int set, int stage) __attribute__((always_inline)) {
-        char *s = smem + stage * 128 * PITCH + sr * PITCH + sk;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            *(i32x4_t *)(s + i * 64) = w[set][i];
-            *(i32x4_t *)(s + 64 * PITCH + i * 64) = h[set][i];
-        }
+        for (int j = 0; j < T; ++j)
+            *(i32x4_t *)(smem + stage * STAGE + (sr + j * RPT) * PITCH + sk) = x[set][j];
     };
-    const int wv = (wave & 1) * 32, wm = (wave >> 1) * 32;
+    const int wv = wave % NWV * WV, wm = wave / NWV * WM;
     const int fr = lane & 15, kg = lane >> 4;
-    i32x4_t acc[2][2];
+    i32x4_t acc[AV][AM];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < AV; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < AM; ++b)
             acc[a][b] = i32x4_t{0, 0, 0, 0};
     const int nk = (d + BK - 1) / BK;
     // K tile kt from stage P = kt % 2, which held kt - 2 before; kt + 2 is fetched meanwhile
-    auto step = [&](auto parity, int kt) __attribute__((always_inline)) {
+    // (whole: it ends inside the row; past the row's end: zeros, unused)
+    auto step = [&](auto parity, int kt, auto whole) __attribute__((always_inline)) {
         constexpr int P = decltype(parity)::value;
-        fetch_tile(P, kt + 2);   // past the end: zeros, unused
-        const char *s = smem + P * 128 * PITCH;
+        fetch_tile(P, kt + 2, whole);
+        const char *s = smem + P * STAGE;
 #pragma unroll
         for (int q = 0; q < BK / 64; ++q) {
-            i32x4_t af[2], bf[2];
+            i32x4_t af[AV], bf[AM];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a < AV; ++a)
                 af[a] = *(const i32x4_t *)(s + (wv + a * 16 + fr) * PITCH + q * 64 + kg * 16);
-                bf[a] = *(const i32x4_t *)(s + (64 + wm + a * 16 + fr) * PITCH + q * 64 + kg * 16);
-            }
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int b = 0; b < AM; ++b)
+                bf[b] = *(const i32x4_t *)(s + (BV + wm + b * 16 + fr) * PITCH + q * 64 + kg * 16);
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+            for (int a = 0; a < AV; ++a)
+#pragma unroll
+                for (int b = 0; b < AM; ++b)
                     acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[a], bf[b], acc[a][b], 0, 0, 0);
         }
         put_tile(1 - P, 1 - P);   // last read two steps ago, a barrier in between
-        __syncthreads();
+        wait_vm<63>();   // (the LDS accesses; K tile kt + 2 stays under way)
+        bar();
     };
-    fetch_tile(0, 0);
-    fetch_tile(1, 1);
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    fetch_tile(0, 0, std::false_type{});
+    fetch_tile(1, 1, std::false_type{});
     put_tile(0, 0);
-    __syncthreads();
-    for (int kt = 0; kt < nk; kt += 2) {
-        step(std::integral_constant<int, 0>{}, kt);
+    wait_vm<63>();
+    bar();
+    int kt = 0;
+    for (; (kt + 4) * BK <= d; kt += 2) {
+        step(even, kt, std::true_type{});
+        step(odd, kt + 1, std::true_type{});
+    }
+    for (; kt < nk; kt += 2) {
+        step(even, kt, std::false_type{});
         if (kt + 1 < nk)
-            step(std::integral_constant<int, 1>{}, kt + 1);
+            step(odd, kt + 1, std::false_type{});
     }
     // lane (fr, kg) holds entries 4 kg .. 4 kg + 3 of a 16-entry block for row fr of a 16-row block
     const bool vec = OUT_BF16 ? ((uintptr_t)out & 7) == 0 && (ldo & 3) == 0
                               : ((uintptr_t)out & 15) == 0 && (ldo & 3) == 0;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < AM; ++b) {
         const int row = m0 + wm + b * 16 + fr;
         if (row >= rows)
             continue;
         const float hsc = hs[row];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < AV; ++a) {
             const int v = v0 + wv + a * 16 + kg * 4;
             if (v >= V)
                 continue;
-            float x[4];
+            float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x[e] = (float)acc[a][b][e] * hsc * ws[min(v + e, V - 1)];
-            store4<OUT_BF16>(out, (int64_t)row * ldo + v, x, v, V, vec);
+                y[e] = (float)acc[a][b][e] * hsc * ws[min(v + e, V - 1)];
+            store4<OUT_BF16>(out, (int64_t)row * ldo + v, y, v, V, vec);
         }
     }
 }
@@ -175,23 +232,6 @@ __device__ __forceinline__ void request(const void *src, void *lds)
 __device__ __forceinline__ void request4(const void *src, void *lds)
 {
     __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 4, 0, 0);
-}
-
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_vm()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
-}
-
-// Workgroup barrier without the fence of __syncthreads(), which would wait for the requests
-// in flight.
-__device__ __forceinline__ void bar()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
 }
 
 // What a request past the end of a row reads (rows whose d is no multiple of the K tile).
@@ -696,7 +736,11 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 
 // Which form runs, from the sizes and the alignment alone (times of one launch on an MI355X,
 // bf16 output; the forms give the same bits):
-//  * codes that are not 16-byte aligned rows (d % 16 != 0): gemm_int8_any_kernel.
+//  * codes that are not 16-byte aligned rows (d % 16 != 0): gemm_int8_any_kernel, in tiles of
+//    32 x 128 (20 x 152064 x 3583: 141 us, 153 in tiles of 32 x 64, 189 of 64 x 64), 64 x 128 (64 x
+//    152064 x 3585: 163 us, 188 of 64 x 64, 192 of 128 x 128), or 128 x 128 where these fill more
+//    than half of the chip (1000 x 50000 x 2001: 241 us, 347 of 64 x 64; 200 x 8192 x 4095, 128
+//    tiles: 45 against 39 us).
 //  * at most 32 rows, at most 64 rows: W is streamed once past a row tile of 32 or 64 rows.
 //    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 106 us with tiles of 128 rows; 64 rows:
 //    109 against 108 us, but 48 rows 104 against 105, 33 rows 96 against 108.  Vocabulary tiles
@@ -728,7 +772,17 @@ hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *co
     auto pick = [&](auto bf16_tag) {
         constexpr bool B = decltype(bf16_tag)::value;
         if (d % 16 != 0 || ((uintptr_t)Hq & 15) || ((uintptr_t)Wq & 15))
-            return go(gemm_int8_any_kernel<B>, tiles(64, 64), 256);
+        {
+            if (rows <= 32 && tiles(32, 128) >= cus)
+                return go(gemm_int8_any_kernel<32, 128, 4, 4, B>, tiles(32, 128), 256, kDefaultGroupM);
+            if (rows <= 32)
+                return go(gemm_int8_any_kernel<32, 64, 4, 4, B>, tiles(32, 64), 256, kDefaultGroupM);
+            if (rows <= 64 && tiles(64, 128) >= cus)
+                return go(gemm_int8_any_kernel<64, 128, 4, 4, B>, tiles(64, 128), 256, kDefaultGroupM);
+            if (rows <= 64 || tiles(128, 128) * 8 < cus * 5)
+                return go(gemm_int8_any_kernel<64, 64, 4, 2, B>, tiles(64, 64), 256, kDefaultGroupM);
+            return go(gemm_int8_any_kernel<128, 128, 8, 4, B>, tiles(128, 128), 512, kDefaultGroupM);
+        }
         if (rows <= 32 && tiles(32, 128) >= cus)
             return go(gemm_int8_small_kernel<32, 128, 1, 4, true, B>, tiles(32, 128), 256);
         if (rows <= 32)

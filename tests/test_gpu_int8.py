@@ -61,11 +61,15 @@ def test_int8_few_rows(m, M, V, d):
     (300, 25601, 16), (300, 25601, 272), (300, 25603, 1040),     # ... that the depth does not fill
     (1100, 25600, 128), (1100, 25600, 400),                      # ... several tiles per workgroup
     (16484, 600, 128), (16484, 600, 304),                        # ... row tiles past a full super-group
+    (20, 40001, 259), (32, 33000, 1), (17, 9001, 4099),          # unaligned rows: tiles of 32 rows
+    (50, 40001, 259), (64, 33000, 15), (64, 33003, 513),         # ... 64 x 128 tiles
+    (300, 7003, 1031), (65, 20000, 17),                          # ... 64 x 64 tiles
+    (500, 20000, 515), (130, 33000, 15), (130, 33001, 17), (1300, 2500, 129), (1300, 2501, 127),   # ... 128 x 128 tiles
 ])
 def test_int8_large_tiles(m, M, V, d):
     hq, hs = _codes(M, M, d)
     wq, ws = _codes(V, V, d)
-    rows = torch.tensor(sorted({0, 1, 63, 64, 255 % M, 256 % M, M // 2, M - 65, M - 2, M - 1}), device=DEV)
+    rows = torch.tensor(sorted({0, 1, 63 % M, 64 % M, 255 % M, 256 % M, M // 2, max(M - 65, 0), M - 2, M - 1}), device=DEV)
     for out_dtype in (BF, F32):
         out = torch.full((M + 1, V), 7.0, dtype=out_dtype, device=DEV)
         got = m.mosaic_quantized_logits(hq, hs, wq, ws, out=out)
@@ -92,7 +96,8 @@ def test_int8_largest_sums(m):
 
 
 @pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100), (300, 11000, 256), (90, 17000, 128),
-                                   (300, 25600, 256), (120, 25600, 256), (200, 33000, 128)])
+                                   (300, 25600, 256), (120, 25600, 256), (200, 33000, 128), (500, 20000, 131),
+                                   (50, 33000, 33)])
 def test_int8_device_count(m, M, V, d):
     hq, hs = _codes(1, M, d)
     wq, ws = _codes(2, V, d)
@@ -106,7 +111,7 @@ def test_int8_device_count(m, M, V, d):
             assert torch.equal(out[:n], want[:n]) and bool((out[n:] == 5).all()), cnt
 
 
-@pytest.mark.parametrize("M,V,d,off", [(30, 500, 128, 1), (30, 500, 128, 8), (300, 700, 256, 5), (9, 100, 33, 3)])
+@pytest.mark.parametrize("M,V,d,off", [(30, 500, 128, 1), (30, 500, 128, 8), (300, 700, 256, 5), (9, 100, 33, 3), (300, 20000, 144, 3), (50, 33000, 128, 1)])
 def test_int8_unaligned_codes(m, M, V, d, off):
     hq, hs = _codes(1, M, d)
     wq, ws = _codes(2, V, d)
