@@ -520,7 +520,9 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const Distill a, int sl
                 barrier_after_stores();
                 fix_entries<BF16, NT>(a, t, row, 0, V, f);
             } else {
-                part_grad<BF16, NT, false>(a, t, row, 0, V, x);
+                // the row's second and last read, out of the Infinity Cache: with the streaming
+                // policy, reads and stores leave it to the rows under way
+                part_grad<BF16, NT, true>(a, t, row, 0, V, x);
             }
         }
         __syncthreads();   // the teacher's arrays are refilled for the next row
@@ -737,10 +739,15 @@ int parts_of(int64_t rows, int64_t V)
     return (int)std::max<int64_t>(1, std::min<int64_t>({64, 2048 / std::max<int64_t>(rows, 1), V / 4096}));
 }
 
-// Few rows of many logits go over several workgroups each.  20 x 152064 bf16, the loss: 11 us
-// in two launches against 20 us with a workgroup per row; 129 x 126464, loss and gradient: as
-// fast either way.
-bool is_split(int64_t rows, int64_t V, bool grad) { return rows <= (grad ? 128 : 1024) && V >= 16384; }
+// Few rows of many logits go over several workgroups each: for the gradient from 16384 logits
+// on (129 x 126464, loss and gradient: as fast either way), for the loss alone, two launches
+// against one, where a row passes 400 KB
+// (20 x 524288 bf16: 16 against 39 us; 20 x 152064: 16.0 against 15.7 us, 20 x 100000 fp32: 15.4
+// against 14.0; 256 x 262144: 34 against 29).
+bool is_split(int64_t rows, int64_t V, bool bf16, bool grad)
+{
+    return rows <= 128 && (grad ? V >= 16384 : V * (bf16 ? 2 : 4) > 409600);
+}
 
 // Logits that cannot stay in the 256 MB Infinity Cache are read and written with the streaming
 // cache policy: 4096 x 126464 bf16, loss and gradient: 435 against 463 us, the gradient alone
@@ -760,18 +767,22 @@ constexpr int kStreamChunks[3] = {BF16 ? 13 : 10, BF16 ? 17 : 15, 20};
 //  * up to 2048 logits: a wave per row.  Up to 8192: a wave per row where there are rows enough
 //    for several waves per SIMD, else four waves (8000 x 8000, loss and gradient: 56 against
 //    60 us; the loss alone 31 against 46 us).
+//  * the loss alone of longer rows: 4 waves per row, 8 up to three rows per CU, 16 up to one
+//    (126464 logits: 256 rows 16 us with 16 waves, 18 with 8, 27 with 4; 512 rows 30, 26, 31; 850
+//    rows 53, 44, 42).
 //  * up to 65536: 4 or 8 waves per row, several rows on a CU.  4000 x 20000: 72 us with 4 waves,
 //    88 us with 8, 105 us through the stream form; 2000 x 50000: 90 us with 8, 97 us there.
 //  * longer: the stream form, a row at a time on each CU, up to what its registers hold, 153600
 //    bf16 logits (4096 x 126464: 419 us; without the reads of the next row beside the writes of
 //    this one 475 us).
-//  * longer still: the row is read twice.
+//  * longer still: the row is read twice (2000 x 200000: 338 us, 375 us without the streaming
+//    policy in the second pass).
 template <bool BF16>
 hipError_t run(const Distill &a, hipStream_t stream)
 {
     const int slots = table_slots(a.K);
     const size_t lds = teacher_bytes(a.K);
-    if (is_split(a.rows, a.V, a.grad)) {
+    if (is_split(a.rows, a.V, BF16, a.grad)) {
         const int parts = parts_of(a.rows, a.V), cuts = a.grad ? parts : 1;
         float *z_at = a.partials + 2 * a.rows * parts;
         hipLaunchKernelGGL(distill_part_kernel<BF16>, dim3((unsigned)(a.rows * parts)), dim3(kPartThreads), 0, stream,
@@ -784,10 +795,10 @@ hipError_t run(const Distill &a, hipStream_t stream)
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(threads), lds, stream, a,
                            slots);
     };
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess)
+        (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     auto rows_per_cu = [&](auto kernel, auto kernel_large) {
-        int dev = 0, cus = 256;
-        if (hipGetDevice(&dev) == hipSuccess)
-            (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
         const dim3 grid((unsigned)std::min<int64_t>(a.rows, cus));
         if (is_large<BF16>(a))
             hipLaunchKernelGGL(kernel_large, grid, dim3(1024), 2 * lds, stream, a, slots, (int)(lds / 4));
@@ -800,8 +811,12 @@ hipError_t run(const Distill &a, hipStream_t stream)
         rows(distill_row_kernel<BF16, 64, 4 * B>, 64);
     else if (!a.grad && many && a.V <= 16384)
         rows(distill_row_kernel<BF16, 64, 0>, 64);
-    else if (!a.grad)
+    else if (!a.grad && (a.rows > 3 * cus || a.V <= 32768))
         rows(distill_row_kernel<BF16, 256, 0>, 256);
+    else if (!a.grad && a.rows > cus)
+        rows(distill_row_kernel<BF16, 512, 0>, 512);
+    else if (!a.grad)
+        rows(distill_row_kernel<BF16, 1024, 0>, 1024);
     else if (BF16 && many && a.V <= 8192)
         rows(distill_row_kernel<BF16, 64, BF16 ? 16 : 4 * B>, 64);
     else if (a.V <= 8192)
@@ -872,7 +887,9 @@ hipError_t run_grad(const Distill &a, hipStream_t stream)
 
 int64_t distill_workspace_bytes(int64_t rows, int64_t V, int64_t K)
 {
-    return is_split(rows, V, false) ? 4 * rows * (2 * parts_of(rows, V) + K) : 0;
+    // whichever type and direction the call has: what is split as bf16 is split as fp32
+    const bool split = is_split(rows, V, false, false) || is_split(rows, V, false, true);
+    return split ? 4 * rows * (2 * parts_of(rows, V) + K) : 0;
 }
 
 hipError_t launch_distill(const Distill &a, bool z_bf16, hipStream_t stream)

@@ -55,7 +55,8 @@ def test_distill_sizes(m, M, V, K, dtype):
 # row counts and lengths on both sides of each form's limits
 FORMS = [(200, 2047), (200, 2049), (2100, 2048), (2050, 8192), (150, 8191), (140, 8193), (130, 16384), (130, 16385),
          (130, 32768), (130, 32769), (129, 38401), (129, 57601), (129, 65536), (129, 65537), (129, 76801),
-         (129, 99841), (129, 130561), (129, 153600), (129, 153601), (2049, 4097), (1025, 16400), (300, 126464)]
+         (129, 99841), (129, 130561), (129, 153600), (129, 153601), (2049, 4097), (1025, 16400), (300, 126464),
+         (128, 102400), (128, 102401), (40, 204800), (40, 204801), (257, 32800), (768, 32769), (769, 32769), (200, 210000)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
