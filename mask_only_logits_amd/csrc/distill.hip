@@ -14,7 +14,8 @@
 // rounded once, to the logits' type.
 //
 // HBM bounds both directions: the loss reads the logits once, the gradient reads and writes
-// them.
+// them.  1229 x 126464 bf16, loss and gradient: 131 us (4.75 TB/s, a large copy's rate); 4096 x
+// 126464, the gradient alone: 369 us (5.6 TB/s).
 //  * distill_row_kernel: a workgroup per row.  Loss and gradient together keep the row in
 //    registers between the two, so the logits are read once.
 //  * distill_part_kernel, distill_split_kernel: rows split over several workgroups, for few

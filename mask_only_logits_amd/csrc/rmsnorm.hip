@@ -145,7 +145,7 @@ __device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f
 
 // One row per WPR waves, a thread holding CH chunks of 16 bytes (d <= 64 WPR CH kChunk).
 // NORM off: y = x (plain quantization).  STREAM: streaming cache policy.
-// Bound: HBM.  32768 x 4096 bf16 with residual, sum, out and codes moves 1.21 GB in 187 us, 6.4
+// Bound: HBM.  32768 x 4096 bf16 with residual, sum, out and codes moves 1.21 GB in 185 us, 6.5
 // TB/s (a large copy runs at 4.75); 1229 gathered rows to codes alone take 8.5 us, where the
 // chain of row id, row, two reductions and store counts.
 template <bool BF16, bool GAIN_BF16, bool NORM, int WPR, int CH, bool STREAM>
