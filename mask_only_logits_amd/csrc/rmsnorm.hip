@@ -143,21 +143,33 @@ struct Gain {
 // Power of two that keeps top / amax inside fp32 for the smallest rows (1 for all others).
 __device__ __forceinline__ float code_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
 
-// One row per WPR waves, a thread holding CH chunks of 16 bytes (d <= 64 WPR CH kChunk).
+// Reduction over the LPR threads of a row: lanes of a wave, or a workgroup's waves.
+template <int LPR, typename Op>
+__device__ __forceinline__ float row_reduce(float v, Op op, float *red)
+{
+    if constexpr (LPR > 64)
+        return block_reduce<LPR / 64>(v, op, red);
+#pragma unroll
+    for (int o = LPR / 2; o >= 1; o >>= 1)
+        v = op(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// LPR threads per row, a thread holding CH chunks of 16 bytes (d <= LPR CH kChunk): lanes of a
+// wave, which then has 64 / LPR rows, or whole waves.
 // NORM off: y = x (plain quantization).  STREAM: streaming cache policy.
 // Bound: HBM.  32768 x 4096 bf16 with residual, sum, out and codes moves 1.21 GB in 185 us, 6.5
 // TB/s (a large copy runs at 4.75); 1229 gathered rows to codes alone take 8.5 us, where the
 // chain of row id, row, two reductions and store counts.
-template <bool BF16, bool GAIN_BF16, bool NORM, int WPR, int CH, bool STREAM>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(const RowsNorm a)
+template <bool BF16, bool GAIN_BF16, bool NORM, int LPR, int CH, bool STREAM>
+__global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const RowsNorm a)
 {
-    constexpr int RPB = WPR == 1 ? 4 : 1;   // rows per workgroup
-    constexpr int N = kChunk<BF16>, STEP = 64 * WPR * N;
-    __shared__ float red[WPR];
-    const int t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
+    constexpr int RPB = LPR <= 64 ? 256 / LPR : 1;   // rows per workgroup
+    constexpr int N = kChunk<BF16>, STEP = LPR * N;
+    __shared__ float red[LPR <= 64 ? 1 : LPR / 64];
+    const int t = threadIdx.x % LPR;
     const int64_t n = row_count(a.count, a.rows);
-    for (int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? threadIdx.x >> 6 : 0); row < n;
-         row += (int64_t)gridDim.x * RPB) {
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < n; row += (int64_t)gridDim.x * RPB) {
         const int64_t src = a.row_idx ? (int64_t)a.row_idx[row] : row;
         const bool inside = src >= 0 && src < a.nsrc;   // a row id outside gives a row of NaN
         float v[CH][N];
@@ -209,7 +221,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     ss += v[c][i] * v[c][i];
-            ss = block_reduce<WPR>(ss, AddOp{}, red);
+            ss = row_reduce<LPR>(ss, AddOp{}, red);
             float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
             if (__builtin_isinf(ss)) {
                 // the squares of finite values passed fp32's range: take them 2^-80 smaller
@@ -221,7 +233,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
                     for (int i = 0; i < N; ++i)
                         s2 += (v[c][i] * down) * (v[c][i] * down);
-                s2 = block_reduce<WPR>(s2, AddOp{}, red);
+                s2 = row_reduce<LPR>(s2, AddOp{}, red);
                 rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
             }
 #pragma unroll
@@ -245,7 +257,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_norm_kernel(co
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 amax = MaxBitsOp{}(amax, abs_bits(v[c][i]));
-        amax = block_reduce<WPR>(amax, MaxBitsOp{}, red);
+        amax = row_reduce<LPR>(amax, MaxBitsOp{}, red);
         const float top = a.code_int8 ? 127.0f : 448.0f;
         // a row with a NaN or an infinity has zero codes and that scale, so that what is
         // computed from it is not finite either
@@ -334,7 +346,7 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
     }
 }
 
-// Workgroups of a launch: one for each row (or four), and no more than 2^20, over which the
+// Workgroups of a launch: one for each row (or 4 to 32), and no more than 2^20, over which the
 // kernels walk: a launch holds at most 2^32 - 1 threads.
 unsigned grid_of(int64_t rows, int per_block)
 {
@@ -352,40 +364,65 @@ bool is_large(const RowsNorm &a, int64_t esize)
 }
 
 // CH: chunks of eight elements per thread
-template <bool BF16, bool NORM, int WPR, int CH>
+template <bool BF16, bool NORM, int LPR, int CH>
 void run(const RowsNorm &a, hipStream_t stream)
 {
     constexpr int C = CH * 8 / kChunk<BF16>;
-    const dim3 grid(grid_of(a.rows, WPR == 1 ? 4 : 1)), block(WPR == 1 ? 256 : 64 * WPR);
+    const dim3 grid(grid_of(a.rows, LPR <= 64 ? 256 / LPR : 1)), block(LPR <= 64 ? 256 : LPR);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
     if (NORM && is_large(a, BF16 ? 2 : 4))
-        a.gain_bf16 ? go(rows_norm_kernel<BF16, true, NORM, WPR, C, NORM>)
-                    : go(rows_norm_kernel<BF16, false, NORM, WPR, C, NORM>);
+        a.gain_bf16 ? go(rows_norm_kernel<BF16, true, NORM, LPR, C, NORM>)
+                    : go(rows_norm_kernel<BF16, false, NORM, LPR, C, NORM>);
     else
-        a.gain_bf16 || !NORM ? go(rows_norm_kernel<BF16, true, NORM, WPR, C, false>)
-                             : go(rows_norm_kernel<BF16, !NORM, NORM, WPR, C, false>);
+        a.gain_bf16 || !NORM ? go(rows_norm_kernel<BF16, true, NORM, LPR, C, false>)
+                             : go(rows_norm_kernel<BF16, !NORM, NORM, LPR, C, false>);
 }
 
-// Waves per row and chunks per thread, by the row's length: enough waves for short rows to
-// finish soon, few enough that several rows share a CU and one's reductions lie under the
-// others' reads (bf16, residual, sum, out and codes: 16384 x 8192: 182 us with 8 waves, 285 us
-// with 16; 32768 x 4096: 187 us with 4, 238 us with 8; 65536 x 2048, no codes: 169 us with 2 or
-// 4, 173 us with 1).
+// Threads per row and chunks per thread, by the row's length: enough threads for the row to
+// finish soon, few enough that several rows share a wave or a CU and one's reductions lie under
+// the others' reads (bf16, residual, sum, out and codes: 16384 x 8192: 182 us with 512 threads,
+// 285 us with 1024; 32768 x 4096: 187 us with 256, 238 us with 512; 131072 x 127: 54 us with 16,
+// 148 us with 64; 131072 x 64: 14 us with 8, 63 us with 64).  Three chunks where two would leave
+// many threads without one (bf16: 131072 x 260: 79 us with 16 threads, 139 us with 64; 131072 x
+// 700: 173 us with 32, 198 us with 64; 32768 x 1100: 85 us with 64, 98 us with 128; 32768 x 2500:
+// 152 us with 128, 175 us with 256; 32768 x 4097: 265 us with 256, 286 us with 512; but 32768 x
+// 3000: 153 us with 128, 146 us with 256); in fp32, whose chunks of eight are two loads, only the
+// last of these gains (381 against 407 us).
 template <bool BF16, bool NORM>
 void pick(const RowsNorm &a, hipStream_t stream)
 {
+    if (a.d <= 64)
+        return run<BF16, NORM, 8, 1>(a, stream);
+    if (a.d <= 128)
+        return run<BF16, NORM, 16, 1>(a, stream);
+    if constexpr (BF16) {
+        if (a.d <= 192)
+            return run<BF16, NORM, 8, 3>(a, stream);
+        if (a.d > 256 && a.d <= 384)
+            return run<BF16, NORM, 16, 3>(a, stream);
+        if (a.d > 512 && a.d <= 768)
+            return run<BF16, NORM, 32, 3>(a, stream);
+        if (a.d > 1024 && a.d <= 1536)
+            return run<BF16, NORM, 64, 3>(a, stream);
+        if (a.d > 2048 && a.d <= 2560)
+            return run<BF16, NORM, 128, 3>(a, stream);
+    }
+    if (a.d <= 256)
+        return run<BF16, NORM, 32, 1>(a, stream);
     if (a.d <= 512)
-        return run<BF16, NORM, 1, 1>(a, stream);
+        return run<BF16, NORM, 64, 1>(a, stream);
     if (a.d <= 1024)
-        return run<BF16, NORM, 1, 2>(a, stream);
+        return run<BF16, NORM, 64, 2>(a, stream);
     if (a.d <= 2048)
-        return run<BF16, NORM, 2, 2>(a, stream);
+        return run<BF16, NORM, 128, 2>(a, stream);
     if (a.d <= 4096)
-        return run<BF16, NORM, 4, 2>(a, stream);
+        return run<BF16, NORM, 256, 2>(a, stream);
+    if (a.d <= 6144)
+        return run<BF16, NORM, 256, 3>(a, stream);
     if (a.d <= 8192)
-        return run<BF16, NORM, 8, 2>(a, stream);
+        return run<BF16, NORM, 512, 2>(a, stream);
     if (a.d <= 16384)
-        return run<BF16, NORM, 8, 4>(a, stream);
+        return run<BF16, NORM, 512, 4>(a, stream);
     hipLaunchKernelGGL((rows_norm_long_kernel<BF16, NORM>), dim3(grid_of(a.rows, 1)), dim3(1024), 0, stream, a);
 }
 

@@ -25,7 +25,8 @@ def _data(seed, n, d, dtype, gain_dtype=None):
 
 # widths at and around each form's limits, aligned and not
 WIDTHS = [1, 2, 7, 8, 63, 64, 65, 504, 512, 513, 520, 1021, 1024, 1032, 2040, 2048, 2049, 2056, 3584, 4096, 4104,
-          8192, 8193, 8200, 16384, 16392, 20001]
+          8192, 8193, 8200, 16384, 16392, 20001, 127, 128, 129, 191, 192, 193, 256, 257, 383, 384, 385, 767, 768, 769,
+          1025, 1535, 1536, 1537, 2559, 2560, 2561, 4097, 6143, 6144, 6145]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -38,6 +39,27 @@ def test_norm_widths(m, d, dtype):
         plain64.check_norm(s, ws, "sum")
         plain64.check_norm(y, wy, "out")
         plain64.check_codes(q, sc, wy, code == m.MOSAIC_INT8, "codes")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [1, 64, 65, 128, 150, 192, 255, 384, 700])
+def test_norm_narrow_rows_share_a_wave(m, d, dtype):
+    # each row as if it were alone, whatever its neighbours hold, at counts that end inside a wave
+    x, r, gain = _data(d, 1003, d, dtype)
+    r[5::7] = float("nan")
+    r[6::11] = torch.finfo(dtype).max
+    for rows in (1, 2, 9, 33, 1003):
+        idx = torch.randperm(1003, generator=torch.Generator().manual_seed(rows))[:rows].to(torch.int32).to(DEV)
+        got = m.mosaic_add_rmsnorm(x, gain, residual=r, row_idx=idx, store_sum=True, code=m.MOSAIC_INT8)
+        for i in sorted({0, rows // 3, rows // 2, rows - 1}):
+            alone = m.mosaic_add_rmsnorm(x, gain, residual=r, row_idx=idx[i:i + 1], store_sum=True, code=m.MOSAIC_INT8)
+            for a, b in zip(got, alone):
+                assert torch.equal(a[i:i + 1].nan_to_num(7.0), b.nan_to_num(7.0))
+        fine = ~torch.isnan(r[idx.long()]).any(1) & (r[idx.long()].abs() < 1e30).all(1)
+        ws, wy = plain64.norm(x, r, gain, 1e-6, idx)
+        keep = fine.to(wy.device)
+        plain64.check_norm(got[1][fine], wy[keep], "out")
+        plain64.check_codes(got[2][fine], got[3][fine], wy[keep], True, "codes")
 
 
 @pytest.mark.parametrize("dtype,gain_dtype", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
@@ -55,7 +77,7 @@ def test_norm_gathered(m, rows, dtype, gain_dtype):
     plain64.check_codes(q, sc, plain64.norm(x, None, gain, 1e-6, idx)[1], False, "codes alone")
 
 
-@pytest.mark.parametrize("d", [256, 4096, 1000, 1023, 9000])
+@pytest.mark.parametrize("d", [256, 4096, 1000, 1023, 9000, 50, 150, 2500, 5000])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_norm_strides_and_in_place(m, d, dtype):
     x, r, gain = _data(d, 9, d + 24, dtype)
@@ -76,7 +98,7 @@ def test_norm_strides_and_in_place(m, d, dtype):
             assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("d", [512, 4096, 1001, 10000])
+@pytest.mark.parametrize("d", [512, 4096, 1001, 10000, 40, 100, 150, 250, 300])
 def test_norm_special_rows(m, d):
     x = torch.randn(8, d, device=DEV)
     x[0] = 0
