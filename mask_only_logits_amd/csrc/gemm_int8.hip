@@ -92,13 +92,14 @@ __device__ __forceinline__ i32x4_t row_chunk(const int8_t *p, int k, int d)
 }
 
 // Any shape and alignment.  BM x BV outputs per workgroup of NW waves, NWV of them side by side
-// along the vocabulary; K in steps of 128 codes, fetched two steps ahead into registers with
+// along the vocabulary; K in steps of 128 codes, fetched SETS steps ahead into registers with
 // 16-byte loads at any byte address and staged into LDS (rows of 128 + 16 bytes, which spreads
 // the 16-byte fragment reads over the banks).  Rows past V / rows re-read the last valid row.
+// SETS: 4 for the small tiles (2 x 13433 x 5656: 20 us, 25 with 2), 2 where registers are short.
 // Bound by the L1, which takes a 16-byte load at an odd address in four parts: 3000 x 32000 x
 // 4095 takes 726 to 777 us (1.05 POP/s; L1 busy 77% of the time, matrix pipes 23%), x 4100: 604
 // us, x 4096 in this form 578 us, in the aligned forms 350 us.
-template <int BM, int BV, int NW, int NWV, bool OUT_BF16>
+template <int BM, int BV, int NW, int NWV, int SETS, bool OUT_BF16>
 __global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__restrict__ Hq,
                                                                 const float *__restrict__ hs,
                                                                 const int32_t *__restrict__ count, int32_t max_rows,
@@ -130,7 +131,8 @@ __global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__
 #pragma unroll
     for (int j = 0; j < T; ++j)
         off[j] = (uint32_t)(j < LW ? min(sr + j * RPT, V - 1 - v0) : min(sr + (j - LW) * RPT, rows - 1 - m0)) * (uint32_t)d;
-    i32x4_t x[2][T];   // K tiles under way
+    static_assert(SETS % 2 == 0, "a set of registers meets one LDS stage");
+    i32x4_t x[SETS][T];   // K tiles under way
     auto fetch_tile = [&](int set, int kt, auto whole) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < T; ++j) {
@@ -155,12 +157,12 @@ __global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__
         for (int b = 0; b < AM; ++b)
             acc[a][b] = i32x4_t{0, 0, 0, 0};
     const int nk = (d + BK - 1) / BK;
-    // K tile kt from stage P = kt % 2, which held kt - 2 before; kt + 2 is fetched meanwhile
-    // (whole: it ends inside the row; past the row's end: zeros, unused)
-    auto step = [&](auto parity, int kt, auto whole) __attribute__((always_inline)) {
-        constexpr int P = decltype(parity)::value;
-        fetch_tile(P, kt + 2, whole);
-        const char *s = smem + P * STAGE;
+    // K tile kt (kt % SETS = P) from stage kt % 2; kt + SETS is fetched meanwhile (whole: it ends
+    // inside the row; past the row's end: zeros, unused)
+    auto step = [&](auto set, int kt, auto whole) __attribute__((always_inline)) {
+        constexpr int P = decltype(set)::value;
+        fetch_tile(P, kt + SETS, whole);
+        const char *s = smem + P % 2 * STAGE;
 #pragma unroll
         for (int q = 0; q < BK / 64; ++q) {
             i32x4_t af[AV], bf[AM];
@@ -176,27 +178,36 @@ __global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__
                 for (int b = 0; b < AM; ++b)
                     acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[a], bf[b], acc[a][b], 0, 0, 0);
         }
-        put_tile(1 - P, 1 - P);   // last read in the step before, a barrier in between
-        wait_vm<63>();   // (the LDS accesses; K tile kt + 2 stays under way)
+        put_tile((P + 1) % SETS, 1 - P % 2);   // last read in the step before, a barrier in between
+        wait_vm<63>();   // (the LDS accesses; the K tiles under way stay so)
         bar();
     };
-    const std::integral_constant<int, 0> even;
-    const std::integral_constant<int, 1> odd;
-    fetch_tile(0, 0, std::false_type{});
-    fetch_tile(1, 1, std::false_type{});
+    // calls f with 0 .. SETS - 1 as constants
+    auto each_set = [&](auto f) __attribute__((always_inline)) {
+        f(std::integral_constant<int, 0>{});
+        f(std::integral_constant<int, 1>{});
+        if constexpr (SETS == 4) {
+            f(std::integral_constant<int, 2>{});
+            f(std::integral_constant<int, 3>{});
+        }
+    };
+    each_set([&](auto set) __attribute__((always_inline)) {
+        if ((set + 1) * BK <= d)
+            fetch_tile(set, set, std::true_type{});
+        else
+            fetch_tile(set, set, std::false_type{});
+    });
     put_tile(0, 0);
     wait_vm<63>();
     bar();
     int kt = 0;
-    for (; (kt + 4) * BK <= d; kt += 2) {
-        step(even, kt, std::true_type{});
-        step(odd, kt + 1, std::true_type{});
-    }
-    for (; kt < nk; kt += 2) {
-        step(even, kt, std::false_type{});
-        if (kt + 1 < nk)
-            step(odd, kt + 1, std::false_type{});
-    }
+    for (; (kt + 2 * SETS) * BK <= d; kt += SETS)
+        each_set([&](auto set) __attribute__((always_inline)) { step(set, kt + set, std::true_type{}); });
+    for (; kt < nk; kt += SETS)
+        each_set([&](auto set) __attribute__((always_inline)) {
+            if (kt + set < nk)
+                step(set, kt + set, std::false_type{});
+        });
     // lane (fr, kg) holds entries 4 kg .. 4 kg + 3 of a 16-entry block for row fr of a 16-row block
     const bool vec = OUT_BF16 ? ((uintptr_t)out & 7) == 0 && (ldo & 3) == 0
                               : ((uintptr_t)out & 15) == 0 && (ldo & 3) == 0;
@@ -743,6 +754,9 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 //    152064 x 3585: 163 us, 188 of 64 x 64, 192 of 128 x 128), or 128 x 128 where these fill more
 //    than half of the chip (1000 x 50000 x 2001: 241 us, 347 of 64 x 64; 200 x 8192 x 4095, 128
 //    tiles: 45 against 39 us).
+//  * so few outputs that 32 x 32 tiles fit on the chip at once, one on a CU: these, with more K
+//    tiles under way (100 x 700 x 8192: 16 against 24 us; unaligned, d = 8001: 23 against 41 us;
+//    20 x 4096 x 4096, 128 tiles: 9.6 against 12 us; 256 x 4096 x 4096, 1024 tiles: 23 against 15).
 //  * at most 32 rows, at most 64 rows: W is streamed once past a row tile of 32 or 64 rows.
 //    d = 3584, V = 152064, 20 rows: 86 us (6.4 TB/s), 106 us with tiles of 128 rows; 64 rows:
 //    109 against 108 us, but 48 rows 104 against 105, 33 rows 96 against 108.  Vocabulary tiles
@@ -775,16 +789,20 @@ hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *co
         constexpr bool B = decltype(bf16_tag)::value;
         if (d % 16 != 0 || ((uintptr_t)Hq & 15) || ((uintptr_t)Wq & 15))
         {
+            if (tiles(32, 32) <= cus)
+                return go(gemm_int8_any_kernel<32, 32, 4, 2, 4, B>, tiles(32, 32), 256, kDefaultGroupM);
             if (rows <= 32 && tiles(32, 128) >= cus)
-                return go(gemm_int8_any_kernel<32, 128, 4, 4, B>, tiles(32, 128), 256, kDefaultGroupM);
+                return go(gemm_int8_any_kernel<32, 128, 4, 4, 4, B>, tiles(32, 128), 256, kDefaultGroupM);
             if (rows <= 32)
-                return go(gemm_int8_any_kernel<32, 64, 4, 4, B>, tiles(32, 64), 256, kDefaultGroupM);
+                return go(gemm_int8_any_kernel<32, 64, 4, 4, 4, B>, tiles(32, 64), 256, kDefaultGroupM);
             if (rows <= 64 && tiles(64, 128) >= cus)
-                return go(gemm_int8_any_kernel<64, 128, 4, 4, B>, tiles(64, 128), 256, kDefaultGroupM);
+                return go(gemm_int8_any_kernel<64, 128, 4, 4, 4, B>, tiles(64, 128), 256, kDefaultGroupM);
             if (rows <= 64 || tiles(128, 128) * 8 < cus * 5)
-                return go(gemm_int8_any_kernel<64, 64, 4, 2, B>, tiles(64, 64), 256, kDefaultGroupM);
-            return go(gemm_int8_any_kernel<128, 128, 8, 4, B>, tiles(128, 128), 512, kDefaultGroupM);
+                return go(gemm_int8_any_kernel<64, 64, 4, 2, 4, B>, tiles(64, 64), 256, kDefaultGroupM);
+            return go(gemm_int8_any_kernel<128, 128, 8, 4, 2, B>, tiles(128, 128), 512, kDefaultGroupM);
         }
+        if (tiles(32, 32) <= cus)
+            return go(gemm_int8_small_kernel<32, 32, 2, 8, false, B>, tiles(32, 32), 256);
         if (rows <= 32 && tiles(32, 128) >= cus)
             return go(gemm_int8_small_kernel<32, 128, 1, 4, true, B>, tiles(32, 128), 256);
         if (rows <= 32)

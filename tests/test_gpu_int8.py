@@ -61,6 +61,8 @@ def test_int8_few_rows(m, M, V, d):
     (300, 25601, 16), (300, 25601, 272), (300, 25603, 1040),     # ... that the depth does not fill
     (1100, 25600, 128), (1100, 25600, 400),                      # ... several tiles per workgroup
     (16484, 600, 128), (16484, 600, 304),                        # ... row tiles past a full super-group
+    (40, 700, 8192), (40, 700, 8191), (5, 33, 5008), (250, 1000, 640),   # 32 x 32 tiles
+    (20, 9000, 512), (200, 2000, 1024), (250, 3001, 515), (250, 3001, 2064),   # few tiles of 32 x 64 and 64 x 64
     (20, 40001, 259), (32, 33000, 1), (17, 9001, 4099),          # unaligned rows: tiles of 32 rows
     (50, 40001, 259), (64, 33000, 15), (64, 33003, 513),         # ... 64 x 128 tiles
     (300, 7003, 1031), (65, 20000, 17),                          # ... 64 x 64 tiles
@@ -97,7 +99,7 @@ def test_int8_largest_sums(m):
 
 @pytest.mark.parametrize("M,V,d", [(20, 1000, 256), (40, 3000, 128), (300, 600, 512), (70, 300, 100), (300, 11000, 256), (90, 17000, 128),
                                    (300, 25600, 256), (120, 25600, 256), (200, 33000, 128), (500, 20000, 131),
-                                   (50, 33000, 33)])
+                                   (50, 33000, 33), (40, 700, 1024), (300, 2000, 1024), (300, 2000, 515)])
 def test_int8_device_count(m, M, V, d):
     hq, hs = _codes(1, M, d)
     wq, ws = _codes(2, V, d)
