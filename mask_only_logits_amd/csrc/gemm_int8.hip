@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "launch_ops.h"
 #include "row_ops.h"
 
 namespace mosaic {

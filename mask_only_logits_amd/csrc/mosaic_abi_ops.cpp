@@ -9,6 +9,7 @@
 #include "../../include/mosaic.h"
 #include "abi_common.h"
 #include "launch.h"
+#include "launch_ops.h"
 
 namespace {
 

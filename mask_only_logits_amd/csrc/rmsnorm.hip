@@ -19,7 +19,7 @@
 
 #include <algorithm>
 
-#include "launch.h"
+#include "launch_ops.h"
 #include "row_ops.h"
 
 namespace mosaic {

@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../mask_only_logits_amd/csrc/launch.h"
+#include "../../mask_only_logits_amd/csrc/launch_ops.h"
 
 namespace mosaic {
 
