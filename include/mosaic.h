@@ -436,8 +436,8 @@ mosaic_status_t mosaic_distill_topk(const void *logits, int64_t ldz, int64_t M, 
                                     void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Workspace bytes of mosaic_distill_topk for M rows over V vocabulary entries and K teacher
- * logits (0 where every row has a workgroup of its own), or -1 on a negative size or K >
- * 1024. */
+ * logits, for either type, with and without grad (0 where no such call splits rows), or -1
+ * on a negative size or K > 1024. */
 int64_t mosaic_distill_topk_workspace_bytes(int64_t M, int64_t V, int64_t K);
 
 /* The gradient alone, from the stats that mosaic_distill_topk left for the same logits and
