@@ -269,7 +269,16 @@ __device__ __forceinline__ float row_loss(const Distill &a, const Teacher &t, fl
     float x = 0.0f;
     for (int j = threadIdx.x & 63; j < a.K; j += 64)
         x += t.p[j] != 0.0f ? t.p[j] * ((t.z[j] - m) * inv - l) : 0.0f;
-    return T * T * (*t.entropy - wave_reduce(x, AddOp{}));
+    const float loss = T * T * (*t.entropy - wave_reduce(x, AddOp{}));
+    if (loss != kInf)
+        return loss;
+    // The teacher has mass where z is -inf, or so low (a mask of the type's lowest value) that
+    // z - m or its quotient by T passed fp32's range.  T times the difference need not, so it is
+    // taken in halves, with T beside p; what is infinite stays so.
+    x = 0.0f;
+    for (int j = threadIdx.x & 63; j < a.K; j += 64)
+        x += t.p[j] != 0.0f ? t.p[j] * T * (0.5f * m - 0.5f * t.z[j]) : 0.0f;
+    return T * T * (*t.entropy + l) + 2.0f * wave_reduce(x, AddOp{});
 }
 
 // The gradient of a row without teacher entries.
