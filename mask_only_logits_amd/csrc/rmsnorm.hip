@@ -222,10 +222,11 @@ __global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const 
                 for (int i = 0; i < N; ++i)
                     ss += v[c][i] * v[c][i];
             ss = row_reduce<LPR>(ss, AddOp{}, red);
-            float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
-            if (__builtin_isinf(ss)) {
-                // the squares of finite values passed fp32's range: take them 2^-80 smaller
-                // (2^128 and d < 2^31 terms then stay inside), where eps no longer counts
+            const float mean = ss / (float)a.d + a.eps;
+            float rstd = 1.0f / sqrtf(mean);
+            if (__builtin_isinf(mean)) {
+                // the squares of finite values, or eps beside them, passed fp32's range: take all
+                // of it 2^-160 smaller (2^128 and d < 2^31 terms then stay inside)
                 constexpr float down = 0x1p-80f;
                 float s2 = 0.0f;
 #pragma unroll
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const 
                     for (int i = 0; i < N; ++i)
                         s2 += (v[c][i] * down) * (v[c][i] * down);
                 s2 = row_reduce<LPR>(s2, AddOp{}, red);
-                rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
+                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps * down * down) * down;
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -306,8 +307,9 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
                 ss += x * x;
             }
             ss = block_reduce<16>(ss, AddOp{}, red);
-            rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
-            if (__builtin_isinf(ss)) {   // as in rows_norm_kernel
+            const float mean = ss / (float)a.d + a.eps;
+            rstd = 1.0f / sqrtf(mean);
+            if (__builtin_isinf(mean)) {   // as in rows_norm_kernel
                 constexpr float down = 0x1p-80f;
                 float s2 = 0.0f;
                 for (int k = threadIdx.x; k < a.d; k += 1024) {
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
                     s2 += x * x;
                 }
                 s2 = block_reduce<16>(s2, AddOp{}, red);
-                rstd = 1.0f / sqrtf(s2 / (float)a.d) * down;
+                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps * down * down) * down;
             }
         }
         auto normed = [&](float x, int k) { return NORM ? x * rstd * load1(a.gain, k, a.gain_bf16) : x; };

@@ -25,6 +25,21 @@ def _data(seed, n, d, dtype):
     return x.to(DEV), r.to(DEV), (1 + 0.2 * torch.randn(d, generator=g)).to(dtype).to(DEV)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 1000, 4096, 16384, 16385, 20001])
+def test_norm_large_eps_beside_overflowing_squares(m, d, dtype):
+    # the squares' sum, or the mean plus eps, passes fp32's range while eps still counts
+    for size, eps in ((2.0 ** 62, 1e38), (2.0 ** 62, 1e36), (1.7e19, 3e38), (1e19, 3.4e38), (3e38, 3.4e38), (1.0, 3.4e38),
+                      (2.0 ** 61, 1e-6), (2.0 ** 60, 1e33), (2.0 ** 60, 3.4e38)):
+        x = (torch.randn(3, d, generator=torch.Generator().manual_seed(d)).clamp(-1, 1) * size).to(dtype).to(DEV)
+        gain = torch.ones(d, dtype=dtype, device=DEV)
+        _, y, q, sc = m.mosaic_add_rmsnorm(x, gain, eps=eps, code=m.MOSAIC_INT8)
+        eps32 = float(torch.tensor(eps, dtype=F32))
+        want = plain64.norm(x, None, gain, eps32)[1]
+        plain64.check_norm(y, want, f"{size} with eps {eps}")
+        plain64.check_codes(q, sc, want, True, f"{size} with eps {eps}")
+
+
 LONG = [16385, 16392, 20001]
 
 
