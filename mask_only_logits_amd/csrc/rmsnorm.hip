@@ -285,6 +285,8 @@ __global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const 
 // Rows too long for the registers: the row is read again for each of the three passes (sum
 // of squares, maximum, results), from L2 after the first.  `sum` is written in the last pass,
 // each element by the thread that has read it for the last time, so that it may be X or R.
+// A thread adds up to 2^20 squares: in 64 bits, since in fp32 equal squares, whose additions all
+// round the same way, would take the row off by 114 half steps at d = 2^20, by 551 at 2^24.
 template <bool BF16, bool NORM>
 __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
 {
@@ -301,22 +303,22 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
         };
         float rstd = 1.0f;
         if constexpr (NORM) {
-            float ss = 0.0f;
+            double sum = 0.0;
             for (int k = threadIdx.x; k < a.d; k += 1024) {
                 const float x = element(k);
-                ss += x * x;
+                sum += (double)(x * x);
             }
-            ss = block_reduce<16>(ss, AddOp{}, red);
+            const float ss = block_reduce<16>((float)sum, AddOp{}, red);
             const float mean = ss / (float)a.d + a.eps;
             rstd = 1.0f / sqrtf(mean);
             if (__builtin_isinf(mean)) {   // as in rows_norm_kernel
                 constexpr float down = 0x1p-80f;
-                float s2 = 0.0f;
+                sum = 0.0;
                 for (int k = threadIdx.x; k < a.d; k += 1024) {
                     const float x = element(k) * down;
-                    s2 += x * x;
+                    sum += (double)(x * x);
                 }
-                s2 = block_reduce<16>(s2, AddOp{}, red);
+                const float s2 = block_reduce<16>((float)sum, AddOp{}, red);
                 rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps * down * down) * down;
             }
         }

@@ -40,6 +40,20 @@ def test_norm_large_eps_beside_overflowing_squares(m, d, dtype):
         plain64.check_codes(q, sc, want, True, f"{size} with eps {eps}")
 
 
+@pytest.mark.parametrize("dtype,d", [(F32, 1 << 20), (F32, (1 << 24) + 3), (BF, (1 << 24) + 3)])
+def test_norm_sums_of_very_long_rows(m, dtype, d):
+    # equal elements, so that every addition may round the same way
+    for v in (0.1, 0.3, 0.7, 1.1, 1.3, 1.7):
+        x = torch.full((1, d), v, dtype=dtype, device=DEV)
+        gain = torch.ones(d, dtype=dtype, device=DEV)
+        _, y, q, sc = m.mosaic_add_rmsnorm(x, gain, code=m.MOSAIC_INT8)
+        want = plain64.norm(x[:, :1], None, gain[:1], 1e-6)[1].to(DEV)
+        tol = want.abs() * (plain64.HALF[dtype] + plain64.NORM_REL)
+        assert bool(((y.double() - want).abs() <= tol).all()), float((y.double() / want - 1).abs().max() / plain64.U32)
+        assert bool((q == 127).all())
+        assert bool(((sc.double() * 127 / want[0] - 1).abs() <= plain64.NORM_REL).all())
+
+
 LONG = [16385, 16392, 20001]
 
 
