@@ -15,7 +15,7 @@ struct RowsNorm {
     int32_t d = 0;
     const void *gain = nullptr;         // [d]
     bool gain_bf16 = false;
-    float eps = 0.0f;
+    float eps = 0.0f, eps_low = 0.0f;   // and eps 2^-160
     const int32_t *row_idx = nullptr;   // row r of the results is source row row_idx[r] (null: r)
     const int32_t *count = nullptr;     // device-side row count (null: rows)
     int64_t rows = 0;

@@ -72,6 +72,7 @@ mosaic_status_t mosaic_add_rmsnorm(const void *X, int64_t ldx, const void *R, in
     a.gain = gain;
     a.gain_bf16 = gain_dtype == MOSAIC_BF16;
     a.eps = eps;
+    a.eps_low = eps * 0x1p-80f * 0x1p-80f;   // (2^-160 itself is no fp32 number)
     a.row_idx = row_idx;
     a.count = count;
     a.rows = rows;

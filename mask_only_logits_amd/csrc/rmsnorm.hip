@@ -222,11 +222,10 @@ __global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const 
                 for (int i = 0; i < N; ++i)
                     ss += v[c][i] * v[c][i];
             ss = row_reduce<LPR>(ss, AddOp{}, red);
-            const float mean = ss / (float)a.d + a.eps;
-            float rstd = 1.0f / sqrtf(mean);
-            if (__builtin_isinf(mean)) {
+            float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+            if (rstd == 0.0f) {
                 // the squares of finite values, or eps beside them, passed fp32's range: take all
-                // of it 2^-160 smaller (2^128 and d < 2^31 terms then stay inside)
+                // of it 2^-160 smaller, eps too (2^128 and d < 2^31 terms then stay inside)
                 constexpr float down = 0x1p-80f;
                 float s2 = 0.0f;
 #pragma unroll
@@ -235,7 +234,7 @@ __global__ __launch_bounds__(LPR <= 64 ? 256 : LPR) void rows_norm_kernel(const 
                     for (int i = 0; i < N; ++i)
                         s2 += (v[c][i] * down) * (v[c][i] * down);
                 s2 = row_reduce<LPR>(s2, AddOp{}, red);
-                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps * down * down) * down;
+                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps_low) * down;
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -309,9 +308,8 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
                 sum += (double)(x * x);
             }
             const float ss = block_reduce<16>((float)sum, AddOp{}, red);
-            const float mean = ss / (float)a.d + a.eps;
-            rstd = 1.0f / sqrtf(mean);
-            if (__builtin_isinf(mean)) {   // as in rows_norm_kernel
+            rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+            if (rstd == 0.0f) {   // as in rows_norm_kernel
                 constexpr float down = 0x1p-80f;
                 sum = 0.0;
                 for (int k = threadIdx.x; k < a.d; k += 1024) {
@@ -319,7 +317,7 @@ __global__ __launch_bounds__(1024) void rows_norm_long_kernel(const RowsNorm a)
                     sum += (double)(x * x);
                 }
                 const float s2 = block_reduce<16>((float)sum, AddOp{}, red);
-                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps * down * down) * down;
+                rstd = 1.0f / sqrtf(s2 / (float)a.d + a.eps_low) * down;
             }
         }
         auto normed = [&](float x, int k) { return NORM ? x * rstd * load1(a.gain, k, a.gain_bf16) : x; };
