@@ -328,8 +328,8 @@ mosaic_status_t mosaic_masked_logits_fp8(const void *H, int64_t L, int64_t d, co
  *   y_k = s_k * gain[k] / sqrt(mean_k(s_k^2) + eps)
  *   sum[i, k] = s_k,  out[i, k] = y_k,
  *   q[i, k]   = RNE(y_k * (top / amax)),  scale[i] = amax / top,  amax = max_k |y_k|,
- * top = 448 (MOSAIC_E4M3) or 127 (MOSAIC_INT8).  All arithmetic is fp32; sum, out and q are
- * each rounded once, from unrounded fp32 values.  A zero row has zero codes and scale 0.
+ * top = 448 (MOSAIC_E4M3) or 127 (MOSAIC_INT8).  All arithmetic is fp32 or wider; sum, out
+ * and q are each rounded once, from unrounded fp32 values.  A zero row has zero codes and scale 0.
  *   X, R      [nsrc, d] in in_dtype (F32 or BF16), row strides ldx, ldr >= d elements.
  *   gain      [d] in gain_dtype.  2^-126 <= eps < inf: squares too small for fp32 then do
  *             not count beside it.
@@ -343,8 +343,9 @@ mosaic_status_t mosaic_masked_logits_fp8(const void *H, int64_t L, int64_t d, co
  *             itself (same pointer and stride): the residual stream is updated in place.
  *             No other overlap of outputs with inputs or each other is allowed.
  * A row holding a NaN or an infinity (or whose result does) has that scale and zero codes.
- * Any d >= 1 and element-aligned pointers; multiples of 8 elements at 16-byte aligned rows
- * take the vector form.  rows == 0: OK, nothing enqueued.  Row strides below d, a NULL
+ * Any d >= 1 and element-aligned pointers.  Elements move 16 bytes at a time from any address,
+ * those that a row's end cuts off one by one; rows of more than 16384 elements one by one, and
+ * are read two or three times.  rows == 0: OK, nothing enqueued.  Row strides below d, a NULL
  * required pointer, misalignment, sum aliasing an input with row_idx or another stride, or
  * rows > nsrc without row_idx: INVALID_ARG.  nsrc or rows of 2^31 and more, d of more than
  * 2^30: UNSUPPORTED. */
@@ -368,13 +369,15 @@ mosaic_status_t mosaic_quantize_rows_int8(const void *X, int64_t nsrc, int64_t d
  * w_scale[v] for i < n, v < V.
  *   code     MOSAIC_INT8: the sums are exact (int32), converted to fp32, multiplied by
  *            h_scale[i], then by w_scale[v]; out_dtype F32 or BF16 (round to nearest even).
- *            Any 1 <= d <= 131071; Hq, Wq of any alignment.  The fast forms take d % 128
- *            == 0 and 16-byte aligned codes.  Codes of -128 are allowed.
+ *            Any 1 <= d <= 131071; Hq, Wq of any alignment.  The fast forms take d % 16
+ *            == 0 and 16-byte aligned codes (d % 128 == 0 is the fastest).  Codes of -128
+ *            are allowed.
  *            MOSAIC_E4M3: what mosaic_masked_logits_fp8 computes from these codes, in one
  *            chunk, with its requirements: d % 128 == 0, out_dtype BF16, count NULL (else
  *            UNSUPPORTED), 16-byte aligned Hq, Wq and w_scale.
  *   Hq [M, d], Wq [V, d] codes, row-major and contiguous; h_scale float[M], w_scale float[V].
- *   count    NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.
+ *   count    NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.  The form
+ *            is chosen by M, so a count far below it takes longer than a call of that M.
  *   out      [M, V] row-major, aligned to 16 bytes.  Rows >= n are not written.
  * M == 0 or V == 0: OK, nothing enqueued.  The results do not depend on M, on count or on
  * which form runs.  More than 2^24 - 1 tiles of 64 x 64 outputs: UNSUPPORTED. */

@@ -13,9 +13,11 @@
 // number would lose bits of l when m is large.  All arithmetic is fp32; the gradient is
 // rounded once, to the logits' type.
 //
-// HBM bounds both directions: the loss reads the logits once, the gradient reads and writes
-// them.  1229 x 126464 bf16, loss and gradient: 131 us (4.75 TB/s, a large copy's rate); 4096 x
-// 126464, the gradient alone: 369 us (5.6 TB/s).
+// The loss reads the logits once, the gradient reads and writes them.  4096 x 126464 bf16, the
+// gradient alone: 369 us (5.6 TB/s, what HBM bounds); the loss alone: 167 us (6.2 TB/s).  1229 x
+// 126464, loss and gradient: 131 us (4.75 TB/s), where the gradient alone moves the same bytes in
+// 110: between a row's reads and its writes its CU goes over the registers twice with little
+// under way, and 1229 rows take five turns of 256 CUs for 4.8.
 //  * distill_row_kernel: a workgroup per row.  Loss and gradient together keep the row in
 //    registers between the two, so the logits are read once.
 //  * distill_part_kernel, distill_split_kernel: rows split over several workgroups, for few
@@ -776,7 +778,11 @@ int parts_of(int64_t rows, int64_t V)
 // on (129 x 126464, loss and gradient: as fast either way), for the loss alone, two launches
 // against one, where a row passes 400 KB
 // (20 x 524288 bf16: 16 against 39 us; 20 x 152064: 16.0 against 15.7 us, 20 x 100000 fp32: 15.4
-// against 14.0; 256 x 262144: 34 against 29).
+// against 14.0; 256 x 262144: 34 against 29).  These are calls with their launches.  Replayed in a
+// graph, where a second launch costs less, two would be faster for fewer rows or shorter ones too:
+// 20 x 152064: 8.8 against 13.6 us, 64 x 126464: 11.5 against 13.4, 20 x 32000: 8.2 against 9.7;
+// but 128 x 126464: 14.5 against 14.1.  A captured call takes the eager call's form all the same,
+// so that both give the same bits.
 bool is_split(int64_t rows, int64_t V, bool bf16, bool grad)
 {
     return rows <= 128 && (grad ? V >= 16384 : V * (bf16 ? 2 : 4) > 409600);
@@ -881,8 +887,11 @@ hipError_t run(const Distill &a, hipStream_t stream)
 // Parts of a row for the gradient alone: 12288 to 32768 logits each, so that the workgroups under
 // way cover a compact stretch of memory (4096 x 126464 bf16: 367 us in 4 parts per row, 410 us
 // in one, 423 us in 16, where the teacher is prepared too often).  Of these numbers of parts
-// the one that best fills the last round of workgroups, 8 on a CU, and the last turn of their
-// loops, 4 chunks per thread (1229 rows: 109 us in 8 parts, 117 us in 4, 121 us in 5).
+// the one that best fills the last round of workgroups, counted as 8 on a CU, and the last turn of
+// their loops, 4 chunks per thread (1229 rows: 109 us in 8 parts, 117 us in 4, 121 us in 5).  The
+// kernel's registers let 7 on a CU.  Neither count is the better model: with 7 in the rule 4096 x
+// 126464 takes 349 us instead of 375 and 1000 rows 100 instead of 106, but 1229 rows 119 instead of
+// 111 and 1600 rows 151 instead of 140; with the kernel held to 8, 0 to 3% slower (300 rows: 9%).
 int cuts_of(int64_t rows, int64_t V, int chunk)
 {
     int dev = 0, cus = 256;

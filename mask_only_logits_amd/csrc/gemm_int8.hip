@@ -97,9 +97,10 @@ __device__ __forceinline__ i32x4_t row_chunk(const int8_t *p, int k, int d)
 // 16-byte loads at any byte address and staged into LDS (rows of 128 + 16 bytes, which spreads
 // the 16-byte fragment reads over the banks).  Rows past V / rows re-read the last valid row.
 // SETS: 4 for the small tiles (2 x 13433 x 5656: 20 us, 25 with 2), 2 where registers are short.
-// Bound by the L1, which takes a 16-byte load at an odd address in four parts: 3000 x 32000 x
-// 4095 takes 726 to 777 us (1.05 POP/s; L1 busy 77% of the time, matrix pipes 23%), x 4100: 604
-// us, x 4096 in this form 578 us, in the aligned forms 350 us.
+// 3000 x 32000 x 4095 takes 726 to 777 us (1.05 POP/s; L1 busy 77% of the time, matrix pipes
+// 23%), x 4100: 604 us, x 4096 in this form 578 us, in the aligned forms 350 us.  So most of what
+// is lost to those is the form, whose smaller tiles go through registers; the rest is the L1,
+// which takes a 16-byte load at an odd address in four parts.
 template <int BM, int BV, int NW, int NWV, int SETS, bool OUT_BF16>
 __global__ __launch_bounds__(64 * NW) void gemm_int8_any_kernel(const int8_t *__restrict__ Hq,
                                                                 const float *__restrict__ hs,
@@ -773,7 +774,10 @@ __global__ __launch_bounds__(256) void gemm_int8_small_kernel(const int8_t *__re
 //  * one row tile reads W once, with the streaming cache policy: 128 x 152064 x 3584: 111 against
 //    119 us, 256 x 100000 x 2048: 69 against 75.  It holds for a smaller W too where other work
 //    has been through the caches since the last call (20 x 50000 x 4096: 42 against 48 us; right
-//    after a call that left W there, 39 against 32).
+//    after a call that left W there, 39 against 32).  Rows of 128 or 256 whose d is no multiple of
+//    128 go without it: 128 x 126464 x 4112: 130 us, 112 us for d = 4096 with it.
+//  * a device-side count does not choose: `rows` does, the capacity.  Capacity 1229, V = 126464, d =
+//    4096: 20 counted rows 136 us, 92 us in a call of 20; 128 rows 124 against 108.
 hipError_t launch_gemm_int8(const int8_t *Hq, const float *hs, const int32_t *count, int64_t rows, const int8_t *Wq,
                             const float *ws, int64_t V, int64_t d, void *out, bool out_bf16, int64_t ldo,
                             hipStream_t stream)
