@@ -147,3 +147,52 @@ def test_distill_more_rows_than_a_grid(m):
     loss, stats, grad = m.mosaic_distill_topk(z, t, ids, with_grad=True, grad_loss=w)
     device64.check_distill(z, t, ids, 1.0, w, loss, stats, grad, "both")
     device64.check_distill(z, t, ids, 1.0, w, None, None, m.mosaic_distill_topk_grad(z, t, ids, stats, grad_loss=w), "grad")
+
+
+@pytest.mark.parametrize("dtype,M,V", SHAPES + [(BF, 20, 152064), (BF, 1000, 50001), (F32, 300, 126464), (BF, 300, 200003)])
+def test_distill_exact_sums(m, dtype, M, V):
+    # T = log2(e) as fp32 holds it makes the exponentials powers of two, and whole logits down to -6
+    # below the maximum make their sums exact in any order: a chunk left out or taken twice, or a
+    # sum in fewer bits, shows beside a few half steps
+    U = device64.U32
+    T = float(torch.tensor(math.log2(math.e), dtype=F32))
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = torch.randint(-6, 1, (M, V), generator=g, device=DEV).to(dtype)
+    z[:, V // 2] = 0
+    z += torch.randint(-9, 9, (M, 1), generator=g, device=DEV).to(dtype)
+    t = torch.randint(-4, 5, (M, 8), generator=g, device=DEV).float()
+    ids = torch.randint(0, V, (M, 8), generator=g, dtype=torch.int32, device=DEV)
+    w = torch.rand(M, generator=g, device=DEV) + 0.1
+    loss, stats, grad = m.mosaic_distill_topk(z, t, ids, temperature=T, with_grad=True, grad_loss=w)
+    alone, stats2, _ = m.mosaic_distill_topk(z, t, ids, temperature=T)
+    later = m.mosaic_distill_topk_grad(z, t, ids, stats, grad_loss=w, temperature=T)
+    assert torch.equal(stats, stats2)                # the same exact sum, whatever the form
+    step = max(1, (1 << 25) // V)
+    for i in range(0, M, step):
+        r = slice(i, min(M, i + step))
+        zd = z[r].double()
+        top = zd.amax(1, keepdim=True)
+        logq = (zd - top) / T
+        l = torch.logsumexp(logq, 1, keepdim=True)
+        logq -= l
+        p = torch.softmax(t[r].double() / T, 1)
+        # the powers stand for exp(x) with an x of T's half step: 5 U at 6 below the maximum, once
+        # for the term and once for the sum; the logarithm: 4 U of l
+        assert bool(((stats[r, 1:].double() - l).abs() <= (4 * l + 6) * U).all()), i
+        lq = torch.gather(logq, 1, ids[r].long())
+        want = (T * T * (p * (p.log() - lq)).sum(1))
+        # p: 6 U of T's half step twice, a division; the terms and their sums: 20 U of each
+        size = (p * (p.log().abs() + lq.abs() + l)).sum(1) + (p * 14 * (p.log().abs() + lq.abs() + 1)).sum(1)
+        tol = T * T * U * (20 * size + 4 * l[:, 0] + 6)
+        for got in (loss, alone):
+            assert bool(((got[r].double() - want).abs() <= tol).all()), i
+        q = torch.exp(logq)
+        P = torch.zeros_like(zd).scatter_add_(1, ids[r].long(), p)
+        tg = T * w[r].double()[:, None]
+        grad_want = tg * (q - P)
+        # q: 10 U of T's half step, five roundings (and exp(l) where l is given: l's error and 4 U);
+        # P: 14 U, a division, two products, eight additions; the difference and the stored type
+        for got, extra in ((grad, 0.0), (later, 4 * l + 10)):
+            tol = tg * U * (q * (16 + extra) + P * 26) + grad_want.abs() * (device64.HALF[dtype] + 2 * U)
+            bad = (got[r].double() - grad_want).abs() > tol
+            assert not bool(bad.any()), (i, bad.nonzero()[:3].tolist())
