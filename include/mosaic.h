@@ -426,7 +426,8 @@ mosaic_status_t mosaic_masked_logits_int8(const void *H, int64_t L, int64_t d, m
  *   grad            NULL (the loss alone), or [M, V] in dtype with row stride ldg >= V: the
  *                   gradient too, in the same call.  It may be logits itself (same pointer
  *                   and stride); no other overlap is allowed.
- *   grad_loss       NULL (1) or float[M], the gradient with respect to loss.
+ *   grad_loss       NULL (1) or float[M], the gradient with respect to loss (from |T grad_loss|
+ *                   = 2^60 on, a row whose maximum passes 2^29 T may come out infinite).
  *   workspace       >= mosaic_distill_topk_workspace_bytes(M, V, K) bytes, 16-byte
  *                   aligned (NULL if that is 0); calls that overlap in time need one each.
  * Rows >= n of every output are not written.  M == 0: OK, nothing enqueued.  V == 0 with M >
