@@ -144,7 +144,8 @@ def _pack_fp4(x):
     b = torch.zeros((n, nb * 32), dtype=torch.float32, device=x.device)
     b[:, :d] = x
     b = b.view(n, nb, 32)
-    e = (torch.frexp(b.abs().amax(dim=2)).exponent - 3).clamp(-127, 127)
+    amax = b.abs().amax(dim=2)   # (a block of zeros takes the smallest scale)
+    e = torch.where(amax > 0, torch.frexp(amax).exponent - 3, -127).clamp(-127, 127)
     y = (b * torch.exp2(-e.float())[:, :, None]).abs()
     # the number of midpoints that |y| has passed (a tie goes to the even code)
     c = torch.zeros(y.shape, dtype=torch.uint8, device=x.device)
@@ -262,7 +263,8 @@ def _plain_codes(x):
     b = torch.zeros((n, nb * 32), dtype=torch.float32, device=x.device)
     b[:, :d] = x
     b = b.view(n, nb, 32)
-    e = (torch.frexp(b.abs().amax(dim=2)).exponent - 3).clamp(-127, 127).float()
+    amax = b.abs().amax(dim=2)
+    e = torch.where(amax > 0, torch.frexp(amax).exponent - 3, -127).clamp(-127, 127).float()
     y = b * torch.exp2(-e)[:, :, None]
     step = torch.where(y.abs() < 2.0, 0.5, torch.where(y.abs() < 4.0, 1.0, 2.0))
     v = (torch.round(y / step) * step).clamp(-6.0, 6.0)
@@ -355,8 +357,9 @@ def _exact_codes(x):
     """Nearest E2M1 values in units of each block's scale, that is 2^(floor(log2 max) - 2)."""
     n, d = x.shape
     x = torch.nn.functional.pad(x, (0, -d % 32)).unflatten(1, (-1, 32))
-    _, e = torch.frexp(x.abs().max(dim=2, keepdim=True).values)
-    scale = torch.ldexp(torch.ones_like(x[:, :, :1]), (e - 3).clamp(-127, 127))
+    top = x.abs().max(dim=2, keepdim=True).values
+    _, e = torch.frexp(top)
+    scale = torch.ldexp(torch.ones_like(top), torch.where(top > 0, e - 3, -127).clamp(-127, 127))
     grid = torch.tensor(_E2M1[:8], dtype=torch.float64, device=x.device)
     mid = (grid[1:] + grid[:-1]) / 2
     y = x.abs() / scale
