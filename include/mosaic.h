@@ -453,6 +453,166 @@ mosaic_status_t mosaic_distill_topk_grad(const void *logits, int64_t ldz, int64_
                                          float temperature, const int32_t *count, const float *stats,
                                          const float *grad_loss, void *grad, int64_t ldg, void *stream);
 
+/* ------------------- layer norm, MXFP4 head and log-probabilities of the masked rows --- */
+
+/* Residual addition with layer norm, as mosaic_add_rmsnorm is with the root-mean-square norm.
+ * For row i < n of the results, with j = row_idx[i] (or i when row_idx is NULL):
+ *   s_k = X[j, k] + R[j, k]                              (R NULL: s = X)
+ *   mu = mean_k(s_k),  rho = 1 / sqrt(mean_k((s_k - mu)^2) + eps)
+ *   sum[i, k] = s_k,  out[i, k] = (s_k - mu) * rho * gain[k] + bias[k],  stats[i] = (mu, rho)
+ * mu and rho are computed in fp64, the rest in fp32; sum and out are each rounded once, from
+ * unrounded values.
+ *   X, R      [nsrc, d] in in_dtype (F32 or BF16), row strides ldx, ldr >= d elements.
+ *   gain, bias  [d] in gain_dtype; NULL: 1 and 0.  2^-126 <= eps < inf.
+ *   row_idx   NULL or int32[rows], any order, repeats allowed.  A value outside [0, nsrc)
+ *             gives a row of NaN.
+ *   count     NULL (n = rows), or a device-side row count as for mosaic_add_rmsnorm.
+ *   sum, out, stats   each may be NULL, not all three.  sum is [rows, d] in in_dtype with row
+ *             stride ldsum; out is [rows, d] contiguous in in_dtype; stats is double[rows, 2].
+ *             Without row_idx, sum may be X or R itself (same pointer and stride).  No other
+ *             overlap of outputs with inputs or each other is allowed.
+ * Rows >= n of every output are not written.  A row with a NaN or an infinity is NaN.  Any
+ * d >= 1 and element-aligned pointers.  rows == 0: OK, nothing enqueued.  Errors as for
+ * mosaic_add_rmsnorm. */
+mosaic_status_t mosaic_add_layernorm(const void *X, int64_t ldx, const void *R, int64_t ldr, int64_t nsrc, int64_t d,
+                                     mosaic_dtype_t in_dtype, const void *gain, const void *bias,
+                                     mosaic_dtype_t gain_dtype, float eps, const int32_t *row_idx,
+                                     const int32_t *count, int64_t rows, void *sum, int64_t ldsum, void *out,
+                                     double *stats, void *stream);
+
+/* The gradient of mosaic_add_layernorm.  For row i < n, with j = row_idx[i] (or i), s = S[j],
+ * (mu, rho) = stats[i], xh_k = (s_k - mu) * rho and a_k = dY[i, k] * gain[k]:
+ *   dX[i, k] = rho * (a_k - mean(a) - xh_k * mean(a * xh)) + dsum[i, k]
+ *   dgain[k] = sum_{i < n} dY[i, k] * xh_k,   dbias[k] = sum_{i < n} dY[i, k]
+ * dX is the gradient with respect to s, and so to X and to R alike.  It is rounded once; the
+ * sums over rows are added in a fixed order, so results repeat bit for bit.
+ *   dY        [rows, d] in in_dtype, row stride lddy >= d.
+ *   S         [nsrc, d] in in_dtype, row stride lds >= d: the rows that were normed, that is X
+ *             (with the forward call's row_idx), or its sum output (without).
+ *   stats     double[rows, 2] from the forward call.
+ *   gain      [d] in gain_dtype; NULL: 1.
+ *   dsum      NULL or [rows, d] in in_dtype, row stride lddsum: the gradient that reaches s by
+ *             another way, the residual stream.
+ *   dX        NULL or [rows, d] in in_dtype, row stride lddx: row i belongs to result i (rows
+ *             that row_idx names twice have two gradients, to be added by the caller).  It may
+ *             be dY, dsum or, without row_idx, S itself (same pointer and stride).
+ *   dgain, dbias  NULL or float[d]; written whole, with zeros where n is 0, also by a call
+ *             with rows == 0.  One of dX, dgain and dbias has to be given.
+ *   workspace >= mosaic_layernorm_grad_workspace_bytes(rows, d) bytes, 16-byte aligned, where
+ *             dgain or dbias is given (else NULL is allowed); calls that overlap in time need
+ *             one each.
+ * A row_idx value outside [0, nsrc) gives a row of NaN, and NaN weight gradients.  Any d >= 1
+ * and element-aligned pointers; errors as for mosaic_add_rmsnorm. */
+mosaic_status_t mosaic_layernorm_grad(const void *dY, int64_t lddy, const void *S, int64_t lds, int64_t nsrc, int64_t d,
+                                      mosaic_dtype_t in_dtype, const double *stats, const void *gain,
+                                      mosaic_dtype_t gain_dtype, const int32_t *row_idx, const int32_t *count,
+                                      int64_t rows, const void *dsum, int64_t lddsum, void *dX, int64_t lddx,
+                                      float *dgain, float *dbias, void *workspace, int64_t workspace_bytes,
+                                      void *stream);
+
+/* Workspace bytes of mosaic_layernorm_grad's weight gradients, or -1 on a size that it does not
+ * take. */
+int64_t mosaic_layernorm_grad_workspace_bytes(int64_t rows, int64_t d);
+
+/* MXFP4 codes of rows (the 4-bit format of the OCP microscaling specification): each 32
+ * consecutive elements of a row are a block with one scale, a power of two.  With amax the
+ * block's largest magnitude,
+ *   e = clamp(floor(log2(amax)) - 2, -127, 127),  scale byte = e + 127 (E8M0),
+ *   code = the E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) nearest to x * 2^-e,
+ *          ties to the even code, magnitudes above 6 taken to 6.
+ * A block of zeros has scale byte 0.  A block with a NaN or an infinity has scale byte 255 (NaN)
+ * and zero codes.
+ *   X         [nsrc, d] in in_dtype (F32 or BF16), row-major and contiguous, element-aligned.
+ *   row_idx   NULL or int32[rows]; values outside [0, nsrc) give rows of NaN scales.
+ *   q         [rows, B * 16] bytes, B = ceil(d / 32), 16-byte aligned: element k of a row is in
+ *             byte k / 2, an even one in the low half; the last block is filled up with zeros.
+ *   scale     [rows, B] bytes.  q and scale may both be NULL.
+ *   values    NULL or [rows, d] in in_dtype, contiguous: what the codes stand for (exact in
+ *             either type).  Without row_idx it may be X itself.
+ * Any 1 <= d <= 2^30.  rows == 0 or d == 0: OK, nothing enqueued.  Errors as for
+ * mosaic_quantize_rows_int8. */
+mosaic_status_t mosaic_quantize_rows_mxfp4(const void *X, int64_t nsrc, int64_t d, mosaic_dtype_t in_dtype,
+                                           const int32_t *row_idx, int64_t rows, uint8_t *q, uint8_t *scale,
+                                           void *values, void *stream);
+
+/* The LM head on MXFP4 codes in hand: out[i, v] = sum over blocks b of
+ * 2^(eh + ew) * sum_{k in b} h_k * w_k for i < n, v < V.  Products of codes are exact, sums are
+ * fp32; out_dtype F32, or BF16 (round to nearest even).
+ *   Hq, h_scale  [M, B * 16] codes and [M, B] scale bytes; Wq, w_scale [V, B * 16] and [V, B],
+ *             as mosaic_quantize_rows_mxfp4 makes them (codes 16-byte aligned, scales anywhere).
+ *             Where d is no multiple of 32, one of the two has to hold zeros behind d.
+ *   count     NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.  The form is
+ *             chosen by M.
+ *   out       [M, V] row-major, 16-byte aligned.  Rows >= n are not written.
+ * A scale byte of 255 makes its row (or column) NaN.  M == 0 or V == 0: OK, nothing enqueued.
+ * The results do not depend on M, on count or on which form runs.  Any 1 <= d <= 2^25; more, or
+ * more than 2^24 - 1 tiles of 64 x 64 outputs: UNSUPPORTED. */
+mosaic_status_t mosaic_quantized_logits_mxfp4(const uint8_t *Hq, const uint8_t *h_scale, int64_t M, const int32_t *count,
+                                              const uint8_t *Wq, const uint8_t *w_scale, int64_t V, int64_t d, void *out,
+                                              mosaic_dtype_t out_dtype, void *stream);
+
+/* Workspace bytes of mosaic_masked_logits_mxfp4 for M rows in chunks of chunk_rows: 17 * C *
+ * ceil(d / 32), with C the rows of the largest chunk; -1 on a negative size or overflow. */
+int64_t mosaic_logits_mxfp4_workspace_bytes(int64_t M, int64_t chunk_rows, int64_t d);
+
+/* The MXFP4 form of mosaic_masked_logits_int8: each chunk's rows H[idx[i]] are quantized into
+ * `workspace` as mosaic_quantize_rows_mxfp4 does, then multiplied as by
+ * mosaic_quantized_logits_mxfp4.  An idx value outside [0, L) gives a row of NaN (or INVALID_ARG
+ * under MOSAIC_CHECK_IDX=1).  Arguments and errors as there (Wq 16-byte aligned); workspace >=
+ * mosaic_logits_mxfp4_workspace_bytes(M, chunk_rows, d) bytes, 16-byte aligned.  Results do not
+ * depend on chunk_rows. */
+mosaic_status_t mosaic_masked_logits_mxfp4(const void *H, int64_t L, int64_t d, mosaic_dtype_t in_dtype,
+                                           const int32_t *idx, int64_t M, const uint8_t *Wq, const uint8_t *w_scale,
+                                           int64_t V, void *out, int64_t chunk_rows, mosaic_dtype_t out_dtype,
+                                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Per row of logits: the log-probability of a given token, the entropy and the largest logits,
+ * for a sampler that re-masks by confidence, margin or entropy ([MR] 核心观察 #2: only masked
+ * tokens are sampled), for evaluation, and for training on log-probabilities.  For row i < n:
+ *   m = max_v z_v,  x_v = (z_v - m) / T,  l = log(sum_v exp(x_v)),  p_v = exp(x_v - l)
+ *   stats[i] = (m, l),  logprob[i] = x_t - l with t = tokens[i],  entropy[i] = -sum_v p_v log p_v
+ *   top_ids[i, j], top_logprobs[i, j]: entry and log-probability of the j-th largest logit, the
+ *             lower entry first among equal logits; logits of -inf are none, and places
+ *             without a logit hold -1 and -inf
+ * All arithmetic is fp32.  A token outside [0, V) is none and has logprob 0.  Logits of -inf
+ * are allowed (p_v = 0, a logprob of -inf); a row of nothing but -inf, or with a NaN or +inf,
+ * has NaN in logprob (of a token), entropy, l and top_logprobs, and top_ids of -1.
+ *   logits    [M, V] in dtype (F32 or BF16), row stride ldz >= V elements.
+ *   tokens    NULL (logprob then NULL too) or int32[M].
+ *   temperature  2^-20 <= T <= 2^20, else INVALID_ARG.
+ *   count     NULL (n = M), or a device-side row count as for mosaic_add_rmsnorm.
+ *   logprob   float[M];  entropy  NULL or float[M];  stats  float[M, 2] (8-byte aligned).
+ *   top_ids, top_logprobs  int32[M, top_n], float[M, top_n] where top_n > 0; 0 <= top_n <= 64
+ *             (more: UNSUPPORTED).
+ *   workspace >= mosaic_token_logprobs_workspace_bytes(M, V, top_n) bytes, 16-byte aligned (NULL
+ *             if that is 0); calls that overlap in time need one each.
+ * Rows >= n of every output are not written.  M == 0: OK, nothing enqueued.  V == 0 with M >
+ * 0, a NULL required pointer, misalignment, strides below V or a short workspace:
+ * INVALID_ARG.  M of 2^31 and more, V of more than 2^30: UNSUPPORTED. */
+mosaic_status_t mosaic_token_logprobs(const void *logits, int64_t ldz, int64_t M, int64_t V, mosaic_dtype_t dtype,
+                                      const int32_t *tokens, float temperature, const int32_t *count, float *logprob,
+                                      float *entropy, int64_t top_n, int32_t *top_ids, float *top_logprobs,
+                                      float *stats, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of mosaic_token_logprobs for either type (0 where no such call splits rows), or
+ * -1 on a size that it does not take. */
+int64_t mosaic_token_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t top_n);
+
+/* The gradient of sum_i grad_logprob[i] * logprob[i] + grad_entropy[i] * entropy[i] with respect
+ * to the logits, from what mosaic_token_logprobs left for the same logits and temperature:
+ *   grad[i, v] = (g * ([v = t] - p_v) - h * p_v * (log p_v + entropy[i])) / T
+ * with g = grad_logprob[i] (0 without a token) and h = grad_entropy[i], rounded once to the
+ * logits' type.  A row whose l is NaN has a gradient of NaN.
+ *   tokens, grad_logprob   both NULL, or both given;  grad_entropy  NULL, or float[M] with
+ *             entropy given.  One of the two gradients has to be given.
+ *   grad      [M, V] in dtype, row stride ldg >= V.  It may be logits itself (same pointer and
+ *             stride); no other overlap is allowed.
+ * Other arguments and errors as there. */
+mosaic_status_t mosaic_token_logprobs_grad(const void *logits, int64_t ldz, int64_t M, int64_t V, mosaic_dtype_t dtype,
+                                           const int32_t *tokens, float temperature, const int32_t *count,
+                                           const float *stats, const float *entropy, const float *grad_logprob,
+                                           const float *grad_entropy, void *grad, int64_t ldg, void *stream);
+
 /* ------------------------------------------------------------ host helpers --- */
 
 /* Number of chunks a call of mosaic_masked_logits makes for M rows ([DS] §3.2.2):

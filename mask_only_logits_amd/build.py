@@ -12,7 +12,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libmosaic.so"
 SOURCES = ["compact.hip", "gather_gemm.hip", "gather_gemm_fp8.hip", "gemm_int8.hip", "rmsnorm.hip", "distill.hip",
-           "mosaic_abi.cpp", "mosaic_abi_ops.cpp"]
+           "layernorm.hip", "gemm_mxfp4.hip", "token_logprobs.hip",
+           "mosaic_abi.cpp", "mosaic_abi_ops.cpp", "mosaic_abi_head.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++20", "-fPIC", "-Wall",

@@ -56,6 +56,16 @@ EXPORTS = (
     "mosaic_distill_topk",
     "mosaic_distill_topk_workspace_bytes",
     "mosaic_distill_topk_grad",
+    "mosaic_add_layernorm",
+    "mosaic_layernorm_grad",
+    "mosaic_layernorm_grad_workspace_bytes",
+    "mosaic_quantize_rows_mxfp4",
+    "mosaic_quantized_logits_mxfp4",
+    "mosaic_logits_mxfp4_workspace_bytes",
+    "mosaic_masked_logits_mxfp4",
+    "mosaic_token_logprobs",
+    "mosaic_token_logprobs_workspace_bytes",
+    "mosaic_token_logprobs_grad",
     "mosaic_debug_reload_env",
 )
 
@@ -125,6 +135,27 @@ def _load() -> ctypes.CDLL:
     lib.mosaic_distill_topk_workspace_bytes.argtypes = [i64, i64, i64]
     lib.mosaic_distill_topk_grad.restype = st
     lib.mosaic_distill_topk_grad.argtypes = [p, i64, i64, i64, st, p, st, p, i64, f32, p, p, p, p, i64, p]
+    lib.mosaic_add_layernorm.restype = st
+    lib.mosaic_add_layernorm.argtypes = [p, i64, p, i64, i64, i64, st, p, p, st, f32, p, p, i64, p, i64, p, p, p]
+    lib.mosaic_layernorm_grad.restype = st
+    lib.mosaic_layernorm_grad.argtypes = [p, i64, p, i64, i64, i64, st, p, p, st, p, p, i64, p, i64, p, i64, p, p, p,
+                                          i64, p]
+    lib.mosaic_layernorm_grad_workspace_bytes.restype = i64
+    lib.mosaic_layernorm_grad_workspace_bytes.argtypes = [i64, i64]
+    lib.mosaic_quantize_rows_mxfp4.restype = st
+    lib.mosaic_quantize_rows_mxfp4.argtypes = [p, i64, i64, st, p, i64, p, p, p, p]
+    lib.mosaic_quantized_logits_mxfp4.restype = st
+    lib.mosaic_quantized_logits_mxfp4.argtypes = [p, p, i64, p, p, p, i64, i64, p, st, p]
+    lib.mosaic_logits_mxfp4_workspace_bytes.restype = i64
+    lib.mosaic_logits_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.mosaic_masked_logits_mxfp4.restype = st
+    lib.mosaic_masked_logits_mxfp4.argtypes = [p, i64, i64, st, p, i64, p, p, i64, p, i64, st, p, i64, p]
+    lib.mosaic_token_logprobs.restype = st
+    lib.mosaic_token_logprobs.argtypes = [p, i64, i64, i64, st, p, f32, p, p, p, i64, p, p, p, p, i64, p]
+    lib.mosaic_token_logprobs_workspace_bytes.restype = i64
+    lib.mosaic_token_logprobs_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.mosaic_token_logprobs_grad.restype = st
+    lib.mosaic_token_logprobs_grad.argtypes = [p, i64, i64, i64, st, p, f32, p, p, p, p, p, p, i64, p]
     lib.mosaic_debug_reload_env.restype = None
     lib.mosaic_debug_reload_env.argtypes = []
     lib.mosaic_lazy_chunk_rows.restype = st
@@ -766,4 +797,292 @@ def mosaic_distill_topk_grad(logits: torch.Tensor, teacher_logits: torch.Tensor,
             z, ldz, M, V, _dtype_code(logits.dtype), top, top_type, ids, K, temperature,
             _vector(count, "count", 1, torch.int32), _vector(stats, "stats", 2 * M, torch.float32),
             _vector(grad_loss, "grad_loss", M, torch.float32), g, ldg, _raw_stream(device)), "mosaic_distill_topk_grad")
+    return grad
+
+
+def _weights(gain: torch.Tensor | None, bias: torch.Tensor | None, d: int, dtype: torch.dtype) -> torch.dtype:
+    """The type of a norm's gain and bias [d], which share it (dtype where there is neither)."""
+    for name, t in (("gain", gain), ("bias", bias)):
+        if t is not None and t.numel() != d:
+            raise ValueError(f"{name} must have d entries")
+    if gain is not None and bias is not None and gain.dtype != bias.dtype:
+        raise TypeError("gain and bias must share a dtype")
+    return gain.dtype if gain is not None else bias.dtype if bias is not None else dtype
+
+
+def mosaic_add_layernorm(X: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                         eps: float = 1e-5, residual: torch.Tensor | None = None,
+                         row_idx: torch.Tensor | None = None, count: torch.Tensor | None = None,
+                         rows: int | None = None, store_sum: bool = False, sum_out: torch.Tensor | None = None,
+                         store_out: bool = True, out: torch.Tensor | None = None, with_stats: bool = False,
+                         stats: torch.Tensor | None = None, stream=None):
+    """s = X + residual and y = (s - mean(s)) / sqrt(var(s) + eps) * gain + bias of rows of X [n, d]
+    (bf16 or fp32; the rows row_idx names, or all): returns (sum_out, out, stats), None for what
+    is not asked for.
+
+    sum_out [rows, d] holds s (with `store_sum`, or where it is given; without row_idx it may
+    be X or residual itself), out [rows, d] holds y (unless store_out is False), and stats
+    [rows, 2] float64 (with `with_stats`, or where it is given) holds the mean and 1 / sqrt(var +
+    eps), which mosaic_layernorm_grad takes.  X, residual and sum_out may have any row stride.
+    count: an int32 device tensor with the number of rows (clamped to rows); rows past it are
+    not written."""
+    if X.dim() != 2:
+        raise ValueError("X must be [n, d]")
+    n, d = X.shape
+    if rows is None:
+        rows = n if row_idx is None else row_idx.numel()
+    if row_idx is not None and rows > row_idx.numel():
+        raise ValueError("rows exceeds the length of row_idx")
+    dtype = X.dtype
+    w_type = _weights(gain, bias, d, dtype)
+    with _on(stream, X, gain, bias, residual, row_idx, count, sum_out, out, stats):
+        device = X.get_device()
+        if store_sum and sum_out is None:
+            sum_out = X.new_empty((rows, d))
+        if store_out and out is None:
+            out = X.new_empty((rows, d))
+        if with_stats and stats is None:
+            stats = X.new_empty((rows, 2), dtype=torch.float64)
+        x, ldx = _dev_rows(X, "X", n, d, dtype)
+        r, ldr = _dev_rows(residual, "residual", n, d, dtype)
+        s, lds = _dev_rows(sum_out, "sum_out", rows, d, dtype)
+        _check(lib.mosaic_add_layernorm(
+            x, ldx, r, ldr, n, d, _dtype_code(dtype), _vector(gain, "gain", d, w_type), _vector(bias, "bias", d, w_type),
+            _dtype_code(w_type), eps, _vector(row_idx, "row_idx", rows, torch.int32),
+            _vector(count, "count", 1, torch.int32), rows, s, lds, _vector(out, "out", rows * d, dtype),
+            _vector(stats, "stats", 2 * rows, torch.float64), _raw_stream(device)), "mosaic_add_layernorm")
+    return sum_out, out, stats
+
+
+def mosaic_layernorm_grad_workspace_bytes(rows: int, d: int) -> int:
+    """Workspace bytes of mosaic_layernorm_grad's weight gradients."""
+    n = int(lib.mosaic_layernorm_grad_workspace_bytes(int(rows), int(d)))
+    if n < 0:
+        raise ValueError("a negative size, or one that the call does not take")
+    return n
+
+
+def mosaic_layernorm_grad(grad_out: torch.Tensor, S: torch.Tensor, stats: torch.Tensor,
+                          gain: torch.Tensor | None = None, row_idx: torch.Tensor | None = None,
+                          count: torch.Tensor | None = None, grad_sum: torch.Tensor | None = None,
+                          with_x: bool = True, grad_x: torch.Tensor | None = None, with_gain: bool = True,
+                          grad_gain: torch.Tensor | None = None, with_bias: bool = True,
+                          grad_bias: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of mosaic_add_layernorm: returns (grad_x [rows, d], grad_gain float32 [d],
+    grad_bias float32 [d]), None for what is not asked for.
+
+    grad_out [rows, d] is the gradient with respect to out; S holds the rows that were normed: X
+    with the forward call's row_idx, or its sum_out without; stats is what it left.  grad_x is the
+    gradient with respect to the sum, result row by result row, with grad_sum [rows, d] (the
+    gradient that reaches the sum by the residual stream) added where it is given.  grad_x may
+    be grad_out, grad_sum or, without row_idx, S itself.  count: as there; rows past it count
+    nothing."""
+    if grad_out.dim() != 2 or S.dim() != 2 or S.shape[1] != grad_out.shape[1]:
+        raise ValueError("grad_out must be [rows, d] and S [n, d]")
+    if S.dtype != grad_out.dtype:
+        raise TypeError("grad_out and S must share a dtype")
+    rows, d = grad_out.shape
+    n, dtype = S.shape[0], S.dtype
+    w_type = _weights(gain, None, d, dtype)
+    with _on(stream, grad_out, S, stats, gain, row_idx, count, grad_sum, grad_x, grad_gain, grad_bias, workspace):
+        device = grad_out.get_device()
+        if with_x and grad_x is None:
+            grad_x = grad_out.new_empty((rows, d))
+        if with_gain and grad_gain is None:
+            grad_gain = grad_out.new_empty(d, dtype=torch.float32)
+        if with_bias and grad_bias is None:
+            grad_bias = grad_out.new_empty(d, dtype=torch.float32)
+        if workspace is None and (grad_gain is not None or grad_bias is not None):
+            need = mosaic_layernorm_grad_workspace_bytes(rows, d)
+            workspace = grad_out.new_empty(need, dtype=torch.uint8) if need > 0 else None
+        dy, lddy = _dev_rows(grad_out, "grad_out", rows, d, dtype)
+        s, lds = _dev_rows(S, "S", n, d, dtype)
+        ds, ldds = _dev_rows(grad_sum, "grad_sum", rows, d, dtype)
+        dx, lddx = _dev_rows(grad_x, "grad_x", rows, d, dtype)
+        _check(lib.mosaic_layernorm_grad(
+            dy, lddy, s, lds, n, d, _dtype_code(dtype), _vector(stats, "stats", 2 * rows, torch.float64),
+            _vector(gain, "gain", d, w_type), _dtype_code(w_type), _vector(row_idx, "row_idx", rows, torch.int32),
+            _vector(count, "count", 1, torch.int32), rows, ds, ldds, dx, lddx,
+            _vector(grad_gain, "grad_gain", d, torch.float32), _vector(grad_bias, "grad_bias", d, torch.float32),
+            _vector(workspace, "workspace", 0, torch.uint8), 0 if workspace is None else workspace.numel(),
+            _raw_stream(device)), "mosaic_layernorm_grad")
+    return grad_x, grad_gain, grad_bias
+
+
+def mosaic_quantize_rows_mxfp4(X: torch.Tensor, row_idx: torch.Tensor | None = None, rows: int | None = None,
+                               store_codes: bool = True, q: torch.Tensor | None = None,
+                               scale: torch.Tensor | None = None, with_values: bool = False,
+                               values: torch.Tensor | None = None, stream=None):
+    """MXFP4 codes of rows of X [n, d] (bf16 or fp32; the rows row_idx names, or all): returns (q uint8
+    [rows, 16 B], scale uint8 [rows, B], values) with B = ceil(d / 32) blocks of 32 elements: two
+    E2M1 codes to a byte, the even element in the low half, and one E8M0 scale byte per block.
+    values [rows, d] (with `with_values`, or where it is given; it may be X itself without
+    row_idx) holds what the codes stand for, in X's type, else None.  store_codes=False: values alone."""
+    if X.dim() != 2:
+        raise ValueError("X must be [n, d]")
+    n, d = X.shape
+    if rows is None:
+        rows = n if row_idx is None else row_idx.numel()
+    blocks = (d + 31) // 32
+    with _on(stream, X, row_idx, q, scale, values):
+        device = X.get_device()
+        if store_codes:
+            q = X.new_empty((rows, 16 * blocks), dtype=torch.uint8) if q is None else q
+            scale = X.new_empty((rows, blocks), dtype=torch.uint8) if scale is None else scale
+        if with_values and values is None:
+            values = X.new_empty((rows, d))
+        _check(lib.mosaic_quantize_rows_mxfp4(
+            _vector(X, "X", 0, X.dtype), n, d, _dtype_code(X.dtype), _vector(row_idx, "row_idx", rows, torch.int32),
+            rows, _vector(q, "q", rows * 16 * blocks, torch.uint8), _vector(scale, "scale", rows * blocks, torch.uint8),
+            _vector(values, "values", rows * d, X.dtype), _raw_stream(device)), "mosaic_quantize_rows_mxfp4")
+    return q, scale, values
+
+
+def _blocks_of(Wq: torch.Tensor, w_scale: torch.Tensor, name: str) -> int:
+    """Blocks of 32 elements in a row of packed MXFP4 codes, whose scales have to agree."""
+    if Wq.dim() != 2 or w_scale.dim() != 2 or Wq.shape[1] != 16 * w_scale.shape[1] or Wq.shape[0] > w_scale.shape[0]:
+        raise ValueError(f"{name} must be [n, 16 B] codes with [n, B] scales")
+    return w_scale.shape[1]
+
+
+def mosaic_quantized_logits_mxfp4(Hq: torch.Tensor, h_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                                  M: int | None = None, count: torch.Tensor | None = None,
+                                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                                  stream=None) -> torch.Tensor:
+    """logits = Hq . Wq^T of MXFP4 codes Hq [M, 16 B] with scales [M, B] and Wq [V, 16 B] with scales
+    [V, B], as mosaic_quantize_rows_mxfp4 makes them (bf16 or fp32 logits).  count: an int32 device
+    tensor with the number of rows (clamped to M); rows past it are not written."""
+    blocks = _blocks_of(Wq, w_scale, "Wq")
+    if _blocks_of(Hq, h_scale, "Hq") != blocks:
+        raise ValueError("Hq and Wq must have the same number of blocks")
+    V = Wq.shape[0]
+    M = Hq.shape[0] if M is None else int(M)
+    if M > Hq.shape[0]:
+        raise ValueError("M exceeds the rows of Hq")
+    with _on(stream, Hq, h_scale, Wq, w_scale, count, out):
+        device = Hq.get_device()
+        if out is None:
+            out = Hq.new_empty((M, V), dtype=out_dtype or torch.bfloat16)
+        _check(lib.mosaic_quantized_logits_mxfp4(
+            _vector(Hq, "Hq", 0, torch.uint8), _vector(h_scale, "h_scale", M * blocks, torch.uint8), M,
+            _vector(count, "count", 1, torch.int32), _vector(Wq, "Wq", 0, torch.uint8),
+            _vector(w_scale, "w_scale", V * blocks, torch.uint8), V, 32 * blocks, _vector(out, "out", M * V, out.dtype),
+            _dtype_code(out.dtype), _raw_stream(device)), "mosaic_quantized_logits_mxfp4")
+    return out
+
+
+def mosaic_logits_mxfp4_workspace_bytes(M: int, chunk_rows: int, d: int) -> int:
+    """Workspace bytes mosaic_masked_logits_mxfp4 needs for M rows in chunks of chunk_rows."""
+    n = int(lib.mosaic_logits_mxfp4_workspace_bytes(int(M), int(chunk_rows), int(d)))
+    if n < 0:
+        raise ValueError("workspace size overflows")
+    return n
+
+
+def mosaic_masked_logits_mxfp4(H: torch.Tensor, idx: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                               M: int | None = None, out: torch.Tensor | None = None, chunk_rows: int = 0,
+                               out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                               stream=None) -> torch.Tensor:
+    """Logits [M, V] (bf16 or fp32) of the MXFP4 LM head: H[idx[:M]] (bf16 or fp32) quantized in
+    blocks of 32 on the fly, times the pre-quantized W (Wq uint8 [V, 16 B], w_scale uint8 [V, B], B =
+    ceil(d / 32))."""
+    if H.dim() != 2:
+        raise ValueError("H must be [L, d]")
+    L, d = H.shape
+    blocks = _blocks_of(Wq, w_scale, "Wq")
+    if blocks != (d + 31) // 32:
+        raise ValueError("Wq must have a block for each 32 elements of H's rows")
+    V = Wq.shape[0]
+    M = idx.numel() if M is None else int(M)
+    if M > idx.numel():
+        raise ValueError("M exceeds the length of idx")
+    with _on(stream, H, idx, Wq, w_scale, out, workspace):
+        device = H.get_device()
+        if out is None:
+            out = H.new_empty((M, V), dtype=out_dtype or torch.bfloat16)
+        if workspace is None:
+            workspace = H.new_empty(max(16, mosaic_logits_mxfp4_workspace_bytes(M, chunk_rows, d)), dtype=torch.uint8)
+        _check(lib.mosaic_masked_logits_mxfp4(
+            _vector(H, "H", 0, H.dtype), L, d, _dtype_code(H.dtype), _vector(idx, "idx", M, torch.int32), M,
+            _vector(Wq, "Wq", 0, torch.uint8), _vector(w_scale, "w_scale", V * blocks, torch.uint8), V,
+            _vector(out, "out", M * V, out.dtype), int(chunk_rows), _dtype_code(out.dtype),
+            _vector(workspace, "workspace", 0, torch.uint8), workspace.numel(),
+            _raw_stream(device)), "mosaic_masked_logits_mxfp4")
+    return out
+
+
+def mosaic_token_logprobs_workspace_bytes(M: int, V: int, top_n: int) -> int:
+    """Workspace bytes mosaic_token_logprobs needs for M rows over V vocabulary entries and top_n
+    alternatives."""
+    n = int(lib.mosaic_token_logprobs_workspace_bytes(int(M), int(V), int(top_n)))
+    if n < 0:
+        raise ValueError("a negative size, or one that the call does not take")
+    return n
+
+
+def mosaic_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, temperature: float = 1.0,
+                          top_n: int = 0, with_entropy: bool = False, count: torch.Tensor | None = None,
+                          logprob: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                          top_ids: torch.Tensor | None = None, top_logprobs: torch.Tensor | None = None,
+                          stats: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Per row i of logits [M, V] (bf16 or fp32, any row stride), of p = softmax(logits[i] / T): the
+    log-probability of tokens[i] (int32; outside [0, V): none, 0), the entropy, and the top_n most
+    likely entries (at most 64; the lower entry first among equal logits, -1 and -inf where there
+    are fewer).  Returns (logprob float32 [M], entropy float32 [M], top_ids int32 [M, top_n],
+    top_logprobs float32 [M, top_n], stats float32 [M, 2]), None for what is not asked for (entropy:
+    `with_entropy`, or where it is given); stats is what mosaic_token_logprobs_grad takes.  count: an
+    int32 device tensor with the number of rows (clamped to M)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    if tokens is None and logprob is not None:
+        raise ValueError("logprob needs tokens")
+    with _on(stream, logits, tokens, count, logprob, entropy, top_ids, top_logprobs, stats, workspace):
+        device = logits.get_device()
+        if tokens is not None and logprob is None:
+            logprob = logits.new_empty(M, dtype=torch.float32)
+        if with_entropy and entropy is None:
+            entropy = logits.new_empty(M, dtype=torch.float32)
+        if top_n > 0:
+            top_ids = logits.new_empty((M, top_n), dtype=torch.int32) if top_ids is None else top_ids
+            top_logprobs = logits.new_empty((M, top_n), dtype=torch.float32) if top_logprobs is None else top_logprobs
+        stats = logits.new_empty((M, 2), dtype=torch.float32) if stats is None else stats
+        z, ldz = _dev_rows(logits, "logits", M, V, logits.dtype)
+        if workspace is None:
+            need = int(lib.mosaic_token_logprobs_workspace_bytes(M, V, top_n))
+            workspace = logits.new_empty(need, dtype=torch.uint8) if need > 0 else None
+        _check(lib.mosaic_token_logprobs(
+            z, ldz, M, V, _dtype_code(logits.dtype), _vector(tokens, "tokens", M, torch.int32), temperature,
+            _vector(count, "count", 1, torch.int32), _vector(logprob, "logprob", M, torch.float32),
+            _vector(entropy, "entropy", M, torch.float32), top_n, _vector(top_ids, "top_ids", M * top_n, torch.int32),
+            _vector(top_logprobs, "top_logprobs", M * top_n, torch.float32),
+            _vector(stats, "stats", 2 * M, torch.float32), _vector(workspace, "workspace", 0, torch.uint8),
+            0 if workspace is None else workspace.numel(), _raw_stream(device)), "mosaic_token_logprobs")
+    return logprob, entropy, top_ids, top_logprobs, stats
+
+
+def mosaic_token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor | None, stats: torch.Tensor,
+                               grad_logprob: torch.Tensor | None, entropy: torch.Tensor | None = None,
+                               grad_entropy: torch.Tensor | None = None, temperature: float = 1.0,
+                               count: torch.Tensor | None = None, grad: torch.Tensor | None = None,
+                               stream=None) -> torch.Tensor:
+    """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with respect to logits, from
+    what mosaic_token_logprobs left for the same logits and temperature.  tokens and grad_logprob
+    float32 [M] go together, as do entropy and grad_entropy float32 [M]; either pair may be None.
+    grad (allocated if absent) may be logits itself."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    with _on(stream, logits, tokens, stats, grad_logprob, entropy, grad_entropy, count, grad):
+        device = logits.get_device()
+        if grad is None:
+            grad = logits.new_empty((M, V))
+        z, ldz = _dev_rows(logits, "logits", M, V, logits.dtype)
+        g, ldg = _dev_rows(grad, "grad", M, V, logits.dtype)
+        _check(lib.mosaic_token_logprobs_grad(
+            z, ldz, M, V, _dtype_code(logits.dtype), _vector(tokens, "tokens", M, torch.int32), temperature,
+            _vector(count, "count", 1, torch.int32), _vector(stats, "stats", 2 * M, torch.float32),
+            _vector(entropy, "entropy", M, torch.float32), _vector(grad_logprob, "grad_logprob", M, torch.float32),
+            _vector(grad_entropy, "grad_entropy", M, torch.float32), g, ldg, _raw_stream(device)),
+            "mosaic_token_logprobs_grad")
     return grad
