@@ -186,6 +186,87 @@ __device__ __forceinline__ void store_upto(void *p, int64_t off, const float (&x
             store1<BF16>(p, off + i, x[i]);
 }
 
+// A thread's CH chunks of a row of d elements, chunk c from element c * STEP + t0 on, zeros
+// behind the row's end.  The whole chunks' loads go first, without a branch between them.
+template <bool BF16, int CH, int STEP, bool STREAM>
+__device__ __forceinline__ void load_row(const void *p, int64_t off, int t0, int d, Raw<BF16> (&r)[CH])
+{
+    constexpr int N = kChunk<BF16>;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        r[c].fill(0.0f);
+        if (c * STEP + t0 + N <= d)
+            r[c].template load<STREAM>(p, off + c * STEP + t0);
+    }
+    if (d % N) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = c * STEP + t0;
+            if (k < d && k + N > d)
+                r[c].load_part(p, off + k, d - k);
+        }
+    }
+}
+
+// The gain's elements beside a chunk of N of the row's, as stored: 8, 16 or 32 bytes.
+template <bool BF16, int N>
+struct Gain {
+    static constexpr int WORDS = N * (BF16 ? 2 : 4) / 4, V = WORDS < 4 ? WORDS : 4;
+    typedef uint32_t vec_t __attribute__((ext_vector_type(V)));
+    typedef vec_t vec_any __attribute__((aligned(2)));
+    vec_t w[WORDS / V];
+
+    __device__ __forceinline__ void load(const void *p, int k, int d)
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / V; ++i) {
+            w[i] = (vec_t)(0u);
+            if (k + N <= d)
+                w[i] = ((const vec_any *)((const char *)p + (int64_t)k * (BF16 ? 2 : 4)))[i];
+        }
+    }
+    // the chunk that the row's end cuts: its first n elements
+    __device__ __forceinline__ void load_part(const void *p, int k, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i) {
+            if (i >= n)
+                continue;
+            if constexpr (BF16)
+                w[i / 2 / V][i / 2 % V] |= (uint32_t)((const uint16_t *)p)[k + i] << (16 * (i % 2));
+            else
+                w[i / V][i % V] = ((const uint32_t *)p)[k + i];
+        }
+    }
+    // keeps the elements packed up to here (as Raw::opaque does)
+    __device__ __forceinline__ void opaque()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / V; ++i)
+            asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t e = BF16 ? w[i / 2 / V][i / 2 % V] : w[i / V % (WORDS / V)][i % V];
+        if constexpr (BF16)
+            return i % 2 ? bf16_hi(e) : bf16_lo(e);
+        else
+            return __builtin_bit_cast(float, e);
+    }
+};
+
+// Reduction over the LPR threads of a row: lanes of a wave, or a workgroup's waves.
+template <int LPR, typename Op>
+__device__ __forceinline__ float row_reduce(float v, Op op, float *red)
+{
+    if constexpr (LPR > 64)
+        return block_reduce<LPR / 64>(v, op, red);
+#pragma unroll
+    for (int o = LPR / 2; o >= 1; o >>= 1)
+        v = op(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
 // rows, or min(max(*count, 0), rows) where a device-side count is given.
 __device__ __forceinline__ int64_t row_count(const int32_t *count, int64_t rows)
 {
