@@ -224,3 +224,23 @@ def test_long_rows_of_memory(m):
     dx, dg, db = m.mosaic_layernorm_grad(x, x, st, gain)
     head64.check_layernorm_grad(x[-2:], x[-2:], st[-2:], gain, None, None, dx[-2:])
     head64.check_layernorm_grad(x[-2:], x[-2:], st[-2:], gain, None, None, None, dg, db)
+
+
+@pytest.mark.parametrize("d", [40, 190, 500, 700, 1021])
+def test_weight_gradients_of_very_many_rows(m, d):
+    # more than 128 rows to each group of threads: the sums are taken in runs
+    n = 2 ** 30 // d + 7
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x = torch.randn(n, d, generator=g, device=DEV, dtype=torch.float32).to(BF)
+    dy = (1 + torch.rand(n, d, generator=g, device=DEV)).to(BF)     # sums that grow
+    _, _, st = m.mosaic_add_layernorm(x, with_stats=True, store_out=False)
+    _, dg, db = m.mosaic_layernorm_grad(dy, x, st, with_x=False)
+    want_g, want_b = torch.zeros(d, dtype=torch.float64, device=DEV), torch.zeros(d, dtype=torch.float64, device=DEV)
+    size_g = torch.zeros_like(want_g)
+    for i in range(0, n, 1 << 17):
+        k = slice(i, i + (1 << 17))
+        t = dy[k].double() * ((x[k].double() - st[k, :1]) * st[k, 1:])
+        want_g, want_b, size_g = want_g + t.sum(0), want_b + dy[k].double().sum(0), size_g + t.abs().sum(0)
+    # runs of 128 rows in fp32, 4 half steps for a term, one rounding of the result
+    assert bool(((dg.double() - want_g).abs() <= 134 * 2.0 ** -24 * size_g).all())
+    assert bool(((db.double() - want_b).abs() <= 130 * 2.0 ** -24 * want_b).all())
