@@ -18,6 +18,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "launch.h"
 #include "launch_head.h"
@@ -31,107 +33,391 @@ using namespace rows;
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// Eight consecutive elements of a row a thread, four threads a block.  Bound: HBM.
+// Eight consecutive elements of a row.
+template <bool BF16>
+struct Eight {
+    Raw<BF16> r[8 / kChunk<BF16>];
+
+    __device__ __forceinline__ void load(const void *row, int k, int d)
+    {
+        constexpr int N = kChunk<BF16>;
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) {
+            const int at = k + i * N;
+            if (at + N <= d) {
+                r[i].load(row, at);
+            } else {
+                r[i].fill(0.0f);
+                if (at < d)
+                    r[i].load_part(row, at, d - at);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        constexpr int N = kChunk<BF16>;
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) {
+            float y[N];
+            r[i].get(y);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                x[i * N + e] = y[e];
+        }
+    }
+};
+
+// 2^lpr threads (4 to 256) take a row, eight elements a thread and turn and four threads a block,
+// and a workgroup 256 >> lpr rows.
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const void *__restrict__ X, int64_t nsrc, int32_t d,
-                                                             int32_t blocks, const int32_t *__restrict__ row_idx,
+                                                             int32_t blocks, int lpr, const int32_t *__restrict__ row_idx,
                                                              int64_t rows, uint8_t *__restrict__ q,
-                                                             uint8_t *__restrict__ scale, void *__restrict__ values)
+                                                             uint8_t *__restrict__ scale, void *values)
 {
-    constexpr int ES = BF16 ? 2 : 4;
-    const int64_t total = rows * blocks * 4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / (blocks * 4);
-        const int c = (int)(i - row * (blocks * 4)), k = c * 8;
+    constexpr int ES = BF16 ? 2 : 4, UN = 2;
+    const int t = threadIdx.x & ((1 << lpr) - 1), each = 256 >> lpr, chunks = blocks * 4;
+    for (int64_t row = (int64_t)blockIdx.x * each + (threadIdx.x >> lpr); row < rows; row += (int64_t)gridDim.x * each) {
         const int64_t src = row_idx ? (int64_t)row_idx[row] : row;
         const bool inside = src >= 0 && src < nsrc;   // a row id outside gives a row of NaN
-        float x[8];
-        uint32_t top = 0;
+        const char *from = (const char *)X + (inside ? src : 0) * d * ES;
+        for (int c0 = t; c0 < chunks; c0 += UN << lpr) {
+            Eight<BF16> in[UN];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = k + e < d ? (inside ? load1(X, src * d + k + e, BF16) : __builtin_nanf("")) : 0.0f;
-            top = max(top, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+            for (int u = 0; u < UN; ++u)
+                if (c0 + (u << lpr) < chunks)
+                    in[u].load(from, (c0 + (u << lpr)) * 8, d);
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const int c = c0 + (u << lpr);
+                if (c >= chunks)   // (the four threads of a block alike)
+                    continue;
+                float x[8];
+                in[u].get(x);
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    top = max(top, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+                top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
+                top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+                const int field = (int)(top >> 23);   // of the exponent: amax lies in [2^(field - 127), twice that)
+                const bool fine = field != 255 && inside;
+                const int byte = fine ? max(field - 2, 0) : 255;
+                const float down = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
+                uint32_t w = 0;
+                if (fine) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = __builtin_amdgcn_fmed3f(x[e] * down, -6.0f, 6.0f);
+                    // v_cvt_scalef32_pk_fp4_f32 rounds to nearest even
+                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], 1.0f, 0);
+                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
+                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 1.0f, 2);
+                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 1.0f, 3);
+                }
+                if (q)
+                    *(uint32_t *)(q + (row * blocks + (c >> 2)) * 16 + (c & 3) * 4) = w;
+                if (scale && (c & 3) == 0)
+                    scale[row * blocks + (c >> 2)] = (uint8_t)byte;
+                if (values) {
+                    const float up = !fine ? __builtin_nanf("")
+                                           : (byte ? __builtin_bit_cast(float, (uint32_t)byte << 23) : 0x1p-127f);
+                    float v[8];
+                    auto pair = [&](auto i) __attribute__((always_inline)) {
+                        const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, decltype(i)::value);
+                        v[2 * i] = p[0] * up;
+                        v[2 * i + 1] = p[1] * up;
+                    };
+                    pair(std::integral_constant<int, 0>{});
+                    pair(std::integral_constant<int, 1>{});
+                    pair(std::integral_constant<int, 2>{});
+                    pair(std::integral_constant<int, 3>{});
+                    constexpr int N = kChunk<BF16>;
+                    char *to = (char *)values + row * d * ES;
+#pragma unroll
+                    for (int i = 0; i < 8 / N; ++i)
+                        if (c * 8 + i * N < d)
+                            store_upto<BF16>(to, c * 8 + i * N, *(float(*)[N])&v[i * N], d - c * 8 - i * N);
+                }
+            }
         }
-        // the four threads of a block are neighbours, and in the loop together
-        top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
-        const int field = (int)(top >> 23);
-        const bool fine = field != 255;
-        const int byte = fine ? max(field - 2, 0) : 255;
-        const float down = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
-        const float up = byte ? __builtin_bit_cast(float, (uint32_t)byte << 23) : 0x1p-127f;
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = fine ? fabsf(x[e]) * down : 0.0f;
-            // the number of midpoints that y has passed; a tie goes to the even code
-            const uint32_t code = (uint32_t)(y > 0.25f) + (y >= 0.75f) + (y > 1.25f) + (y >= 1.75f) + (y > 2.5f) +
-                                  (y >= 3.5f) + (y > 5.0f);
-            const uint32_t sign = fine ? __builtin_bit_cast(uint32_t, x[e]) >> 31 : 0u;
-            w |= (code | sign << 3) << (4 * e);
-            const float v = code < 2 ? 0.5f * code : (code & 1 ? 1.5f : 1.0f) * (float)(1 << ((code >> 1) - 1));
-            x[e] = fine ? (sign ? -v : v) * up : __builtin_nanf("");
-        }
-        if (q)
-            *(uint32_t *)(q + (row * blocks + (c >> 2)) * 16 + (c & 3) * 4) = w;
-        if (scale && (c & 3) == 0)
-            scale[row * blocks + (c >> 2)] = (uint8_t)byte;
-        if (values)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < d)
-                    store1<BF16>((char *)values + row * d * ES, k + e, x[e]);
     }
 }
 
-__device__ __forceinline__ f32x4_t mfma_fp4(const i32x4_t &a, const i32x4_t &b, const f32x4_t &c, int sa, int sb)
+// c + a b of four blocks, with the scale bytes sa of a's register and sb of b's.
+template <int SA, int SB>
+__device__ __forceinline__ f32x4_t mfma_fp4(const i32x4_t &a, const i32x4_t &b, const f32x4_t &c, int scale_a, int scale_b)
 {
     const i32x8_t x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8_t y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, SA, scale_a, SB, scale_b);
 }
 
-// Any sizes: a wave for 16 x 16 outputs, its operands straight from memory.
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier without the fence of __syncthreads(), which would wait for the requests
+// in flight.
+__device__ __forceinline__ void bar()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// Requests straight to LDS: 16 bytes per lane, lane i's to lds + 16 i (STREAM: streaming cache
+// policy).
+template <bool STREAM>
+__device__ __forceinline__ void request(const void *src, void *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 16, 0, STREAM ? 2 : 0);
+}
+
+// What a request past the end of a row reads: codes and scale bytes of zero.
+__device__ __attribute__((aligned(16))) const uint8_t kZeroCodes[16] = {};
+
+// Four consecutive vocabulary entries v .. v + 3 of one row; vec: the address is a multiple of
+// the four values' size.
 template <bool OUT_BF16>
-__global__ __launch_bounds__(256) void gemm_mxfp4_any_kernel(const uint8_t *__restrict__ Hq,
-                                                             const uint8_t *__restrict__ hs,
-                                                             const int32_t *__restrict__ count, int32_t max_rows,
-                                                             const uint8_t *__restrict__ Wq,
-                                                             const uint8_t *__restrict__ ws, int32_t V, int32_t blocks,
-                                                             void *__restrict__ out)
+__device__ __forceinline__ void store4(void *out, int64_t off, const f32x4_t &x, int v, int V, bool vec)
+{
+    if (vec && v + 3 < V) {
+        if constexpr (OUT_BF16)
+            *(u32x2_t *)((uint16_t *)out + off) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        else
+            *(f32x4_t *)((float *)out + off) = x;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (v + e < V)
+            store1<OUT_BF16>(out, off + e, x[e]);
+}
+
+// The two scale bytes of a row's blocks b, b + 1 (b even), zeros behind the row's end, in the low
+// half of a register.  WORDS: the row's bytes are whole aligned words, one of which is loaded; else,
+// for rows of two blocks and more at any address, both bytes.  The loads have no branch: a row's end
+// moves them back, and `get` leaves out what they read too early.  They are relaxed atomics of the
+// wave's own scope, which are plain loads that the compiler leaves in their place and order: the
+// kernel counts them among its requests.
+template <bool WORDS>
+struct ScalePair {
+    int x;
+    uint8_t lo, hi;
+
+    __device__ __forceinline__ void load(const uint8_t *row, int b, int blocks)
+    {
+        if constexpr (WORDS) {
+            x = __hip_atomic_load((const int *)(row + min(b & ~3, blocks - 4)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+        } else {
+            const uint8_t *p = row + min(b, blocks - 2);
+            lo = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+            hi = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+        }
+    }
+    // after the wait for the K tile
+    __device__ __forceinline__ int get(int b, int blocks) const
+    {
+        if constexpr (WORDS) {
+            int w = x;
+            asm volatile("" : "+v"(w));   // or the compiler shifts before the wait, and waits for that
+            return b < blocks ? w >> (8 * (b & 2)) : 0;
+        }
+        return (int)(lo | (uint32_t)hi << 8) >> min(8 * max(b - (blocks - 2), 0), 16);
+    }
+};
+
+// Rows of a single block (d <= 32): a wave for 16 x 16 outputs, its operands straight from memory.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(256) void gemm_mxfp4_block_kernel(const uint8_t *__restrict__ Hq,
+                                                               const uint8_t *__restrict__ hs,
+                                                               const int32_t *__restrict__ count, int32_t max_rows,
+                                                               const uint8_t *__restrict__ Wq,
+                                                               const uint8_t *__restrict__ ws, int32_t V,
+                                                               void *__restrict__ out)
 {
     const int rows = (int)row_count(count, max_rows);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int64_t row_tiles = (rows + 15) / 16, tiles = row_tiles * ((V + 15) / 16);
     for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tiles; t += (int64_t)gridDim.x * 4) {
         const int v0 = (int)(t / row_tiles) * 16, m0 = (int)(t % row_tiles) * 16;
-        const int64_t wrow = (int64_t)min(v0 + r, V - 1) * blocks, hrow = (int64_t)min(m0 + r, rows - 1) * blocks;
-        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int kt = 0; kt < blocks; kt += 8) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int b = kt + 2 * g + s;
-                i32x4_t w = {0, 0, 0, 0}, h = w;
-                int sw = 0, sh = 0;
-                if (b < blocks) {
-                    w = *(const i32x4_t *)(Wq + (wrow + b) * 16);
-                    h = *(const i32x4_t *)(Hq + (hrow + b) * 16);
-                    sw = ws[wrow + b];
-                    sh = hs[hrow + b];
-                }
-                acc = mfma_fp4(w, h, acc, sw, sh);
-            }
+        i32x4_t w = {0, 0, 0, 0}, h = w;
+        int sw = 0, sh = 0;
+        if (g == 0) {
+            const int64_t wrow = min(v0 + r, V - 1), hrow = min(m0 + r, rows - 1);
+            w = *(const i32x4_t *)(Wq + wrow * 16);
+            h = *(const i32x4_t *)(Hq + hrow * 16);
+            sw = ws[wrow];
+            sh = hs[hrow];
         }
+        const f32x4_t acc = mfma_fp4<0, 0>(w, h, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, sw, sh);
         // lane (r, g) holds entries 4 g .. 4 g + 3 of the tile for its row r
-        const int row = m0 + r;
-        if (row >= rows)
-            continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (v0 + 4 * g + e < V)
-                store1<OUT_BF16>(out, (int64_t)row * V + v0 + 4 * g + e, acc[e]);
+        if (m0 + r < rows)
+            store4<OUT_BF16>(out, (int64_t)(m0 + r) * V + v0 + 4 * g, acc, v0 + 4 * g, V, false);
     }
 }
+
+// Small tiles: few rows, too few 256 x 256 tiles to fill the chip, or scale rows at any address.
+// BM x BV outputs per workgroup of NW waves, WGM of them side by side along the rows; K tiles of
+// 128 bytes (eight blocks) a row requested straight to LDS, NSTAGE - 1 of them ahead, in a ring with
+// one barrier per step, the rows' 16-byte blocks XOR-swizzled.  The scale bytes of a wave's rows come
+// straight to registers, with the K tile's requests.  Several workgroups share a CU, so one's start
+// and end lie under the others' streams.  STREAM: W is read once (one row tile): its requests take
+// the streaming cache policy.
+template <int BM, int BV, int WGM, int NSTAGE, bool STREAM, bool WORDS, bool OUT_BF16>
+__global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__restrict__ Hq,
+                                                               const uint8_t *__restrict__ hs,
+                                                               const int32_t *__restrict__ rows_dev, int32_t max_rows,
+                                                               const uint8_t *__restrict__ Wq,
+                                                               const uint8_t *__restrict__ ws, int32_t V, int32_t blocks,
+                                                               void *__restrict__ out, int32_t group_m)
+{
+    constexpr int BK = 128, CHUNKS = BK / 16, RPI = 64 / CHUNKS;
+    constexpr int WGV = 4 / WGM, WM = BM / WGM, WV = BV / WGV, AM = WM / 16, AV = WV / 16;
+    constexpr int W_TILE = BV * BK, STAGE = W_TILE + BM * BK;
+    constexpr int LW = BV / RPI / 4, LH = BM / RPI / 4, T = LW + LH;   // requests per wave and K tile
+    constexpr int TS = T + (AV + AM) * (WORDS ? 1 : 2);                 // and loads
+    static_assert(LW >= 1 && LH >= 1 && NSTAGE >= 3 && (NSTAGE - 2) * TS < 64, "requests");
+    __shared__ __attribute__((aligned(1024))) char smem[NSTAGE * STAGE];
+
+    const int rows = (int)row_count(rows_dev, max_rows);
+    const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, nblk = nvt * nmt;
+    const int b = blockIdx.x;
+    if (b >= nblk)
+        return;
+    // the workgroups of one XCD take a contiguous run of tiles: of group_m row tiles, the row
+    // tiles of a vocabulary tile one after another, so that they share its W rows in that XCD's L2
+    const int q8 = nblk >> 3, rem = nblk & 7, xcd = b & 7, slot = b >> 3;
+    const int t = (xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8) + slot;
+    const int first_m = t / (group_m * nvt) * group_m, gsz = min(nmt - first_m, group_m);
+    const int local = t - first_m * nvt;
+    const int m0 = (first_m + local % gsz) * BM, v0 = local / gsz * BV;
+    const int nk = (blocks + CHUNKS - 1) / CHUNKS, d = blocks * 16;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wv = wave % WGV, wm = wave / WGV;
+    auto swz = [](int r) { return (r >> 1) & 7; };
+    const uint8_t *src[T];
+    int chunk[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+        const int r = (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS;
+        chunk[j] = ((lane % CHUNKS) ^ swz(r)) * 16;
+        src[j] = j < LW ? Wq + (int64_t)min(v0 + r, V - 1) * d : Hq + (int64_t)min(m0 + r, rows - 1) * d;
+        src[j] += chunk[j];
+    }
+    const int r16 = lane & 15, qd = lane >> 4;
+    const uint8_t *scale_of[AV + AM];
+#pragma unroll
+    for (int j = 0; j < AV + AM; ++j)
+        scale_of[j] = j < AV ? ws + (int64_t)min(v0 + wv * WV + j * 16 + r16, V - 1) * blocks
+                             : hs + (int64_t)min(m0 + wm * WM + (j - AV) * 16 + r16, rows - 1) * blocks;
+    ScalePair<WORDS> sc[NSTAGE][AV + AM];   // scale bytes of the K tiles under way: stage kt % NSTAGE
+    auto issue = [&](int stage, int kt, ScalePair<WORDS> (&s)[AV + AM]) __attribute__((always_inline)) {
+        const int kb = kt * BK;
+#pragma unroll
+        for (int j = 0; j < AV + AM; ++j)
+            s[j].load(scale_of[j], kt * CHUNKS + 2 * qd, blocks);
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            const uint8_t *p = kb + chunk[j] < d ? src[j] + kb : kZeroCodes;
+            char *at = smem + stage * STAGE + (j < LW ? (wave * LW + j) * 1024 : W_TILE + (wave * LH + j - LW) * 1024);
+            if (j < LW)
+                request<STREAM>(p, at);
+            else
+                request<false>(p, at);
+        }
+    };
+    f32x4_t acc[AV][AM];
+#pragma unroll
+    for (int a = 0; a < AV; ++a)
+#pragma unroll
+        for (int m = 0; m < AM; ++m)
+            acc[a][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // blocks 2 qd and 2 qd + 1 of the lane's row in a K tile
+    const int lane_chunk = ((2 * qd) ^ swz(r16)) * 16;
+    const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = W_TILE + (wm * WM + r16) * BK + lane_chunk;
+
+    // Every step requests a K tile, those past the row's end from kZeroCodes: without a branch
+    // around requests and loads the waits can leave the younger K tiles in flight.
+#pragma unroll
+    for (int s = 0; s < NSTAGE - 1; ++s)
+        issue(s, s, sc[s]);
+    // K tile kt, of stage P = kt % NSTAGE
+    auto step = [&](auto stage, int kt) __attribute__((always_inline)) {
+        constexpr int P = decltype(stage)::value, NEXT = (P + NSTAGE - 1) % NSTAGE;
+        wait_vm<(NSTAGE - 2) * TS>();   // K tile kt has landed; the younger ones may not have
+        bar();   // every wave's part of it, and every wave is done with the stage read before
+        issue(NEXT, kt + NSTAGE - 1, sc[NEXT]);
+        int s[AV + AM];
+#pragma unroll
+        for (int j = 0; j < AV + AM; ++j)
+            s[j] = sc[P][j].get(kt * CHUNKS + 2 * qd, blocks);
+        auto half = [&](auto h) __attribute__((always_inline)) {
+            constexpr int S = decltype(h)::value;
+            i32x4_t af[AV], bf[AM];
+#pragma unroll
+            for (int a = 0; a < AV; ++a)
+                af[a] = *(const i32x4_t *)(smem + P * STAGE + ((a_addr + a * 16 * BK) ^ (16 * S)));
+#pragma unroll
+            for (int m = 0; m < AM; ++m)
+                bf[m] = *(const i32x4_t *)(smem + P * STAGE + ((b_addr + m * 16 * BK) ^ (16 * S)));
+#pragma unroll
+            for (int a = 0; a < AV; ++a)
+#pragma unroll
+                for (int m = 0; m < AM; ++m)
+                    acc[a][m] = mfma_fp4<S, S>(af[a], bf[m], acc[a][m], s[a], s[AV + m]);
+        };
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
+    };
+    // whole rounds, then the rest: a loop with one exit keeps every wait exact
+    int kt = 0;
+    for (; kt + NSTAGE <= nk; kt += NSTAGE)
+        [&]<int... P>(std::integer_sequence<int, P...>) __attribute__((always_inline)) {
+            (step(std::integral_constant<int, P>{}, kt + P), ...);
+        }(std::make_integer_sequence<int, NSTAGE>{});
+    auto rest = [&](auto self, auto stage) __attribute__((always_inline)) {
+        constexpr int P = decltype(stage)::value;
+        if constexpr (P < NSTAGE - 1) {
+            if (kt + P < nk) {
+                step(stage, kt + P);
+                self(self, std::integral_constant<int, P + 1>{});
+            }
+        }
+    };
+    rest(rest, std::integral_constant<int, 0>{});
+    wait_vm<0>();   // no request into the workgroup's LDS may be left when it ends
+    const bool vec = ((uintptr_t)out & 15) == 0 && (V & 3) == 0;
+#pragma unroll
+    for (int a = 0; a < AV; ++a) {
+        const int v = v0 + wv * WV + a * 16 + qd * 4;
+        if (v >= V)
+            continue;
+#pragma unroll
+        for (int m = 0; m < AM; ++m) {
+            const int row = m0 + wm * WM + m * 16 + r16;
+            if (row < rows)
+                store4<OUT_BF16>(out, (int64_t)row * V + v, acc[a][m], v, V, vec);
+        }
+    }
+}
+
+// The forms of the small kernel.
+template <int BM_, int BV_, int WGM_, int NSTAGE_, bool STREAM_>
+struct Small {
+    static constexpr int BM = BM_, BV = BV_, WGM = WGM_, NSTAGE = NSTAGE_;
+    static constexpr bool STREAM = STREAM_;
+};
 
 }  // namespace
 
@@ -139,9 +425,15 @@ hipError_t launch_quantize_rows_mxfp4(const void *X, bool in_bf16, int64_t nsrc,
                                       int64_t rows, uint8_t *q, uint8_t *scale, void *values, hipStream_t stream)
 {
     const int64_t blocks = mxfp4_blocks(d);
-    const dim3 grid((unsigned)std::min<int64_t>((rows * blocks * 4 + 255) / 256, 1 << 20));
+    // the most threads of which four fifths have work over all turns (65536 x 1040 bf16, 132 chunks: 32 threads)
+    const int64_t chunks = blocks * 4;
+    int lpr = 8;
+    while (lpr > 2 && chunks * 5 < ((chunks + (1 << lpr) - 1) >> lpr << lpr) * 4)
+        --lpr;
+    const int64_t each = 256 >> lpr;
+    const dim3 grid((unsigned)std::min<int64_t>((rows + each - 1) / each, 1 << 20));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, X, nsrc, (int32_t)d, (int32_t)blocks, row_idx, rows, q,
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, X, nsrc, (int32_t)d, (int32_t)blocks, lpr, row_idx, rows, q,
                            scale, values);
     };
     in_bf16 ? go(quantize_mxfp4_kernel<true>) : go(quantize_mxfp4_kernel<false>);
@@ -152,12 +444,46 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
                              const uint8_t *Wq, const uint8_t *ws, int64_t V, int64_t blocks, void *out, bool out_bf16,
                              hipStream_t stream)
 {
-    const int64_t row_tiles = (rows + 15) / 16, tiles = row_tiles * ((V + 15) / 16);
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>((tiles + 3) / 4, 1 << 20)), dim3(256), 0, stream, Hq,
-                           hs, count, (int32_t)rows, Wq, ws, (int32_t)V, (int32_t)blocks, out);
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess)
+        (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    auto tiles = [&](int64_t bm, int64_t bv) { return ((V + bv - 1) / bv) * ((rows + bm - 1) / bm); };
+    auto go = [&](auto kernel, int64_t grid, int threads) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, Hq, hs, count, (int32_t)rows, Wq, ws,
+                           (int32_t)V, (int32_t)blocks, out, kDefaultGroupM);
     };
-    out_bf16 ? go(gemm_mxfp4_any_kernel<true>) : go(gemm_mxfp4_any_kernel<false>);
+    auto pick = [&](auto bf16_tag) {
+        constexpr bool B = decltype(bf16_tag)::value;
+        if (blocks == 1) {
+            const dim3 grid((unsigned)std::min<int64_t>((tiles(16, 16) + 3) / 4, 1 << 20));
+            hipLaunchKernelGGL((gemm_mxfp4_block_kernel<B>), grid, dim3(256), 0, stream, Hq, hs, count, (int32_t)rows, Wq,
+                               ws, (int32_t)V, out);
+            return;
+        }
+        const bool words = blocks % 4 == 0 && (((uintptr_t)hs | (uintptr_t)ws) & 3) == 0;
+        auto small = [&](auto form, int64_t grid) {
+            using F = decltype(form);
+            words ? go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, true, B>, grid, 256)
+                 : go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, false, B>, grid, 256);
+        };
+        if (tiles(32, 32) <= cus)
+            return small(Small<32, 32, 2, 8, false>{}, tiles(32, 32));
+        if (rows <= 32 && tiles(32, 128) >= cus)
+            return small(Small<32, 128, 1, 4, true>{}, tiles(32, 128));
+        if (rows <= 32)
+            return small(Small<32, 64, 1, 4, true>{}, tiles(32, 64));
+        if (rows <= 64 && tiles(64, 128) >= cus)
+            return small(Small<64, 128, 1, 3, true>{}, tiles(64, 128));
+        if (rows <= 64)
+            return small(Small<64, 64, 2, 4, true>{}, tiles(64, 64));
+        if (tiles(128, 128) < cus)
+            return small(Small<64, 64, 2, 4, false>{}, tiles(64, 64));
+        return small(Small<128, 128, 2, 3, false>{}, tiles(128, 128));
+    };
+    if (out_bf16)
+        pick(std::true_type{});
+    else
+        pick(std::false_type{});
     return hipGetLastError();
 }
 
