@@ -32,6 +32,7 @@ using namespace rows;
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // Eight consecutive elements of a row.
 template <bool BF16>
@@ -412,6 +413,398 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
     }
 }
 
+__device__ __forceinline__ void request4(const void *src, void *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 4, 0, 0);
+}
+
+// BM x 256 outputs per workgroup of eight waves, BM = 128 or 256, walked persistently.  A K tile is
+// 128 bytes (eight blocks) of each row with its eight scale bytes.  Waves 0-3 (one per SIMD) request
+// it straight to LDS, two stages for codes and scales alike: as soon as every wave has a tile's last
+// fragments in registers, its stage takes the tile after next.  16-byte blocks are XOR-swizzled,
+// the A fragments single-buffered, the B fragments double-buffered.  The tile order keeps the XCDs
+// side by side on the vocabulary.
+//  * Lanes trade words in the epilogue so that each store instruction writes whole 128-byte lines.
+//  * TAIL: the rows' blocks are a multiple of four only; what lies behind a row's end is read from
+//    kZeroCodes.
+//  * STREAM: W is read once (one row tile): its requests take the streaming cache policy.
+template <int BM, bool STREAM, bool OUT_BF16, bool TAIL>
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2))) void
+gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs, const int32_t *__restrict__ rows_dev,
+                  int32_t max_rows, const uint8_t *__restrict__ Wq, const uint8_t *__restrict__ ws, int32_t V,
+                  int32_t blocks, void *__restrict__ out, int32_t group_m)
+{
+    constexpr int NW = 8, NWV = BM == 128 ? 4 : 2, DMAW = 4, BV = 256, BK = 128;
+    constexpr int CHUNKS = BK / 16, RPI = 64 / CHUNKS;          // rows per request instruction
+    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, S_TILE = (BV + BM) * 8;
+    constexpr int H_BASE = 2 * W_TILE, S_BASE = H_BASE + 2 * H_TILE;
+    constexpr int WV = BV / NWV, WM = BM / (NW / NWV), AV = WV / 16, AM = WM / 16;
+    constexpr int LW = BV / RPI / DMAW, LH = BM / RPI / DMAW;   // requests per requesting wave
+    constexpr int SW = BV * 2 / 64 / DMAW, SH = BM * 2 / 64 / DMAW, LT = LW + LH + SW + SH;
+    static_assert(S_BASE + 2 * S_TILE <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(1024))) char smem[S_BASE + 2 * S_TILE];
+
+    const int rows = (int)row_count(rows_dev, max_rows), d = blocks * 16;
+    const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, ntiles = nvt * nmt;
+    const int nk = (blocks + CHUNKS - 1) / CHUNKS;
+
+    // Tile list of this workgroup: in a full super-group of 8 * group_m row tiles, XCD x takes
+    // row tiles x, x + 8, ... of every vocabulary tile; the rest goes to the XCDs in eight
+    // contiguous runs.
+    const int per_xcd = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int per_group = group_m * nvt, sg = 8 * group_m, nfull = nmt / sg;
+    const int full_tiles = nfull * per_group;
+    const int rtiles = ntiles - 8 * full_tiles, q8 = rtiles >> 3, rem = rtiles & 7;
+    const int start = xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8;
+    const int count = full_tiles + q8 + (xcd < rem ? 1 : 0);
+    const int n_my = slot < count ? (count - slot + per_xcd - 1) / per_xcd : 0;
+    if (n_my == 0)
+        return;
+    auto tile_coords = [&](int i, int &m0, int &v0) __attribute__((always_inline)) {
+        const int tx = slot + i * per_xcd;
+        if (tx < full_tiles) {
+            const int s = tx / per_group, t = 8 * (tx - s * per_group) + xcd;
+            m0 = (s * sg + t % sg) * BM;
+            v0 = (t / sg) * BV;
+            return;
+        }
+        const int t = start + tx - full_tiles, g = t / per_group;
+        const int first_m = nfull * sg + g * group_m, gsz = min(nmt - first_m, group_m);
+        const int local = t - g * per_group;
+        m0 = (first_m + local % gsz) * BM;
+        v0 = (local / gsz) * BV;
+    };
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wv = wave % NWV, wm = wave / NWV, dwave = wave % DMAW;
+    auto swz = [](int r) { return (r >> 1) & 7; };
+
+    // Requests: lane i of instruction j fills tile row (dwave * L + j) * RPI + i / CHUNKS, whose
+    // logical block (i % CHUNKS) ^ swz(row) goes to physical block i % CHUNKS.  Scale words: lane i
+    // of instruction j takes half i % 2 of row (dwave * S + j) * 32 + i / 2.  Rows past V / rows
+    // re-read the last valid row; their results are never stored.
+    // Offsets are made anew for each request, from a few registers: kept, they would take twenty.
+    const uint32_t wrow0 = (uint32_t)(dwave * LW * RPI + lane / CHUNKS) * (uint32_t)d;
+    const uint32_t hrow0 = (uint32_t)(dwave * LH * RPI + lane / CHUNKS) * (uint32_t)d;
+    const uint32_t wsrow0 = (uint32_t)(dwave * SW * 32 + lane / 2) * (uint32_t)blocks;
+    const uint32_t hsrow0 = (uint32_t)(dwave * SH * 32 + lane / 2) * (uint32_t)blocks;
+    static_assert(LW % 2 == 0 && LH % 2 == 0 && RPI == 8, "requests of one parity swizzle alike");
+    const uint32_t chunk[2] = {(uint32_t)((lane % CHUNKS) ^ swz(lane / CHUNKS)) * 16,
+                               (uint32_t)((lane % CHUNKS) ^ swz(lane / CHUNKS + RPI)) * 16};
+    const uint32_t half = lane % 2 * 4;
+    const uint8_t *wbase, *hbase, *wsbase, *hsbase;
+    uint32_t wlast, hlast;   // the last valid row of the tile
+    auto make_src = [&](int m0, int v0) __attribute__((always_inline)) {
+        wbase = Wq + (int64_t)v0 * d;
+        hbase = Hq + (int64_t)m0 * d;
+        wsbase = ws + (int64_t)v0 * blocks;
+        hsbase = hs + (int64_t)m0 * blocks;
+        wlast = (uint32_t)min(BV, V - v0) - 1;
+        hlast = (uint32_t)min(BM, rows - m0) - 1;
+    };
+    // K tile kt into stage p
+    auto issue = [&](int p, int kt) __attribute__((always_inline)) {
+        const uint32_t d32 = (uint32_t)d, b32 = (uint32_t)blocks;
+        uint32_t wr = wrow0, hr = hrow0, wsr = wsrow0, hsr = hsrow0;
+        asm volatile("" : "+v"(wr), "+v"(hr), "+v"(wsr), "+v"(hsr));   // (or the offsets are kept after all)
+        auto code_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
+            const uint32_t off = min(row0 + (uint32_t)(j * RPI) * d32, last * d32) + chunk[j & 1];
+            return !TAIL || kt * BK + chunk[j & 1] < d32 ? base + kt * BK + off : kZeroCodes;
+        };
+        auto scale_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
+            const uint32_t off = min(row0 + (uint32_t)(j * 32) * b32, last * b32) + half;
+            return !TAIL || kt * CHUNKS + half < b32 ? base + kt * CHUNKS + off : kZeroCodes;
+        };
+#pragma unroll
+        for (int j = 0; j < SW; ++j)
+            request4(scale_from(wsbase, wsr, wlast, j), smem + S_BASE + p * S_TILE + (dwave * SW + j) * 256);
+#pragma unroll
+        for (int j = 0; j < SH; ++j)
+            request4(scale_from(hsbase, hsr, hlast, j), smem + S_BASE + p * S_TILE + BV * 8 + (dwave * SH + j) * 256);
+#pragma unroll
+        for (int j = 0; j < LW; ++j)
+            request<STREAM>(code_from(wbase, wr, wlast, j), smem + p * W_TILE + (dwave * LW + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < LH; ++j)
+            request<false>(code_from(hbase, hr, hlast, j), smem + H_BASE + p * H_TILE + (dwave * LH + j) * 1024);
+    };
+
+    f32x4_t acc[AV][AM];
+    auto zero_acc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < AV; ++a)
+#pragma unroll
+            for (int b = 0; b < AM; ++b)
+                acc[a][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    zero_acc();
+
+    // Fragments: lane (r16, qd) reads row r16 of a 16-row block, its blocks 2 qd and 2 qd + 1 in the
+    // two sub-steps; 16-row blocks start at multiples of 16, so a row's swizzle is the lane's.
+    const int r16 = lane & 15, qd = lane >> 4;
+    const int lane_chunk = ((2 * qd) ^ swz(r16)) * 16;
+    const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = H_BASE + (wm * WM + r16) * BK + lane_chunk;
+    const int sa_addr = S_BASE + (wv * WV + r16) * 8 + 2 * qd, sb_addr = S_BASE + (BV + wm * WM + r16) * 8 + 2 * qd;
+    i32x4_t af[AV], bf[2][AM];
+    // scale bytes of the K tile, two 16-row blocks to a register: byte 2 (a % 2) + s for sub-step s
+    u16x2_t sa[AV / 2], sb[AM / 2];
+    auto read_a = [&](int p, int s, int a) __attribute__((always_inline)) {
+        return *(const i32x4_t *)(smem + ((a_addr + p * W_TILE) ^ (16 * s)) + a * 16 * BK);
+    };
+    auto read_b = [&](int p, int s, int b) __attribute__((always_inline)) {
+        return *(const i32x4_t *)(smem + ((b_addr + p * H_TILE) ^ (16 * s)) + b * 16 * BK);
+    };
+    auto read_sa = [&](int p, int a) __attribute__((always_inline)) {
+        return *(const uint16_t *)(smem + sa_addr + p * S_TILE + a * 128);
+    };
+    auto read_sb = [&](int p, int b) __attribute__((always_inline)) {
+        return *(const uint16_t *)(smem + sb_addr + p * S_TILE + b * 128);
+    };
+    // MFMAs of sub-step S of a K tile, while the next sub-step's fragments are read: sub-step 1 of
+    // the same stage p, or sub-step 0 of the next K tile's stage p with its scales.  The B fragments go
+    // first, each A fragment after its row's MFMAs, the last one before them, so that the wave's
+    // last read is not followed by the step's wait.  Odd rows take the B blocks in reverse:
+    // consecutive MFMAs share an operand, which takes less power.
+    auto mma_load = [&](auto sub, int p) __attribute__((always_inline)) {
+        constexpr int S = decltype(sub)::value;
+        u16x2_t nsb[AM / 2], nsa;
+#pragma unroll
+        for (int b = 0; b < AM; ++b) {
+            bf[S ^ 1][b] = read_b(p, S ^ 1, b);
+            if (S == 1)
+                nsb[b / 2][b % 2] = read_sb(p, b);
+        }
+#pragma unroll
+        for (int a = 0; a < AV; ++a) {
+            i32x4_t nxt;
+            if (a == AV - 1) {
+                nxt = read_a(p, S ^ 1, a);
+                if (S == 1)
+                    nsa[1] = read_sa(p, a);
+            }
+#pragma unroll
+            for (int c = 0; c < AM; ++c) {
+                const int b = (a & 1) ? AM - 1 - c : c;
+                const int wsc = __builtin_bit_cast(int, sa[a / 2]), hsc = __builtin_bit_cast(int, sb[b / 2]);
+                if (a % 2 == 0)
+                    acc[a][b] = b % 2 == 0 ? mfma_fp4<S, S>(af[a], bf[S][b], acc[a][b], wsc, hsc)
+                                           : mfma_fp4<S, 2 + S>(af[a], bf[S][b], acc[a][b], wsc, hsc);
+                else
+                    acc[a][b] = b % 2 == 0 ? mfma_fp4<2 + S, S>(af[a], bf[S][b], acc[a][b], wsc, hsc)
+                                           : mfma_fp4<2 + S, 2 + S>(af[a], bf[S][b], acc[a][b], wsc, hsc);
+            }
+            if (a < AV - 1) {
+                nxt = read_a(p, S ^ 1, a);
+                if (S == 1)
+                    nsa[a % 2] = read_sa(p, a);
+            }
+            af[a] = nxt;
+            if (S == 1 && a % 2 == 1)
+                sa[a / 2] = nsa;
+        }
+        if (S == 1)
+#pragma unroll
+            for (int b = 0; b < AM / 2; ++b)
+                sb[b] = nsb[b];
+    };
+    // Instruction order of a sub-step: each request beside an MFMA, then the fragment reads
+    // spread over the MFMAs.
+    auto interleave = [&](int nreq) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LT; ++i) {
+            if (i < nreq) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < AM; ++b) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        const int used = nreq + AM;
+#pragma unroll
+        for (int a = 0; a < AV; ++a) {
+            if (a == AV - 1)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+            for (int c = 0; c < AM; ++c)
+                if (a * AM + c >= used)
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (a < AV - 1)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+    };
+
+    // a tile's first two K tiles
+    auto prologue = [&]() __attribute__((always_inline)) {
+        issue(0, 0);
+        if (nk > 1)
+            issue(1, 1);
+    };
+
+    const bool vec_ok = ((uintptr_t)out & 15) == 0 && V % (OUT_BF16 ? 8 : 4) == 0;
+    // Rows of whole 128-byte lines are stored with the streaming cache policy, which leaves the
+    // caches to the codes.
+    const bool lines = vec_ok && ((uintptr_t)out & 127) == 0 && V % (OUT_BF16 ? 64 : 32) == 0;
+    // one lane's N = 8 (bf16) or 4 (fp32) results of row `row` from vocabulary entry v on
+    auto store_words = [&](int row, int v, const uint32_t (&w)[4]) __attribute__((always_inline)) {
+        constexpr int N = OUT_BF16 ? 8 : 4;
+        if (row >= rows)
+            return;
+        char *o = (char *)out + ((int64_t)row * V + v) * (OUT_BF16 ? 2 : 4);
+        if (vec_ok && v + N <= V) {
+            const i32x4_t x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+            if (lines) {
+                // (between the fences, or the two stores are made one, without the policy)
+                asm volatile("" ::: "memory");
+                __builtin_nontemporal_store(x, (i32x4_t *)o);
+                asm volatile("" ::: "memory");
+            } else {
+                *(i32x4_t *)o = x;
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (v + e < V) {
+                if constexpr (OUT_BF16)
+                    ((uint16_t *)o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else
+                    ((uint32_t *)o)[e] = w[e];
+            }
+        }
+    };
+    // Lanes r16 and r16 ^ 8 trade words (row rotate by 8, the bank mask picks the receiving
+    // half), so that x holds rows 0-7 of both operands and y rows 8-15.
+    auto trade = [&](uint32_t (&x)[4], uint32_t (&y)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int a = (int)x[e], b = (int)y[e];
+            x[e] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xf, 0xc, false);
+            y[e] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xf, 0x3, false);
+        }
+    };
+    // Lane (r16, qd) holds entries 4 qd .. 4 qd + 3 of each 16-entry block for row r16 of each
+    // 16-row block.
+    auto epilogue = [&](int m0, int v0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < AV / 4; ++q) {
+#pragma unroll
+            for (int b = 0; b < AM; ++b) {
+                const int row = m0 + wm * WM + b * 16 + (r16 & 7);
+                if constexpr (OUT_BF16) {
+                    // neighbouring blocks: permlane16_swap gives a lane eight entries of one
+                    uint32_t p[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const f32x4_t &lo = acc[4 * q + 2 * i][b], &hi = acc[4 * q + 2 * i + 1][b];
+                        const auto s0 = __builtin_amdgcn_permlane16_swap(pack_bf16(lo[0], lo[1]), pack_bf16(hi[0], hi[1]),
+                                                                         false, false);
+                        const auto s1 = __builtin_amdgcn_permlane16_swap(pack_bf16(lo[2], lo[3]), pack_bf16(hi[2], hi[3]),
+                                                                         false, false);
+                        p[i][0] = s0[0];
+                        p[i][1] = s1[0];
+                        p[i][2] = s0[1];
+                        p[i][3] = s1[1];
+                    }
+                    trade(p[0], p[1]);
+                    const int v = v0 + wv * WV + (4 * q + 2 * (r16 >> 3) + (qd & 1)) * 16 + 4 * (qd & 2);
+                    store_words(row, v, p[0]);
+                    store_words(row + 8, v, p[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        uint32_t p[2][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[0][e] = __builtin_bit_cast(uint32_t, (float)acc[4 * q + i][b][e]);
+                            p[1][e] = __builtin_bit_cast(uint32_t, (float)acc[4 * q + i + 1][b][e]);
+                        }
+                        trade(p[0], p[1]);
+                        const int v = v0 + wv * WV + (4 * q + i + (r16 >> 3)) * 16 + 4 * qd;
+                        store_words(row, v, p[0]);
+                        store_words(row + 8, v, p[1]);
+                    }
+                }
+            }
+        }
+    };
+
+    auto main_loop = [&](auto dma_tag) __attribute__((always_inline)) {
+        constexpr bool DMA_ON = decltype(dma_tag)::value;
+        constexpr std::integral_constant<int, 0> first{};
+        constexpr std::integral_constant<int, 1> second{};
+        int m0, v0;
+        tile_coords(0, m0, v0);
+        if constexpr (DMA_ON) {
+            make_src(m0, v0);
+            prologue();
+        }
+        for (int i = 0; i < n_my; ++i) {
+            // K tile 0 has landed; K tile 1 may still be in flight
+            if (nk > 1)
+                wait_vm<LT>();
+            else
+                wait_vm<0>();
+            bar();
+#pragma unroll
+            for (int a = 0; a < AV; ++a) {
+                af[a] = read_a(0, 0, a);
+                sa[a / 2][a % 2] = read_sa(0, a);
+            }
+#pragma unroll
+            for (int b = 0; b < AM; ++b) {
+                bf[0][b] = read_b(0, 0, b);
+                sb[b / 2][b % 2] = read_sb(0, b);
+            }
+            int kt = 0, p = 0;
+            for (; kt + 2 < nk; ++kt) {
+                mma_load(first, p);
+                interleave(0);
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vm<0>();   // K tile kt + 1, and this wave's last fragments of this one
+                bar();
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (DMA_ON)
+                    issue(p, kt + 2);
+                p ^= 1;
+                mma_load(second, p);
+                interleave(DMA_ON ? LT : 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            for (; kt < nk; ++kt) {
+                mma_load(first, p);
+                if (kt + 1 < nk) {
+                    wait_vm<0>();
+                    bar();
+                }
+                p ^= 1;
+                mma_load(second, p);   // after the last K tile its reads are unused
+            }
+            // Every wave's last fragments are in registers.  The stores go first, then the next
+            // tile's requests: its first wait then leaves its second K tile in flight instead of
+            // waiting for it behind these stores.
+            wait_vm<0>();
+            bar();
+            epilogue(m0, v0);
+            zero_acc();
+            if (i + 1 < n_my) {
+                tile_coords(i + 1, m0, v0);
+                if constexpr (DMA_ON) {
+                    make_src(m0, v0);
+                    prologue();
+                }
+            }
+        }
+    };
+    if (wave < DMAW)
+        main_loop(std::true_type{});
+    else
+        main_loop(std::false_type{});
+}
+
 // The forms of the small kernel.
 template <int BM_, int BV_, int WGM_, int NSTAGE_, bool STREAM_>
 struct Small {
@@ -478,7 +871,25 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
             return small(Small<64, 64, 2, 4, true>{}, tiles(64, 64));
         if (tiles(128, 128) < cus)
             return small(Small<64, 64, 2, 4, false>{}, tiles(64, 64));
-        return small(Small<128, 128, 2, 3, false>{}, tiles(128, 128));
+        if (!words)
+            return small(Small<128, 128, 2, 3, false>{}, tiles(128, 128));
+        auto large = [&](auto bm_tag) {
+            constexpr int BM = decltype(bm_tag)::value;
+            const int64_t n = tiles(BM, 256);
+            // one persistent workgroup per CU, a multiple of the eight XCDs
+            const int64_t grid = std::min<int64_t>(std::max(8, cus / 8 * 8), (n + 7) / 8 * 8);
+            if (blocks % 8 != 0)
+                go(gemm_mxfp4_kernel<BM, false, B, true>, grid, 512);
+            else if (rows <= BM)
+                go(gemm_mxfp4_kernel<BM, true, B, false>, grid, 512);
+            else
+                go(gemm_mxfp4_kernel<BM, false, B, false>, grid, 512);
+        };
+        auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
+        if (rounds(tiles(128, 256)) * 3 < rounds(tiles(256, 256)) * 5)
+            large(std::integral_constant<int, 128>{});
+        else
+            large(std::integral_constant<int, 256>{});
     };
     if (out_bf16)
         pick(std::true_type{});
