@@ -182,6 +182,19 @@ __device__ __forceinline__ void request(const void *src, void *lds)
     __builtin_amdgcn_global_load_lds(src, (lds_void_t *)lds, 16, 0, STREAM ? 2 : 0);
 }
 
+// Where the eight 16-byte blocks of a row's K tile lie in its 128 bytes of LDS: block 2 g + s, which
+// lanes (r, g) read for sub-step s, at place (4 s + g) ^ swizzle(r).  A 16-byte read goes through
+// the LDS in groups of 16 lanes that mix neighbouring g; the sub-step in the place's high bit and the
+// row's swizzle keep each group on 64 different banks (with 2 g + s as the place, 44% of the LDS'
+// cycles were conflicts).
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+// the block at place `place` of a row
+__device__ __forceinline__ int block_at(int place, int row)
+{
+    const int x = place ^ swizzle(row);
+    return 2 * (x & 3) + (x >> 2);
+}
+
 // What a request past the end of a row reads: codes and scale bytes of zero.
 __device__ __attribute__((aligned(16))) const uint8_t kZeroCodes[16] = {};
 
@@ -306,13 +319,12 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wv = wave % WGV, wm = wave / WGV;
-    auto swz = [](int r) { return (r >> 1) & 7; };
     const uint8_t *src[T];
     int chunk[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) {
         const int r = (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS;
-        chunk[j] = ((lane % CHUNKS) ^ swz(r)) * 16;
+        chunk[j] = block_at(lane % CHUNKS, r) * 16;
         src[j] = j < LW ? Wq + (int64_t)min(v0 + r, V - 1) * d : Hq + (int64_t)min(m0 + r, rows - 1) * d;
         src[j] += chunk[j];
     }
@@ -344,8 +356,7 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
 #pragma unroll
         for (int m = 0; m < AM; ++m)
             acc[a][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    // blocks 2 qd and 2 qd + 1 of the lane's row in a K tile
-    const int lane_chunk = ((2 * qd) ^ swz(r16)) * 16;
+    const int lane_chunk = (qd ^ swizzle(r16)) * 16;
     const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = W_TILE + (wm * WM + r16) * BK + lane_chunk;
 
     // Every step requests a K tile, those past the row's end from kZeroCodes: without a branch
@@ -368,10 +379,10 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
             i32x4_t af[AV], bf[AM];
 #pragma unroll
             for (int a = 0; a < AV; ++a)
-                af[a] = *(const i32x4_t *)(smem + P * STAGE + ((a_addr + a * 16 * BK) ^ (16 * S)));
+                af[a] = *(const i32x4_t *)(smem + P * STAGE + ((a_addr + a * 16 * BK) ^ (64 * S)));
 #pragma unroll
             for (int m = 0; m < AM; ++m)
-                bf[m] = *(const i32x4_t *)(smem + P * STAGE + ((b_addr + m * 16 * BK) ^ (16 * S)));
+                bf[m] = *(const i32x4_t *)(smem + P * STAGE + ((b_addr + m * 16 * BK) ^ (64 * S)));
 #pragma unroll
             for (int a = 0; a < AV; ++a)
 #pragma unroll
@@ -478,10 +489,9 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wv = wave % NWV, wm = wave / NWV, dwave = wave % DMAW;
-    auto swz = [](int r) { return (r >> 1) & 7; };
 
-    // Requests: lane i of instruction j fills tile row (dwave * L + j) * RPI + i / CHUNKS, whose
-    // logical block (i % CHUNKS) ^ swz(row) goes to physical block i % CHUNKS.  Scale words: lane i
+    // Requests: lane i of instruction j fills place i % CHUNKS of tile row (dwave * L + j) * RPI + i /
+    // CHUNKS.  Scale words: lane i
     // of instruction j takes half i % 2 of row (dwave * S + j) * 32 + i / 2.  Rows past V / rows
     // re-read the last valid row; their results are never stored.
     // Offsets are made anew for each request, from a few registers: kept, they would take twenty.
@@ -490,8 +500,8 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     const uint32_t wsrow0 = (uint32_t)(dwave * SW * 32 + lane / 2) * (uint32_t)blocks;
     const uint32_t hsrow0 = (uint32_t)(dwave * SH * 32 + lane / 2) * (uint32_t)blocks;
     static_assert(LW % 2 == 0 && LH % 2 == 0 && RPI == 8, "requests of one parity swizzle alike");
-    const uint32_t chunk[2] = {(uint32_t)((lane % CHUNKS) ^ swz(lane / CHUNKS)) * 16,
-                               (uint32_t)((lane % CHUNKS) ^ swz(lane / CHUNKS + RPI)) * 16};
+    const uint32_t chunk[2] = {(uint32_t)block_at(lane % CHUNKS, lane / CHUNKS) * 16,
+                               (uint32_t)block_at(lane % CHUNKS, lane / CHUNKS + RPI) * 16};
     const uint32_t half = lane % 2 * 4;
     const uint8_t *wbase, *hbase, *wsbase, *hsbase;
     uint32_t wlast, hlast;   // the last valid row of the tile
@@ -543,17 +553,17 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     // Fragments: lane (r16, qd) reads row r16 of a 16-row block, its blocks 2 qd and 2 qd + 1 in the
     // two sub-steps; 16-row blocks start at multiples of 16, so a row's swizzle is the lane's.
     const int r16 = lane & 15, qd = lane >> 4;
-    const int lane_chunk = ((2 * qd) ^ swz(r16)) * 16;
+    const int lane_chunk = (qd ^ swizzle(r16)) * 16;
     const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = H_BASE + (wm * WM + r16) * BK + lane_chunk;
     const int sa_addr = S_BASE + (wv * WV + r16) * 8 + 2 * qd, sb_addr = S_BASE + (BV + wm * WM + r16) * 8 + 2 * qd;
     i32x4_t af[AV], bf[2][AM];
     // scale bytes of the K tile, two 16-row blocks to a register: byte 2 (a % 2) + s for sub-step s
     u16x2_t sa[AV / 2], sb[AM / 2];
     auto read_a = [&](int p, int s, int a) __attribute__((always_inline)) {
-        return *(const i32x4_t *)(smem + ((a_addr + p * W_TILE) ^ (16 * s)) + a * 16 * BK);
+        return *(const i32x4_t *)(smem + ((a_addr + p * W_TILE) ^ (64 * s)) + a * 16 * BK);
     };
     auto read_b = [&](int p, int s, int b) __attribute__((always_inline)) {
-        return *(const i32x4_t *)(smem + ((b_addr + p * H_TILE) ^ (16 * s)) + b * 16 * BK);
+        return *(const i32x4_t *)(smem + ((b_addr + p * H_TILE) ^ (64 * s)) + b * 16 * BK);
     };
     auto read_sa = [&](int p, int a) __attribute__((always_inline)) {
         return *(const uint16_t *)(smem + sa_addr + p * S_TILE + a * 128);
