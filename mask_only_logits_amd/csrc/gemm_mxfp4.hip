@@ -430,16 +430,20 @@ __device__ __forceinline__ void request4(const void *src, void *lds)
 }
 
 // BM x 256 outputs per workgroup of eight waves, BM = 128 or 256, walked persistently.  A K tile is
-// 128 bytes (eight blocks) of each row with its eight scale bytes.  Waves 0-3 (one per SIMD) request
-// it straight to LDS, two stages for codes and scales alike: as soon as every wave has a tile's last
-// fragments in registers, its stage takes the tile after next.  16-byte blocks are XOR-swizzled,
-// the A fragments single-buffered, the B fragments double-buffered.  The tile order keeps the XCDs
-// side by side on the vocabulary.
+// 128 bytes (eight blocks) of each row.  Waves 0-3 (one per SIMD) request it straight to LDS, into two
+// stages: as soon as every wave has a tile's last fragments in registers, its stage takes the tile
+// after next.  16-byte blocks are XOR-swizzled, the A fragments single-buffered, the B fragments
+// double-buffered.  The tile order keeps the XCDs side by side on the vocabulary.
+//  * Scales: eight bytes a row and K tile.  GROUPED (the rows' blocks are a multiple of 16): those of
+//    four K tiles are requested together, 32 bytes a row, a quarter of the rows with each of the four K
+//    tiles before; else the K tile's own two words of each row, with the tile.  What a request costs is
+//    the lines that it touches: the words of a K tile touch 512 lines for their 4 KB, beside the codes'
+//    512 for 64 KB.
 //  * Lanes trade words in the epilogue so that each store instruction writes whole 128-byte lines.
-//  * TAIL: the rows' blocks are a multiple of four only; what lies behind a row's end is read from
-//    kZeroCodes.
+//  * Not GROUPED: the rows' blocks are a multiple of four only; what lies behind a row's end is read
+//    from kZeroCodes.
 //  * STREAM: W is read once (one row tile): its requests take the streaming cache policy.
-template <int BM, bool STREAM, bool OUT_BF16, bool TAIL>
+template <int BM, bool STREAM, bool OUT_BF16, bool GROUPED>
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2))) void
 gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs, const int32_t *__restrict__ rows_dev,
                   int32_t max_rows, const uint8_t *__restrict__ Wq, const uint8_t *__restrict__ ws, int32_t V,
@@ -447,11 +451,12 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
 {
     constexpr int NW = 8, NWV = BM == 128 ? 4 : 2, DMAW = 4, BV = 256, BK = 128;
     constexpr int CHUNKS = BK / 16, RPI = 64 / CHUNKS;          // rows per request instruction
-    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, S_TILE = (BV + BM) * 8;
+    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, S_TILE = GROUPED ? 512 * 32 : (BV + BM) * 8;
     constexpr int H_BASE = 2 * W_TILE, S_BASE = H_BASE + 2 * H_TILE;
     constexpr int WV = BV / NWV, WM = BM / (NW / NWV), AV = WV / 16, AM = WM / 16;
     constexpr int LW = BV / RPI / DMAW, LH = BM / RPI / DMAW;   // requests per requesting wave
-    constexpr int SW = BV * 2 / 64 / DMAW, SH = BM * 2 / 64 / DMAW, LT = LW + LH + SW + SH;
+    constexpr int SW = BV * 2 / 64 / DMAW, SH = BM * 2 / 64 / DMAW;
+    constexpr int LT = LW + LH + (GROUPED ? 1 : SW + SH);       // and with the scales
     static_assert(S_BASE + 2 * S_TILE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem[S_BASE + 2 * S_TILE];
 
@@ -513,25 +518,45 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
         wlast = (uint32_t)min(BV, V - v0) - 1;
         hlast = (uint32_t)min(BM, rows - m0) - 1;
     };
+    // Quarter t % 4 of the scales of group t / 4 + 1 (128 of the 512 rows: W's, then H's; with 128 of H the
+    // last quarter repeats them, unused), two lanes a row, into the group's half of the stages.  Group g is
+    // requested at t = 4 g - 4 .. 4 g - 1, with K tiles t + 1, when the group before the last has been
+    // read; zeros behind the rows' ends.
+    auto issue_group = [&](int t) __attribute__((always_inline)) {
+        const int g = (t >> 2) + 1, q = t & 3;
+        uint32_t r = dwave * 32 + lane / 2 + (q & 1) * 128;
+        asm volatile("" : "+v"(r));
+        const uint32_t off = min(r, q < 2 ? wlast : hlast) * (uint32_t)blocks + g * 32 + lane % 2 * 16;
+        request<false>(g * 32 + lane % 2 * 16 < blocks ? (q < 2 ? wsbase : hsbase) + off : kZeroCodes,
+                       smem + S_BASE + (g & 1) * S_TILE + (q * 128 + dwave * 32) * 32);
+    };
     // K tile kt into stage p
-    auto issue = [&](int p, int kt) __attribute__((always_inline)) {
+    auto issue = [&](int p, int kt, bool first) __attribute__((always_inline)) {
         const uint32_t d32 = (uint32_t)d, b32 = (uint32_t)blocks;
         uint32_t wr = wrow0, hr = hrow0, wsr = wsrow0, hsr = hsrow0;
         asm volatile("" : "+v"(wr), "+v"(hr), "+v"(wsr), "+v"(hsr));   // (or the offsets are kept after all)
+        (void)wsr;
+        (void)hsr;
         auto code_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
             const uint32_t off = min(row0 + (uint32_t)(j * RPI) * d32, last * d32) + chunk[j & 1];
-            return !TAIL || kt * BK + chunk[j & 1] < d32 ? base + kt * BK + off : kZeroCodes;
+            return GROUPED || kt * BK + chunk[j & 1] < d32 ? base + kt * BK + off : kZeroCodes;
         };
         auto scale_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
             const uint32_t off = min(row0 + (uint32_t)(j * 32) * b32, last * b32) + half;
-            return !TAIL || kt * CHUNKS + half < b32 ? base + kt * CHUNKS + off : kZeroCodes;
+            return kt * CHUNKS + half < b32 ? base + kt * CHUNKS + off : kZeroCodes;
         };
+        if constexpr (GROUPED) {
+            if (!first)
+                issue_group(kt - 1);
+        } else {
 #pragma unroll
-        for (int j = 0; j < SW; ++j)
-            request4(scale_from(wsbase, wsr, wlast, j), smem + S_BASE + p * S_TILE + (dwave * SW + j) * 256);
+            for (int j = 0; j < SW; ++j)
+                request4(scale_from(wsbase, wsr, wlast, j), smem + S_BASE + p * S_TILE + (dwave * SW + j) * 256);
 #pragma unroll
-        for (int j = 0; j < SH; ++j)
-            request4(scale_from(hsbase, hsr, hlast, j), smem + S_BASE + p * S_TILE + BV * 8 + (dwave * SH + j) * 256);
+            for (int j = 0; j < SH; ++j)
+                request4(scale_from(hsbase, hsr, hlast, j),
+                         smem + S_BASE + p * S_TILE + BV * 8 + (dwave * SH + j) * 256);
+        }
 #pragma unroll
         for (int j = 0; j < LW; ++j)
             request<STREAM>(code_from(wbase, wr, wlast, j), smem + p * W_TILE + (dwave * LW + j) * 1024);
@@ -555,7 +580,11 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     const int r16 = lane & 15, qd = lane >> 4;
     const int lane_chunk = (qd ^ swizzle(r16)) * 16;
     const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = H_BASE + (wm * WM + r16) * BK + lane_chunk;
-    const int sa_addr = S_BASE + (wv * WV + r16) * 8 + 2 * qd, sb_addr = S_BASE + (BV + wm * WM + r16) * 8 + 2 * qd;
+    constexpr int S_ROW = GROUPED ? 32 : 8;
+    const int sa_addr = S_BASE + (wv * WV + r16) * S_ROW + 2 * qd;
+    const int sb_addr = S_BASE + (BV + wm * WM + r16) * S_ROW + 2 * qd;
+    // where K tile kt's scales lie behind these
+    auto scales_at = [&](int kt) { return GROUPED ? (kt >> 2 & 1) * S_TILE + (kt & 3) * 8 : (kt & 1) * S_TILE; };
     i32x4_t af[AV], bf[2][AM];
     // scale bytes of the K tile, two 16-row blocks to a register: byte 2 (a % 2) + s for sub-step s
     u16x2_t sa[AV / 2], sb[AM / 2];
@@ -565,25 +594,25 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     auto read_b = [&](int p, int s, int b) __attribute__((always_inline)) {
         return *(const i32x4_t *)(smem + ((b_addr + p * H_TILE) ^ (64 * s)) + b * 16 * BK);
     };
-    auto read_sa = [&](int p, int a) __attribute__((always_inline)) {
-        return *(const uint16_t *)(smem + sa_addr + p * S_TILE + a * 128);
+    auto read_sa = [&](int at, int a) __attribute__((always_inline)) {
+        return *(const uint16_t *)(smem + sa_addr + at + a * 16 * S_ROW);
     };
-    auto read_sb = [&](int p, int b) __attribute__((always_inline)) {
-        return *(const uint16_t *)(smem + sb_addr + p * S_TILE + b * 128);
+    auto read_sb = [&](int at, int b) __attribute__((always_inline)) {
+        return *(const uint16_t *)(smem + sb_addr + at + b * 16 * S_ROW);
     };
     // MFMAs of sub-step S of a K tile, while the next sub-step's fragments are read: sub-step 1 of
     // the same stage p, or sub-step 0 of the next K tile's stage p with its scales.  The B fragments go
     // first, each A fragment after its row's MFMAs, the last one before them, so that the wave's
     // last read is not followed by the step's wait.  Odd rows take the B blocks in reverse:
     // consecutive MFMAs share an operand, which takes less power.
-    auto mma_load = [&](auto sub, int p) __attribute__((always_inline)) {
+    auto mma_load = [&](auto sub, int p, int at) __attribute__((always_inline)) {
         constexpr int S = decltype(sub)::value;
         u16x2_t nsb[AM / 2], nsa;
 #pragma unroll
         for (int b = 0; b < AM; ++b) {
             bf[S ^ 1][b] = read_b(p, S ^ 1, b);
             if (S == 1)
-                nsb[b / 2][b % 2] = read_sb(p, b);
+                nsb[b / 2][b % 2] = read_sb(at, b);
         }
 #pragma unroll
         for (int a = 0; a < AV; ++a) {
@@ -591,7 +620,7 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
             if (a == AV - 1) {
                 nxt = read_a(p, S ^ 1, a);
                 if (S == 1)
-                    nsa[1] = read_sa(p, a);
+                    nsa[1] = read_sa(at, a);
             }
 #pragma unroll
             for (int c = 0; c < AM; ++c) {
@@ -607,7 +636,7 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
             if (a < AV - 1) {
                 nxt = read_a(p, S ^ 1, a);
                 if (S == 1)
-                    nsa[a % 2] = read_sa(p, a);
+                    nsa[a % 2] = read_sa(at, a);
             }
             af[a] = nxt;
             if (S == 1 && a % 2 == 1)
@@ -649,9 +678,14 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
 
     // a tile's first two K tiles
     auto prologue = [&]() __attribute__((always_inline)) {
-        issue(0, 0);
+        if constexpr (GROUPED) {
+#pragma unroll
+            for (int t = -4; t <= 0; ++t)   // the first group, and the second one's first quarter
+                issue_group(t);
+        }
+        issue(0, 0, true);
         if (nk > 1)
-            issue(1, 1);
+            issue(1, 1, true);
     };
 
     const bool vec_ok = ((uintptr_t)out & 15) == 0 && V % (OUT_BF16 ? 8 : 4) == 0;
@@ -755,7 +789,7 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
         for (int i = 0; i < n_my; ++i) {
             // K tile 0 has landed; K tile 1 may still be in flight
             if (nk > 1)
-                wait_vm<LT>();
+                wait_vm<LT - (GROUPED ? 1 : 0)>();
             else
                 wait_vm<0>();
             bar();
@@ -771,27 +805,27 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
             }
             int kt = 0, p = 0;
             for (; kt + 2 < nk; ++kt) {
-                mma_load(first, p);
+                mma_load(first, p, 0);
                 interleave(0);
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vm<0>();   // K tile kt + 1, and this wave's last fragments of this one
                 bar();
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (DMA_ON)
-                    issue(p, kt + 2);
+                    issue(p, kt + 2, false);
                 p ^= 1;
-                mma_load(second, p);
+                mma_load(second, p, scales_at(kt + 1));
                 interleave(DMA_ON ? LT : 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
             for (; kt < nk; ++kt) {
-                mma_load(first, p);
+                mma_load(first, p, 0);
                 if (kt + 1 < nk) {
                     wait_vm<0>();
                     bar();
                 }
                 p ^= 1;
-                mma_load(second, p);   // after the last K tile its reads are unused
+                mma_load(second, p, scales_at(kt + 1));   // after the last K tile its reads are unused
             }
             // Every wave's last fragments are in registers.  The stores go first, then the next
             // tile's requests: its first wait then leaves its second K tile in flight instead of
@@ -888,12 +922,13 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
             const int64_t n = tiles(BM, 256);
             // one persistent workgroup per CU, a multiple of the eight XCDs
             const int64_t grid = std::min<int64_t>(std::max(8, cus / 8 * 8), (n + 7) / 8 * 8);
-            if (blocks % 8 != 0)
-                go(gemm_mxfp4_kernel<BM, false, B, true>, grid, 512);
-            else if (rows <= BM)
-                go(gemm_mxfp4_kernel<BM, true, B, false>, grid, 512);
-            else
+            const bool grouped = blocks % 16 == 0 && (((uintptr_t)hs | (uintptr_t)ws) & 15) == 0;
+            if (!grouped)
                 go(gemm_mxfp4_kernel<BM, false, B, false>, grid, 512);
+            else if (rows <= BM)
+                go(gemm_mxfp4_kernel<BM, true, B, true>, grid, 512);
+            else
+                go(gemm_mxfp4_kernel<BM, false, B, true>, grid, 512);
         };
         auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
         if (rounds(tiles(128, 256)) * 3 < rounds(tiles(256, 256)) * 5)
