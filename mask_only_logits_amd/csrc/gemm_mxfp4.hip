@@ -451,14 +451,14 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
 {
     constexpr int NW = 8, NWV = BM == 128 ? 4 : 2, DMAW = 4, BV = 256, BK = 128;
     constexpr int CHUNKS = BK / 16, RPI = 64 / CHUNKS;          // rows per request instruction
-    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, S_TILE = GROUPED ? 512 * 32 : (BV + BM) * 8;
+    constexpr int W_TILE = BV * BK, H_TILE = BM * BK, S_TILE = GROUPED ? 512 * 32 : (BV + BM) * 8, S_ST = GROUPED ? 2 : 4;
     constexpr int H_BASE = 2 * W_TILE, S_BASE = H_BASE + 2 * H_TILE;
     constexpr int WV = BV / NWV, WM = BM / (NW / NWV), AV = WV / 16, AM = WM / 16;
     constexpr int LW = BV / RPI / DMAW, LH = BM / RPI / DMAW;   // requests per requesting wave
     constexpr int SW = BV * 2 / 64 / DMAW, SH = BM * 2 / 64 / DMAW;
     constexpr int LT = LW + LH + (GROUPED ? 1 : SW + SH);       // and with the scales
-    static_assert(S_BASE + 2 * S_TILE <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(1024))) char smem[S_BASE + 2 * S_TILE];
+    static_assert(S_BASE + S_ST * S_TILE <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(1024))) char smem[S_BASE + S_ST * S_TILE];
 
     const int rows = (int)row_count(rows_dev, max_rows), d = blocks * 16;
     const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, ntiles = nvt * nmt;
@@ -520,49 +520,56 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     };
     // Quarter t % 4 of the scales of group t / 4 + 1 (128 of the 512 rows: W's, then H's; with 128 of H the
     // last quarter repeats them, unused), two lanes a row, into the group's half of the stages.  Group g is
-    // requested at t = 4 g - 4 .. 4 g - 1, with K tiles t + 1, when the group before the last has been
+    // requested at t = 4 g - 4 .. 4 g - 1, with K tiles t, when the group before the last has been
     // read; zeros behind the rows' ends.
     auto issue_group = [&](int t) __attribute__((always_inline)) {
         const int g = (t >> 2) + 1, q = t & 3;
         uint32_t r = dwave * 32 + lane / 2 + (q & 1) * 128;
         asm volatile("" : "+v"(r));
-        const uint32_t off = min(r, q < 2 ? wlast : hlast) * (uint32_t)blocks + g * 32 + lane % 2 * 16;
-        request<false>(g * 32 + lane % 2 * 16 < blocks ? (q < 2 ? wsbase : hsbase) + off : kZeroCodes,
+        const uint32_t k = g * 32 + lane % 2 * 16, off = min(r, q < 2 ? wlast : hlast) * (uint32_t)blocks + k;
+        const uint64_t src = (uint64_t)(q < 2 ? wsbase : hsbase) + off, in = k < (uint32_t)blocks ? ~(uint64_t)0 : 0;
+        request<false>((const void *)((src & in) | ((uint64_t)kZeroCodes & ~in)),
                        smem + S_BASE + (g & 1) * S_TILE + (q * 128 + dwave * 32) * 32);
     };
-    // K tile kt into stage p
-    auto issue = [&](int p, int kt, bool first) __attribute__((always_inline)) {
-        const uint32_t d32 = (uint32_t)d, b32 = (uint32_t)blocks;
-        uint32_t wr = wrow0, hr = hrow0, wsr = wsrow0, hsr = hsrow0;
-        asm volatile("" : "+v"(wr), "+v"(hr), "+v"(wsr), "+v"(hsr));   // (or the offsets are kept after all)
-        (void)wsr;
-        (void)hsr;
-        auto code_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
-            const uint32_t off = min(row0 + (uint32_t)(j * RPI) * d32, last * d32) + chunk[j & 1];
-            return GROUPED || kt * BK + chunk[j & 1] < d32 ? base + kt * BK + off : kZeroCodes;
-        };
-        auto scale_from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
+    const uint32_t d32 = (uint32_t)d, b32 = (uint32_t)blocks;
+    // the words of K tile kt's scales
+    auto issue_words = [&](int kt) __attribute__((always_inline)) {
+        uint32_t wsr = wsrow0, hsr = hsrow0;
+        asm volatile("" : "+v"(wsr), "+v"(hsr));   // (or the offsets are kept after all)
+        auto from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
             const uint32_t off = min(row0 + (uint32_t)(j * 32) * b32, last * b32) + half;
             return kt * CHUNKS + half < b32 ? base + kt * CHUNKS + off : kZeroCodes;
         };
-        if constexpr (GROUPED) {
-            if (!first)
-                issue_group(kt - 1);
-        } else {
+        char *at = smem + S_BASE + (kt & 3) * S_TILE;
 #pragma unroll
-            for (int j = 0; j < SW; ++j)
-                request4(scale_from(wsbase, wsr, wlast, j), smem + S_BASE + p * S_TILE + (dwave * SW + j) * 256);
+        for (int j = 0; j < SW; ++j)
+            request4(from(wsbase, wsr, wlast, j), at + (dwave * SW + j) * 256);
 #pragma unroll
-            for (int j = 0; j < SH; ++j)
-                request4(scale_from(hsbase, hsr, hlast, j),
-                         smem + S_BASE + p * S_TILE + BV * 8 + (dwave * SH + j) * 256);
-        }
+        for (int j = 0; j < SH; ++j)
+            request4(from(hsbase, hsr, hlast, j), at + BV * 8 + (dwave * SH + j) * 256);
+    };
+    // K tile kt's codes into stage p
+    auto issue_codes = [&](int p, int kt) __attribute__((always_inline)) {
+        uint32_t wr = wrow0, hr = hrow0;
+        asm volatile("" : "+v"(wr), "+v"(hr));
+        auto from = [&](const uint8_t *base, uint32_t row0, uint32_t last, int j) __attribute__((always_inline)) {
+            const uint32_t off = min(row0 + (uint32_t)(j * RPI) * d32, last * d32) + chunk[j & 1];
+            return GROUPED || kt * BK + chunk[j & 1] < d32 ? base + kt * BK + off : kZeroCodes;
+        };
 #pragma unroll
         for (int j = 0; j < LW; ++j)
-            request<STREAM>(code_from(wbase, wr, wlast, j), smem + p * W_TILE + (dwave * LW + j) * 1024);
+            request<STREAM>(from(wbase, wr, wlast, j), smem + p * W_TILE + (dwave * LW + j) * 1024);
 #pragma unroll
         for (int j = 0; j < LH; ++j)
-            request<false>(code_from(hbase, hr, hlast, j), smem + H_BASE + p * H_TILE + (dwave * LH + j) * 1024);
+            request<false>(from(hbase, hr, hlast, j), smem + H_BASE + p * H_TILE + (dwave * LH + j) * 1024);
+    };
+    // what goes out in step kt, into stage p
+    auto issue = [&](int p, int kt) __attribute__((always_inline)) {
+        if constexpr (GROUPED)
+            issue_group(kt + 2);
+        else
+            issue_words(kt + 3);
+        issue_codes(p, kt + 2);
     };
 
     f32x4_t acc[AV][AM];
@@ -584,7 +591,7 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     const int sa_addr = S_BASE + (wv * WV + r16) * S_ROW + 2 * qd;
     const int sb_addr = S_BASE + (BV + wm * WM + r16) * S_ROW + 2 * qd;
     // where K tile kt's scales lie behind these
-    auto scales_at = [&](int kt) { return GROUPED ? (kt >> 2 & 1) * S_TILE + (kt & 3) * 8 : (kt & 1) * S_TILE; };
+    auto scales_at = [&](int kt) { return GROUPED ? (kt >> 2 & 1) * S_TILE + (kt & 3) * 8 : (kt & 3) * S_TILE; };
     i32x4_t af[AV], bf[2][AM];
     // scale bytes of the K tile, two 16-row blocks to a register: byte 2 (a % 2) + s for sub-step s
     u16x2_t sa[AV / 2], sb[AM / 2];
@@ -594,85 +601,78 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     auto read_b = [&](int p, int s, int b) __attribute__((always_inline)) {
         return *(const i32x4_t *)(smem + ((b_addr + p * H_TILE) ^ (64 * s)) + b * 16 * BK);
     };
-    auto read_sa = [&](int at, int a) __attribute__((always_inline)) {
-        return *(const uint16_t *)(smem + sa_addr + at + a * 16 * S_ROW);
-    };
-    auto read_sb = [&](int at, int b) __attribute__((always_inline)) {
-        return *(const uint16_t *)(smem + sb_addr + at + b * 16 * S_ROW);
+    auto read_scales = [&](int at, u16x2_t (&x)[AV / 2], u16x2_t (&y)[AM / 2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < AV; ++a)
+            x[a / 2][a % 2] = *(const uint16_t *)(smem + sa_addr + at + a * 16 * S_ROW);
+#pragma unroll
+        for (int b = 0; b < AM; ++b)
+            y[b / 2][b % 2] = *(const uint16_t *)(smem + sb_addr + at + b * 16 * S_ROW);
     };
     // MFMAs of sub-step S of a K tile, while the next sub-step's fragments are read: sub-step 1 of
-    // the same stage p, or sub-step 0 of the next K tile's stage p with its scales.  The B fragments go
-    // first, each A fragment after its row's MFMAs, the last one before them, so that the wave's
-    // last read is not followed by the step's wait.  Odd rows take the B blocks in reverse:
-    // consecutive MFMAs share an operand, which takes less power.
+    // the same stage p, or sub-step 0 of the next K tile's stage p.  The B fragments go first, each A
+    // fragment after its row's MFMAs, the last one before them, so that the wave's last read is not
+    // followed by the step's wait.  Odd rows take the B blocks in reverse: consecutive MFMAs share an
+    // operand, which takes less power.  Sub-step 0 also reads the next K tile's scales (at `at`).
+    uint16_t ra[AV], rb[AM];
     auto mma_load = [&](auto sub, int p, int at) __attribute__((always_inline)) {
         constexpr int S = decltype(sub)::value;
-        u16x2_t nsb[AM / 2], nsa;
 #pragma unroll
         for (int b = 0; b < AM; ++b) {
             bf[S ^ 1][b] = read_b(p, S ^ 1, b);
-            if (S == 1)
-                nsb[b / 2][b % 2] = read_sb(at, b);
+            if (S == 0)
+                rb[b] = *(const uint16_t *)(smem + sb_addr + at + b * 16 * S_ROW);
         }
 #pragma unroll
         for (int a = 0; a < AV; ++a) {
-            i32x4_t nxt;
-            if (a == AV - 1) {
-                nxt = read_a(p, S ^ 1, a);
-                if (S == 1)
-                    nsa[1] = read_sa(at, a);
-            }
+            const i32x4_t x = af[a];
+            if (a == AV - 1)
+                af[a] = read_a(p, S ^ 1, a);
+            if (S == 0)
+                ra[a] = *(const uint16_t *)(smem + sa_addr + at + a * 16 * S_ROW);
 #pragma unroll
             for (int c = 0; c < AM; ++c) {
                 const int b = (a & 1) ? AM - 1 - c : c;
                 const int wsc = __builtin_bit_cast(int, sa[a / 2]), hsc = __builtin_bit_cast(int, sb[b / 2]);
                 if (a % 2 == 0)
-                    acc[a][b] = b % 2 == 0 ? mfma_fp4<S, S>(af[a], bf[S][b], acc[a][b], wsc, hsc)
-                                           : mfma_fp4<S, 2 + S>(af[a], bf[S][b], acc[a][b], wsc, hsc);
+                    acc[a][b] = b % 2 == 0 ? mfma_fp4<S, S>(x, bf[S][b], acc[a][b], wsc, hsc)
+                                           : mfma_fp4<S, 2 + S>(x, bf[S][b], acc[a][b], wsc, hsc);
                 else
-                    acc[a][b] = b % 2 == 0 ? mfma_fp4<2 + S, S>(af[a], bf[S][b], acc[a][b], wsc, hsc)
-                                           : mfma_fp4<2 + S, 2 + S>(af[a], bf[S][b], acc[a][b], wsc, hsc);
+                    acc[a][b] = b % 2 == 0 ? mfma_fp4<2 + S, S>(x, bf[S][b], acc[a][b], wsc, hsc)
+                                           : mfma_fp4<2 + S, 2 + S>(x, bf[S][b], acc[a][b], wsc, hsc);
             }
-            if (a < AV - 1) {
-                nxt = read_a(p, S ^ 1, a);
-                if (S == 1)
-                    nsa[a % 2] = read_sa(at, a);
-            }
-            af[a] = nxt;
-            if (S == 1 && a % 2 == 1)
-                sa[a / 2] = nsa;
+            if (a < AV - 1)
+                af[a] = read_a(p, S ^ 1, a);
         }
-        if (S == 1)
+        // here, not later: behind a branch the compiler would gather two sub-steps' MFMAs
 #pragma unroll
-            for (int b = 0; b < AM / 2; ++b)
-                sb[b] = nsb[b];
+        for (int a = 0; a < AV; ++a)
+#pragma unroll
+            for (int b = 0; b < AM; ++b)
+                asm volatile("" : "+v"(acc[a][b]));
     };
-    // Instruction order of a sub-step: each request beside an MFMA, then the fragment reads
-    // spread over the MFMAs.
-    auto interleave = [&](int nreq) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < LT; ++i) {
-            if (i < nreq) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < AM; ++b) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-        const int used = nreq + AM;
+    // Instruction order of a sub-step: the B fragments beside the first row's MFMAs, each A fragment after
+    // its row's, and between them a scale (sub-step 0) or a request (sub-step 1) beside an MFMA.
+    auto interleave = [&](int nreq, bool scales) __attribute__((always_inline)) {
+        int left = nreq;
 #pragma unroll
         for (int a = 0; a < AV; ++a) {
+            if (a > 0)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             if (a == AV - 1)
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 #pragma unroll
-            for (int c = 0; c < AM; ++c)
-                if (a * AM + c >= used)
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (a < AV - 1)
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            for (int c = 0; c < AM; ++c) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (a == 0)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                if (scales && a > 0 && a <= 6 && c % 2 == 0)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                if (left > 0) {
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                    --left;
+                }
+            }
         }
     };
 
@@ -680,12 +680,16 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
     auto prologue = [&]() __attribute__((always_inline)) {
         if constexpr (GROUPED) {
 #pragma unroll
-            for (int t = -4; t <= 0; ++t)   // the first group, and the second one's first quarter
+            for (int t = -4; t < 2; ++t)   // the first group, and half of the second
                 issue_group(t);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                issue_words(t);
         }
-        issue(0, 0, true);
+        issue_codes(0, 0);
         if (nk > 1)
-            issue(1, 1, true);
+            issue_codes(1, 1);
     };
 
     const bool vec_ok = ((uintptr_t)out & 15) == 0 && V % (OUT_BF16 ? 8 : 4) == 0;
@@ -789,43 +793,51 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
         for (int i = 0; i < n_my; ++i) {
             // K tile 0 has landed; K tile 1 may still be in flight
             if (nk > 1)
-                wait_vm<LT - (GROUPED ? 1 : 0)>();
+                wait_vm<LW + LH>();
             else
                 wait_vm<0>();
             bar();
 #pragma unroll
-            for (int a = 0; a < AV; ++a) {
+            for (int a = 0; a < AV; ++a)
                 af[a] = read_a(0, 0, a);
-                sa[a / 2][a % 2] = read_sa(0, a);
-            }
 #pragma unroll
-            for (int b = 0; b < AM; ++b) {
+            for (int b = 0; b < AM; ++b)
                 bf[0][b] = read_b(0, 0, b);
-                sb[b / 2][b % 2] = read_sb(0, b);
-            }
+            read_scales(0, sa, sb);
+            // the scales that sub-step 0 has read, for the next K tile
+            auto next_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+                for (int a = 0; a < AV; ++a)
+                    sa[a / 2][a % 2] = ra[a];
+#pragma unroll
+                for (int b = 0; b < AM; ++b)
+                    sb[b / 2][b % 2] = rb[b];
+            };
             int kt = 0, p = 0;
             for (; kt + 2 < nk; ++kt) {
-                mma_load(first, p, 0);
-                interleave(0);
+                mma_load(first, p, scales_at(kt + 1));
+                interleave(0, true);
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vm<0>();   // K tile kt + 1, and this wave's last fragments of this one
                 bar();
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (DMA_ON)
-                    issue(p, kt + 2, false);
+                    issue(p, kt);
                 p ^= 1;
-                mma_load(second, p, scales_at(kt + 1));
-                interleave(DMA_ON ? LT : 0);
+                mma_load(second, p, 0);
+                interleave(DMA_ON ? LT : 0, false);
                 __builtin_amdgcn_sched_barrier(0);
+                next_scales();
             }
             for (; kt < nk; ++kt) {
-                mma_load(first, p, 0);
+                mma_load(first, p, scales_at(kt + 1));
                 if (kt + 1 < nk) {
                     wait_vm<0>();
                     bar();
                 }
                 p ^= 1;
-                mma_load(second, p, scales_at(kt + 1));   // after the last K tile its reads are unused
+                mma_load(second, p, 0);   // after the last K tile its reads are unused
+                next_scales();
             }
             // Every wave's last fragments are in registers.  The stores go first, then the next
             // tile's requests: its first wait then leaves its second K tile in flight instead of
