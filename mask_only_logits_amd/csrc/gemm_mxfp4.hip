@@ -283,8 +283,9 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_block_kernel(const uint8_t *__
 // BM x BV outputs per workgroup of NW waves, WGM of them side by side along the rows; K tiles of
 // 128 bytes (eight blocks) a row requested straight to LDS, NSTAGE - 1 of them ahead, in a ring with
 // one barrier per step, the rows' 16-byte blocks XOR-swizzled.  The scale bytes of a wave's rows come
-// straight to registers, with the K tile's requests.  Several workgroups share a CU, so one's start
-// and end lie under the others' streams.  STREAM: W is read once (one row tile): its requests take
+// straight to registers, with the K tile's requests.  Several workgroups share a CU, and each goes
+// from tile to tile without letting its requests run dry (64 x 126464 x 4096: 77 us, 81 with a
+// workgroup per tile; 4096 x 126464 x 4000, 128 x 128 tiles: 3.5 ms, 4.4).  STREAM: W is read once (one row tile): its requests take
 // the streaming cache policy.
 template <int BM, int BV, int WGM, int NSTAGE, bool STREAM, bool WORDS, bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__restrict__ Hq,
@@ -304,50 +305,68 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
 
     const int rows = (int)row_count(rows_dev, max_rows);
     const int nvt = (V + BV - 1) / BV, nmt = (rows + BM - 1) / BM, nblk = nvt * nmt;
-    const int b = blockIdx.x;
-    if (b >= nblk)
+    if ((int)blockIdx.x >= nblk)
         return;
-    // the workgroups of one XCD take a contiguous run of tiles: of group_m row tiles, the row
-    // tiles of a vocabulary tile one after another, so that they share its W rows in that XCD's L2
-    const int q8 = nblk >> 3, rem = nblk & 7, xcd = b & 7, slot = b >> 3;
-    const int t = (xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8) + slot;
-    const int first_m = t / (group_m * nvt) * group_m, gsz = min(nmt - first_m, group_m);
-    const int local = t - first_m * nvt;
-    const int m0 = (first_m + local % gsz) * BM, v0 = local / gsz * BV;
+    // Tile i of this workgroup: the workgroups of one XCD (the grid is a multiple of eight, or holds
+    // every tile) take a contiguous run of tiles, of group_m row tiles the row tiles of a vocabulary
+    // tile one after another, so that they share its W rows in that XCD's L2.
+    auto tile_coords = [&](int i, int &m0, int &v0) __attribute__((always_inline)) {
+        const int b = min((int)blockIdx.x + i * (int)gridDim.x, nblk - 1);
+        const int q8 = nblk >> 3, rem = nblk & 7, xcd = b & 7, slot = b >> 3;
+        const int t = (xcd < rem ? xcd * (q8 + 1) : rem * (q8 + 1) + (xcd - rem) * q8) + slot;
+        const int first_m = t / (group_m * nvt) * group_m, gsz = min(nmt - first_m, group_m);
+        const int local = t - first_m * nvt;
+        m0 = (first_m + local % gsz) * BM;
+        v0 = local / gsz * BV;
+    };
+    const int n_my = (nblk - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     const int nk = (blocks + CHUNKS - 1) / CHUNKS, d = blocks * 16;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wv = wave % WGV, wm = wave / WGV;
-    const uint8_t *src[T];
+    const int r16 = lane & 15, qd = lane >> 4;
     int chunk[T];
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-        const int r = (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS;
-        chunk[j] = block_at(lane % CHUNKS, r) * 16;
-        src[j] = j < LW ? Wq + (int64_t)min(v0 + r, V - 1) * d : Hq + (int64_t)min(m0 + r, rows - 1) * d;
-        src[j] += chunk[j];
-    }
-    const int r16 = lane & 15, qd = lane >> 4;
-    const uint8_t *scale_of[AV + AM];
-#pragma unroll
-    for (int j = 0; j < AV + AM; ++j)
-        scale_of[j] = j < AV ? ws + (int64_t)min(v0 + wv * WV + j * 16 + r16, V - 1) * blocks
-                             : hs + (int64_t)min(m0 + wm * WM + (j - AV) * 16 + r16, rows - 1) * blocks;
-    ScalePair<WORDS> sc[NSTAGE][AV + AM];   // scale bytes of the K tiles under way: stage kt % NSTAGE
-    auto issue = [&](int stage, int kt, ScalePair<WORDS> (&s)[AV + AM]) __attribute__((always_inline)) {
-        const int kb = kt * BK;
-#pragma unroll
-        for (int j = 0; j < AV + AM; ++j)
-            s[j].load(scale_of[j], kt * CHUNKS + 2 * qd, blocks);
+    for (int j = 0; j < T; ++j)
+        chunk[j] = block_at(lane % CHUNKS, (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS) * 16;
+    // where the requests have got to: an output tile's rows, and the K tile
+    const uint8_t *src[T], *scale_of[AV + AM];
+    int f_tile = 0, f_kt = 0;
+    auto sources = [&](int i) __attribute__((always_inline)) {
+        int m0, v0;
+        tile_coords(i, m0, v0);
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            const uint8_t *p = kb + chunk[j] < d ? src[j] + kb : kZeroCodes;
+            const int r = (j < LW ? wave * LW + j : wave * LH + j - LW) * RPI + lane / CHUNKS;
+            src[j] = j < LW ? Wq + (int64_t)min(v0 + r, V - 1) * d : Hq + (int64_t)min(m0 + r, rows - 1) * d;
+            src[j] += chunk[j];
+        }
+#pragma unroll
+        for (int j = 0; j < AV + AM; ++j)
+            scale_of[j] = j < AV ? ws + (int64_t)min(v0 + wv * WV + j * 16 + r16, V - 1) * blocks
+                                 : hs + (int64_t)min(m0 + wm * WM + (j - AV) * 16 + r16, rows - 1) * blocks;
+    };
+    ScalePair<WORDS> sc[NSTAGE][AV + AM];   // scale bytes of the K tiles under way: stage kt % NSTAGE
+    // the next K tile into a stage (past the last one: the last tile's again, unused, so that the waits
+    // need not know the end)
+    auto issue = [&](int stage, ScalePair<WORDS> (&s)[AV + AM]) __attribute__((always_inline)) {
+        const int kb = f_kt * BK;
+#pragma unroll
+        for (int j = 0; j < AV + AM; ++j)
+            s[j].load(scale_of[j], f_kt * CHUNKS + 2 * qd, blocks);
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            const uint8_t *p = kb + chunk[j] < d && f_tile < n_my ? src[j] + kb : kZeroCodes;
             char *at = smem + stage * STAGE + (j < LW ? (wave * LW + j) * 1024 : W_TILE + (wave * LH + j - LW) * 1024);
             if (j < LW)
                 request<STREAM>(p, at);
             else
                 request<false>(p, at);
+        }
+        if (++f_kt == nk) {
+            f_kt = 0;
+            sources(++f_tile);
         }
     };
     f32x4_t acc[AV][AM];
@@ -359,17 +378,18 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
     const int lane_chunk = (qd ^ swizzle(r16)) * 16;
     const int a_addr = (wv * WV + r16) * BK + lane_chunk, b_addr = W_TILE + (wm * WM + r16) * BK + lane_chunk;
 
-    // Every step requests a K tile, those past the row's end from kZeroCodes: without a branch
-    // around requests and loads the waits can leave the younger K tiles in flight.
+    const bool vec = ((uintptr_t)out & 15) == 0 && (V & 3) == 0;
+    int tile = 0, kt = 0;
+    sources(0);
 #pragma unroll
     for (int s = 0; s < NSTAGE - 1; ++s)
-        issue(s, s, sc[s]);
-    // K tile kt, of stage P = kt % NSTAGE
-    auto step = [&](auto stage, int kt) __attribute__((always_inline)) {
+        issue(s, sc[s]);
+    // K tile kt of an output tile, of stage P
+    auto step = [&](auto stage) __attribute__((always_inline)) {
         constexpr int P = decltype(stage)::value, NEXT = (P + NSTAGE - 1) % NSTAGE;
         wait_vm<(NSTAGE - 2) * TS>();   // K tile kt has landed; the younger ones may not have
         bar();   // every wave's part of it, and every wave is done with the stage read before
-        issue(NEXT, kt + NSTAGE - 1, sc[NEXT]);
+        issue(NEXT, sc[NEXT]);
         int s[AV + AM];
 #pragma unroll
         for (int j = 0; j < AV + AM; ++j)
@@ -391,37 +411,30 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__
         };
         half(std::integral_constant<int, 0>{});
         half(std::integral_constant<int, 1>{});
-    };
-    // whole rounds, then the rest: a loop with one exit keeps every wait exact
-    int kt = 0;
-    for (; kt + NSTAGE <= nk; kt += NSTAGE)
-        [&]<int... P>(std::integer_sequence<int, P...>) __attribute__((always_inline)) {
-            (step(std::integral_constant<int, P>{}, kt + P), ...);
-        }(std::make_integer_sequence<int, NSTAGE>{});
-    auto rest = [&](auto self, auto stage) __attribute__((always_inline)) {
-        constexpr int P = decltype(stage)::value;
-        if constexpr (P < NSTAGE - 1) {
-            if (kt + P < nk) {
-                step(stage, kt + P);
-                self(self, std::integral_constant<int, P + 1>{});
+        if (++kt < nk)
+            return;
+        int m0, v0;
+        tile_coords(tile, m0, v0);
+#pragma unroll
+        for (int a = 0; a < AV; ++a) {
+            const int v = v0 + wv * WV + a * 16 + qd * 4;
+#pragma unroll
+            for (int m = 0; m < AM; ++m) {
+                const int row = m0 + wm * WM + m * 16 + r16;
+                if (tile < n_my && row < rows && v < V)
+                    store4<OUT_BF16>(out, (int64_t)row * V + v, acc[a][m], v, V, vec);
+                acc[a][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
             }
         }
+        kt = 0;
+        ++tile;
     };
-    rest(rest, std::integral_constant<int, 0>{});
+    // (steps past the last tile of a round are computed and not stored)
+    while (tile < n_my)
+        [&]<int... P>(std::integer_sequence<int, P...>) __attribute__((always_inline)) {
+            (step(std::integral_constant<int, P>{}), ...);
+        }(std::make_integer_sequence<int, NSTAGE>{});
     wait_vm<0>();   // no request into the workgroup's LDS may be left when it ends
-    const bool vec = ((uintptr_t)out & 15) == 0 && (V & 3) == 0;
-#pragma unroll
-    for (int a = 0; a < AV; ++a) {
-        const int v = v0 + wv * WV + a * 16 + qd * 4;
-        if (v >= V)
-            continue;
-#pragma unroll
-        for (int m = 0; m < AM; ++m) {
-            const int row = m0 + wm * WM + m * 16 + r16;
-            if (row < rows)
-                store4<OUT_BF16>(out, (int64_t)row * V + v, acc[a][m], v, V, vec);
-        }
-    }
 }
 
 __device__ __forceinline__ void request4(const void *src, void *lds)
@@ -866,6 +879,7 @@ template <int BM_, int BV_, int WGM_, int NSTAGE_, bool STREAM_>
 struct Small {
     static constexpr int BM = BM_, BV = BV_, WGM = WGM_, NSTAGE = NSTAGE_;
     static constexpr bool STREAM = STREAM_;
+    static constexpr int PER_CU = 163840 / (NSTAGE_ * (BM_ + BV_) * 128);   // workgroups that the LDS holds
 };
 
 }  // namespace
@@ -910,25 +924,27 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
             return;
         }
         const bool words = blocks % 4 == 0 && (((uintptr_t)hs | (uintptr_t)ws) & 3) == 0;
-        auto small = [&](auto form, int64_t grid) {
+        auto small = [&](auto form) {
             using F = decltype(form);
+            const int64_t slots = std::max(8, cus / 8 * 8) * F::PER_CU;
+            const int64_t grid = std::min(tiles(F::BM, F::BV), slots);
             words ? go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, true, B>, grid, 256)
                  : go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, false, B>, grid, 256);
         };
         if (tiles(32, 32) <= cus)
-            return small(Small<32, 32, 2, 8, false>{}, tiles(32, 32));
+            return small(Small<32, 32, 2, 8, false>{});
         if (rows <= 32 && tiles(32, 128) >= cus)
-            return small(Small<32, 128, 1, 4, true>{}, tiles(32, 128));
+            return small(Small<32, 128, 1, 4, true>{});
         if (rows <= 32)
-            return small(Small<32, 64, 1, 4, true>{}, tiles(32, 64));
+            return small(Small<32, 64, 1, 4, true>{});
         if (rows <= 64 && tiles(64, 128) >= cus)
-            return small(Small<64, 128, 1, 3, true>{}, tiles(64, 128));
+            return small(Small<64, 128, 1, 3, true>{});
         if (rows <= 64)
-            return small(Small<64, 64, 2, 4, true>{}, tiles(64, 64));
+            return small(Small<64, 64, 2, 4, true>{});
         if (tiles(128, 128) < cus)
-            return small(Small<64, 64, 2, 4, false>{}, tiles(64, 64));
+            return small(Small<64, 64, 2, 4, false>{});
         if (!words)
-            return small(Small<128, 128, 2, 3, false>{}, tiles(128, 128));
+            return small(Small<128, 128, 2, 3, false>{});
         auto large = [&](auto bm_tag) {
             constexpr int BM = decltype(bm_tag)::value;
             const int64_t n = tiles(BM, 256);
