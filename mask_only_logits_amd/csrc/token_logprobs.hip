@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch_head.h"
 #include "row_ops.h"
@@ -27,6 +28,8 @@ using namespace rows;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 constexpr float kFar = -1000.0f;   // 2^kFar is 0
+constexpr int kAhead = 8;          // chunks of 16 bytes that a thread requests together
+constexpr int kPartsMax = 64, kPartTarget = 1024, kPartMin = 4096;
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -83,13 +86,26 @@ struct Sums {
         s = f * s;
         m = mx;
     }
+    // of the wave's lanes (lane 0's, as joins that round differently leave the lanes bits apart)
     __device__ __forceinline__ void join_wave(float c0)
     {
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1)
             join(__shfl_xor(m, o, 64), __shfl_xor(s, o, 64), __shfl_xor(u, o, 64), c0);
+        m = __shfl(m, 0, 64);
+        s = __shfl(s, 0, 64);
+        u = __shfl(u, 0, 64);
     }
 };
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&z)[N])
+{
+    float a = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    if constexpr (N == 8)
+        a = fmaxf(a, fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+    return a;
+}
 
 // The sums over a stream of logits.
 template <bool ENT>
@@ -118,11 +134,8 @@ struct RunningSums {
         u = f * (x.u + ref.off * x.s);
     }
     template <int N>
-    __device__ __forceinline__ void add(const float (&z)[N])
+    __device__ __forceinline__ void add(const float (&z)[N], float mx)   // mx: the largest
     {
-        float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-        if constexpr (N == 8)
-            mx = fmaxf(mx, fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
         if (mx > m)
             raise(mx);
         float e[N], w[N];
@@ -164,28 +177,34 @@ struct Row {
 
 // Chunks of N logits of [lo, hi), lo a multiple of N: chunk i of this thread's is
 // lo / N + threadIdx.x + i * NT.  UN loads are issued before their values are used.  The chunk
-// that hi cuts is filled up with -inf.
+// that hi cuts is filled up with -inf, and is thread NT - 1's.
 template <bool BF16, int NT, int UN, bool STREAM, typename F>
 __device__ __forceinline__ void for_chunks(const TokenLogprobs &a, int64_t row, int lo, int hi, F f)
 {
     constexpr int N = kChunk<BF16>;
     const int64_t base = row * a.ldz;
     const int full = lo + (hi - lo) / N * N;
-    for (int v = lo + threadIdx.x * N; v < full; v += UN * NT * N) {
+    auto some = [&](int v, auto whole) __attribute__((always_inline)) {
+        constexpr bool W = decltype(whole)::value;
         Raw<BF16> r[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i)
-            if (v + i * NT * N < full)
+            if (W || v + i * NT * N < full)
                 r[i].template load<STREAM>(a.Z, base + v + i * NT * N);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            if (v + i * NT * N < full) {
+            if (W || v + i * NT * N < full) {
                 float z[N];
                 r[i].get(z);
                 f(z, v + i * NT * N, N);
             }
         }
-    }
+    };
+    int v = lo + threadIdx.x * N;
+    for (; v + (UN - 1) * NT * N < full; v += UN * NT * N)
+        some(v, std::true_type{});
+    if (v < full)
+        some(v, std::false_type{});
     if (full < hi && threadIdx.x == NT - 1) {
         Raw<BF16> r;
         r.fill(-kInf);
@@ -213,12 +232,13 @@ constexpr uint32_t kOrderOfMinusInf = 0x007fffffu;   // keys above this value's 
 
 // Words of LDS that select_top takes beside its list.
 constexpr int kSelectWords = 256 + 4;
+constexpr int kListMax = 512;
 
-// The keys of the row's n largest logits above -inf into list[0 .. return value), in any order; NT
+// The keys of the n largest logits of [lo, hi) above -inf into list[0 .. return value), in any order; NT
 // threads.  Digits of the n-th largest key are found one after another, eight bits a pass over
 // the row, so this takes up to nine passes, whatever the logits.
 template <bool BF16, int NT>
-__device__ int select_top(const TokenLogprobs &a, int64_t row, int n, uint64_t *list, int32_t *lds)
+__device__ int select_top(const TokenLogprobs &a, int64_t row, int lo, int hi, int n, uint64_t *list, int32_t *lds)
 {
     int32_t *hist = lds, *found = lds + 256;   // found: digit, still needed, all taken, entries listed
     uint64_t prefix = 0;
@@ -228,7 +248,7 @@ __device__ int select_top(const TokenLogprobs &a, int64_t row, int n, uint64_t *
         for (int i = threadIdx.x; i < 256; i += NT)
             hist[i] = 0;
         __syncthreads();
-        for_chunks<BF16, NT, 4, false>(a, row, 0, a.V, [&](auto &z, int v, int cnt) {
+        for_chunks<BF16, NT, 4, false>(a, row, lo, hi, [&](auto &z, int v, int cnt) {
 #pragma unroll
             for (int i = 0; i < kChunk<BF16>; ++i) {
                 const uint64_t key = key_of(z[i], v + i);
@@ -284,7 +304,7 @@ __device__ int select_top(const TokenLogprobs &a, int64_t row, int n, uint64_t *
     if (threadIdx.x == 0)
         found[3] = 0;
     __syncthreads();
-    for_chunks<BF16, NT, 4, false>(a, row, 0, a.V, [&](auto &z, int v, int cnt) {
+    for_chunks<BF16, NT, 4, false>(a, row, lo, hi, [&](auto &z, int v, int cnt) {
 #pragma unroll
         for (int i = 0; i < kChunk<BF16>; ++i) {
             const uint64_t key = key_of(z[i], v + i);
@@ -299,23 +319,141 @@ __device__ int select_top(const TokenLogprobs &a, int64_t row, int n, uint64_t *
     return min(found[3], n);
 }
 
-// Writes the row's alternatives from a list of `listed` keys that holds the n largest: each
-// thread counts the keys above its own.  Places without one take -1 and -inf.
-template <int NT>
+// A thread's largest logit and the chunk that holds it, and the largest maximum of its other chunks.
+struct Best {
+    float m = -kInf, m2 = -kInf;
+    int at = 0;
+
+    __device__ __forceinline__ void add(float mx, int v)
+    {
+        m2 = fmaxf(m2, fminf(mx, m));
+        at = mx > m ? v : at;
+        m = fmaxf(m, mx);
+    }
+};
+
+// LDS of the search for the top n.
+struct TopLds {
+    uint64_t key[256];
+    uint64_t list[kListMax];
+    uint64_t least;
+    int32_t listed;
+    int32_t words[kSelectWords];
+};
+
+// A key that n of the workgroup's logits reach, from one key of a logit (or 0) of each of its 256
+// threads: the n-th largest of the keys, of groups of four threads for small n.  The lowest key that
+// counts where there are fewer.
+__device__ __forceinline__ uint64_t least_key(uint64_t mine, int n, TopLds &lds)
+{
+    const int t = threadIdx.x;
+    int groups = 256;
+    if (n <= 32) {
+        groups = 64;
+#pragma unroll
+        for (int o = 32; o >= 16; o >>= 1)
+            mine = max(mine, (uint64_t)__shfl_xor((unsigned long long)mine, o, 64));
+        if ((t & 63) < 16)
+            lds.key[(t >> 6) * 16 + (t & 15)] = mine;
+    } else {
+        lds.key[t] = mine;
+    }
+    if (t == 0) {
+        lds.least = (uint64_t)(kOrderOfMinusInf + 1) << 32;
+        lds.listed = 0;
+    }
+    __syncthreads();
+    if (t < groups) {
+        const uint64_t k = lds.key[t];
+        int above = 0;
+#pragma unroll 16
+        for (int j = 0; j < groups; ++j)
+            above += lds.key[j] > k;
+        if (k != 0 && above == n - 1)   // (keys of logits are distinct)
+            lds.least = k;
+    }
+    __syncthreads();
+    return lds.least;
+}
+
+__device__ __forceinline__ void list_key(uint64_t key, TopLds &lds)
+{
+    const int at = atomicAdd(&lds.listed, 1);
+    if (at < kListMax)
+        lds.list[at] = key;
+}
+
+// The keys of [lo, hi)'s n largest logits, and of some below, into lds.list; how many.  256 threads,
+// each with the `best` of its chunks.  Chunks with a logit that may count are read again: of a
+// thread the one with its maximum, and where another may hold one all of them.
+template <bool BF16>
+__device__ int list_top(const TokenLogprobs &a, int64_t row, int lo, int hi, const Best &best, TopLds &lds)
+{
+    constexpr int N = kChunk<BF16>, NT = 256;
+    const int lane = threadIdx.x & 63, full = lo + (hi - lo) / N * N;
+    // (of the maximum's chunk the last entry, as the place of the maximum in it is not known)
+    const uint64_t least = least_key(best.m > -kInf ? key_of(best.m, best.at + N - 1) : 0, a.top_n, lds);
+    auto look = [&](int v) __attribute__((always_inline)) {
+        Raw<BF16> r;
+        r.fill(-kInf);
+        if (v < full)
+            r.load(a.Z, row * a.ldz + v);
+        else
+            r.load_part(a.Z, row * a.ldz + v, hi - v);
+        float z[N];
+        r.get(z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint64_t key = key_of(z[i], v + i);
+            if (key >= least)   // (what fills a chunk up is -inf)
+                list_key(key, lds);
+        }
+    };
+    auto counts = [&](float z) { return z > -kInf && order_of(z) >= (uint32_t)(least >> 32); };
+    if (counts(best.m))
+        look(best.at);
+    for (uint64_t more = __ballot(counts(best.m2)); more != 0; more &= more - 1) {
+        const int from = __builtin_ctzll(more), t = (int)(threadIdx.x & ~63u) + from;
+        const int seen = __shfl(best.at, from, 64);
+        for (int64_t v = lo + ((int64_t)lane * NT + t) * N; v < full; v += (int64_t)64 * NT * N)
+            if (v != seen)
+                look((int)v);
+        if (t == NT - 1 && lane == 0 && full < hi && full != seen)
+            look(full);
+    }
+    __syncthreads();
+    int listed = lds.listed;
+    if (listed > kListMax)
+        listed = select_top<BF16, NT>(a, row, lo, hi, a.top_n, lds.list, lds.words);
+    return listed;
+}
+
+// Calls put(place, key) for the n largest keys other than 0 of a list: each thread counts the keys
+// above its own.
+template <typename F>
+__device__ __forceinline__ void place_top(const uint64_t *list, int listed, int n, F put)
+{
+    for (int i = threadIdx.x; i < listed; i += 256) {
+        const uint64_t key = list[i];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < listed; ++j)
+            place += list[j] > key;
+        if (place < n && key != 0)
+            put(place, key);
+    }
+}
+
+// Writes the row's alternatives from a list with its n largest keys, all there are if those are
+// fewer.  Places without one take -1 and -inf.
 __device__ __forceinline__ void write_top(const TokenLogprobs &a, int64_t row, const Row &x, const uint64_t *list,
                                           int listed)
 {
-    for (int i = threadIdx.x; i < listed; i += NT) {
-        const uint64_t key = list[i];
-        int place = 0;
-        for (int j = 0; j < listed; ++j)
-            place += list[j] > key;
-        if (place < a.top_n) {
-            a.top_ids[row * a.top_n + place] = index_of(key);
-            a.top_logprobs[row * a.top_n + place] = exponent(value_of(key), x.m, a.temperature) - x.l;
-        }
-    }
-    for (int i = listed + threadIdx.x; i < a.top_n; i += NT) {
+    place_top(list, listed, a.top_n, [&](int place, uint64_t key) {
+        a.top_ids[row * a.top_n + place] = index_of(key);
+        a.top_logprobs[row * a.top_n + place] = exponent(value_of(key), x.m, a.temperature) - x.l;
+    });
+    for (int i = listed + threadIdx.x; i < a.top_n; i += 256) {
         a.top_ids[row * a.top_n + i] = -1;
         a.top_logprobs[row * a.top_n + i] = x.fine ? -kInf : x.l;
     }
@@ -332,41 +470,161 @@ __device__ __forceinline__ void write_row(const TokenLogprobs &a, int64_t row, c
         a.entropy[row] = x.H;
 }
 
-// One row per workgroup.
-template <bool BF16, int NT, bool ENT>
-__global__ __launch_bounds__(NT) void token_logprobs_row_kernel(const TokenLogprobs a)
+// The token of a row, and its logit.
+struct Token {
+    bool given = false;
+    float z = 0.0f;
+
+    template <bool BF16>
+    __device__ __forceinline__ void load(const TokenLogprobs &a, int64_t row)
+    {
+        const int32_t t = a.tokens ? a.tokens[row] : -1;
+        given = t >= 0 && t < a.V;
+        if (given)
+            z = load1(a.Z, row * a.ldz + t, BF16);
+    }
+};
+
+// The sums of [lo, hi) of a row in every thread of 256, and the thread's own best.  A thread's sums
+// start anew every 512 chunks, so that their rounding does not grow with the row.
+template <bool BF16, bool ENT, bool TOP>
+__device__ __forceinline__ Sums scan(const TokenLogprobs &a, int64_t row, int lo, int hi, Best &best, float *part)
 {
-    constexpr int NW = NT / 64;
-    __shared__ float part[3 * NW];
-    __shared__ int32_t words[kSelectWords];
-    __shared__ uint64_t list[kTopMax];
+    constexpr int NT = 256, NW = NT / 64, N = kChunk<BF16>, RUN = 512 * NT * N;
     const float c0 = kLog2e / a.temperature;
+    Sums x;
+    for (int at = lo; at < hi; at += RUN) {
+        RunningSums<ENT> run(c0);
+        for_chunks<BF16, NT, kAhead, true>(a, row, at, min(hi, at + RUN), [&](auto &z, int v, int) {
+            const float mx = max_of(z);
+            if constexpr (TOP)
+                best.add(mx, v);
+            run.add(z, mx);
+        });
+        const Sums y = run.done();
+        x.join(y.m, y.s, y.u, c0);
+    }
+    x.join_wave(c0);
+    if ((threadIdx.x & 63) == 0) {
+        part[threadIdx.x >> 6] = x.m;
+        part[NW + (threadIdx.x >> 6)] = x.s;
+        part[2 * NW + (threadIdx.x >> 6)] = x.u;
+    }
+    __syncthreads();
+    x = Sums();
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        x.join(part[w], part[NW + w], part[2 * NW + w], c0);
+    return x;
+}
+
+// One row per workgroup.
+template <bool BF16, bool ENT, bool TOP>
+__global__ __launch_bounds__(256) void token_logprobs_row_kernel(const TokenLogprobs a)
+{
+    __shared__ float part[12];
+    __shared__ TopLds lds;
     const int64_t n = row_count(a.count, a.rows);
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        RunningSums<ENT> run(c0);
-        for_chunks<BF16, NT, 4, false>(a, row, 0, a.V, [&](auto &z, int, int) { run.add(z); });
-        Sums x = run.done();
-        x.join_wave(c0);
-        if ((threadIdx.x & 63) == 0) {
-            part[threadIdx.x >> 6] = x.m;
-            part[NW + (threadIdx.x >> 6)] = x.s;
-            part[2 * NW + (threadIdx.x >> 6)] = x.u;
-        }
-        __syncthreads();
-        x = Sums();
-        for (int w = 0; w < NW; ++w)
-            x.join(part[w], part[NW + w], part[2 * NW + w], c0);
-        const Row r(x);
-        if (threadIdx.x == 0) {
-            const int32_t t = a.tokens ? a.tokens[row] : -1;
-            const bool token = t >= 0 && t < a.V;
-            write_row(a, row, r, token ? load1(a.Z, row * a.ldz + t, BF16) : 0.0f, token);
-        }
-        if (a.top_n > 0) {
-            const int listed = r.fine ? select_top<BF16, NT>(a, row, a.top_n, list, words) : 0;
-            write_top<NT>(a, row, r, list, listed);
+        Token token;
+        if (threadIdx.x == 0)
+            token.load<BF16>(a, row);
+        Best best;
+        const Row r(scan<BF16, ENT, TOP>(a, row, 0, a.V, best, part));
+        if (threadIdx.x == 0)
+            write_row(a, row, r, token.z, token.given);
+        if constexpr (TOP) {
+            const int listed = r.fine ? list_top<BF16>(a, row, 0, a.V, best, lds) : 0;
+            write_top(a, row, r, lds.list, listed);
         }
         __syncthreads();   // the LDS is taken again for the next row
+    }
+}
+
+// What a split row's parts leave in the workspace: top_n keys of each, those without a logit 0, then
+// m, s and u of each.
+struct Parts {
+    uint64_t *keys;
+    float *sums;
+    int parts;
+
+    __host__ __device__ Parts(const TokenLogprobs &a, int parts_) : parts(parts_)
+    {
+        keys = (uint64_t *)a.workspace;
+        sums = (float *)(keys + a.rows * parts * a.top_n);
+    }
+};
+
+// A part of a row per workgroup.
+template <bool BF16, bool ENT, bool TOP>
+__global__ __launch_bounds__(256) void token_logprobs_part_kernel(const TokenLogprobs a, const Parts out)
+{
+    __shared__ float part[12];
+    __shared__ TopLds lds;
+    const int64_t n = row_count(a.count, a.rows);
+    const int parts = out.parts, chunks = (a.V + 7) / 8, each = (chunks + parts - 1) / parts;
+    for (int64_t b = blockIdx.x; b < n * parts; b += gridDim.x) {
+        const int64_t row = b / parts;
+        const int s = (int)(b % parts);
+        const int lo = min(s * each, chunks) * 8, hi = max(lo, min(min((s + 1) * each, chunks) * 8, a.V));
+        Best best;
+        const Sums x = scan<BF16, ENT, TOP>(a, row, min(lo, hi), hi, best, part);
+        if (threadIdx.x == 0) {
+            out.sums[3 * b] = x.m;
+            out.sums[3 * b + 1] = x.s;
+            out.sums[3 * b + 2] = x.u;
+        }
+        if constexpr (TOP) {
+            const int listed = list_top<BF16>(a, row, lo, hi, best, lds);
+            uint64_t *keys = out.keys + b * a.top_n;
+            place_top(lds.list, listed, a.top_n, [&](int place, uint64_t key) { keys[place] = key; });
+            for (int i = listed + threadIdx.x; i < a.top_n; i += 256)
+                keys[i] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the parts of a row, kPartsMax at most.
+template <bool BF16, bool TOP>
+__global__ __launch_bounds__(256) void token_logprobs_join_kernel(const TokenLogprobs a, const Parts in)
+{
+    __shared__ uint64_t all[TOP ? kPartsMax * kTopMax : 1];
+    __shared__ TopLds lds;
+    const int64_t n = row_count(a.count, a.rows);
+    const float c0 = kLog2e / a.temperature;
+    for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+        Token token;
+        if (threadIdx.x == 0)
+            token.load<BF16>(a, row);
+        Sums x;
+        const int lane = threadIdx.x & 63;
+        if (lane < in.parts) {
+            const float *p = in.sums + 3 * (row * in.parts + lane);
+            x.m = p[0];
+            x.s = p[1];
+            x.u = p[2];
+        }
+        x.join_wave(c0);
+        const Row r(x);
+        if (threadIdx.x == 0)
+            write_row(a, row, r, token.z, token.given);
+        if constexpr (TOP) {
+            const int total = r.fine ? in.parts * a.top_n : 0;
+            uint64_t mine = 0;
+            for (int i = threadIdx.x; i < total; i += 256) {
+                all[i] = in.keys[row * in.parts * a.top_n + i];
+                mine = max(mine, all[i]);
+            }
+            const uint64_t least = least_key(mine, a.top_n, lds);
+            for (int i = threadIdx.x; i < total; i += 256)
+                if (all[i] >= least)
+                    list_key(all[i], lds);
+            __syncthreads();
+            const int listed = lds.listed;
+            write_top(a, row, r, listed > kListMax ? all : lds.list, listed > kListMax ? total : listed);
+        }
+        __syncthreads();
     }
 }
 
@@ -402,14 +660,32 @@ __global__ __launch_bounds__(NT) void token_logprobs_grad_kernel(const TokenLogp
     }
 }
 
+// Parts of a row: few rows are split so that the chip is filled.  (The workspace's size is the same
+// on every device, so this counts with 256 CUs.)
+int parts_of(int64_t rows, int64_t V)
+{
+    const int64_t n = std::min<int64_t>({kPartsMax, kPartTarget / std::max<int64_t>(rows, 1), V / kPartMin});
+    return (int)std::max<int64_t>(n, 1);
+}
+
 template <bool BF16>
 hipError_t run(const TokenLogprobs &a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20));
-    if (a.entropy)
-        hipLaunchKernelGGL((token_logprobs_row_kernel<BF16, 1024, true>), grid, dim3(1024), 0, stream, a);
-    else
-        hipLaunchKernelGGL((token_logprobs_row_kernel<BF16, 1024, false>), grid, dim3(1024), 0, stream, a);
+    const int parts = parts_of(a.rows, a.V);
+    const dim3 rows((unsigned)std::min<int64_t>(a.rows, 1 << 20));
+    const Parts p(a, parts);
+    auto go = [&](auto ent, auto top) {
+        constexpr bool E = decltype(ent)::value, T = decltype(top)::value;
+        if (parts == 1) {
+            hipLaunchKernelGGL((token_logprobs_row_kernel<BF16, E, T>), rows, dim3(256), 0, stream, a);
+            return;
+        }
+        hipLaunchKernelGGL((token_logprobs_part_kernel<BF16, E, T>), dim3((unsigned)(a.rows * parts)), dim3(256), 0,
+                           stream, a, p);
+        hipLaunchKernelGGL((token_logprobs_join_kernel<BF16, T>), rows, dim3(256), 0, stream, a, p);
+    };
+    auto with = [&](auto ent) { a.top_n > 0 ? go(ent, std::true_type{}) : go(ent, std::false_type{}); };
+    a.entropy ? with(std::true_type{}) : with(std::false_type{});
     return hipGetLastError();
 }
 
@@ -424,7 +700,11 @@ hipError_t run_grad(const TokenLogprobs &a, hipStream_t stream)
 
 }  // namespace
 
-int64_t token_logprobs_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t V, int64_t top_n)
+{
+    const int64_t parts = parts_of(rows, V);
+    return parts == 1 || rows == 0 ? 0 : rows * parts * (8 * top_n + 12);
+}
 
 hipError_t launch_token_logprobs(const TokenLogprobs &a, bool z_bf16, hipStream_t stream)
 {
