@@ -175,43 +175,50 @@ struct Row {
     }
 };
 
-// Chunks of N logits of [lo, hi), lo a multiple of N: chunk i of this thread's is
-// lo / N + threadIdx.x + i * NT.  UN loads are issued before their values are used.  The chunk
-// that hi cuts is filled up with -inf, and is thread NT - 1's.
+// Calls f(z, v, count, round) for this thread's chunks z of N logits of [lo, hi), lo a multiple of N:
+// in round c the one at v = lo + (c NT + threadIdx.x) N.  UN loads are issued before their values are
+// used.  The chunk that hi cuts is filled up with -inf.  (Rounds that all threads take are counted
+// in scalar registers, and their loads have a scalar base.)
 template <bool BF16, int NT, int UN, bool STREAM, typename F>
 __device__ __forceinline__ void for_chunks(const TokenLogprobs &a, int64_t row, int lo, int hi, F f)
 {
     constexpr int N = kChunk<BF16>;
-    const int64_t base = row * a.ldz;
-    const int full = lo + (hi - lo) / N * N;
-    auto some = [&](int v, auto whole) __attribute__((always_inline)) {
+    const int t = threadIdx.x, rounds = (hi - lo) / (NT * N);
+    const char *from = (const char *)a.Z + (row * a.ldz + lo) * (16 / N);
+    auto some = [&](int c, auto whole) __attribute__((always_inline)) {
         constexpr bool W = decltype(whole)::value;
         Raw<BF16> r[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i)
-            if (W || v + i * NT * N < full)
-                r[i].template load<STREAM>(a.Z, base + v + i * NT * N);
+            if (W || c + i < rounds)
+                r[i].template load<STREAM>(from + (int64_t)(c + i) * (NT * 16) + t * 16u, 0);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            if (W || v + i * NT * N < full) {
+            if (W || c + i < rounds) {
                 float z[N];
                 r[i].get(z);
-                f(z, v + i * NT * N, N);
+                f(z, lo + ((c + i) * NT + t) * N, N, c + i);
             }
         }
     };
-    int v = lo + threadIdx.x * N;
-    for (; v + (UN - 1) * NT * N < full; v += UN * NT * N)
-        some(v, std::true_type{});
-    if (v < full)
-        some(v, std::false_type{});
-    if (full < hi && threadIdx.x == NT - 1) {
-        Raw<BF16> r;
+    int c = 0;
+    for (; c + UN <= rounds; c += UN)
+        some(c, std::true_type{});
+    const int v = lo + (rounds * NT + t) * N;
+    Raw<BF16> r;
+    if (v + N <= hi) {
+        r.template load<STREAM>(from + (int64_t)rounds * (NT * 16) + t * 16u, 0);
+    } else {
         r.fill(-kInf);
-        r.load_part(a.Z, base + full, hi - full);
+        if (v < hi)
+            r.load_part(a.Z, row * a.ldz + v, hi - v);
+    }
+    if (c < rounds)
+        some(c, std::false_type{});
+    if (v < hi) {
         float z[N];
         r.get(z);
-        f(z, full, hi - full);
+        f(z, v, min(N, hi - v), rounds);
     }
 }
 
@@ -236,7 +243,7 @@ constexpr int kListMax = 512;
 
 // The keys of the n largest logits of [lo, hi) above -inf into list[0 .. return value), in any order; NT
 // threads.  Digits of the n-th largest key are found one after another, eight bits a pass over
-// the row, so this takes up to nine passes, whatever the logits.
+// the row, so this takes up to nine passes, whatever the logits; they are written for few registers.
 template <bool BF16, int NT>
 __device__ int select_top(const TokenLogprobs &a, int64_t row, int lo, int hi, int n, uint64_t *list, int32_t *lds)
 {
@@ -244,18 +251,17 @@ __device__ int select_top(const TokenLogprobs &a, int64_t row, int lo, int hi, i
     uint64_t prefix = 0;
     int need = n;
     bool all = false;
+#pragma unroll 1
     for (int shift = 56; shift >= 0 && !all; shift -= 8) {
         for (int i = threadIdx.x; i < 256; i += NT)
             hist[i] = 0;
         __syncthreads();
-        for_chunks<BF16, NT, 4, false>(a, row, lo, hi, [&](auto &z, int v, int cnt) {
-#pragma unroll
-            for (int i = 0; i < kChunk<BF16>; ++i) {
-                const uint64_t key = key_of(z[i], v + i);
-                if (i < cnt && (uint32_t)(key >> 32) > kOrderOfMinusInf && (shift == 56 || key >> (shift + 8) == prefix))
-                    atomicAdd(&hist[(int)(key >> shift) & 255], 1);
-            }
-        });
+#pragma unroll 1
+        for (int v = lo + threadIdx.x; v < hi; v += NT) {
+            const uint64_t key = key_of(load1(a.Z, row * a.ldz + v, BF16), v);
+            if ((uint32_t)(key >> 32) > kOrderOfMinusInf && (shift == 56 || key >> (shift + 8) == prefix))
+                atomicAdd(&hist[(int)(key >> shift) & 255], 1);
+        }
         __syncthreads();
         if (threadIdx.x < 64) {
             // lane i: digits 255 - 4 i and the three below; how many lie above them
@@ -304,30 +310,28 @@ __device__ int select_top(const TokenLogprobs &a, int64_t row, int lo, int hi, i
     if (threadIdx.x == 0)
         found[3] = 0;
     __syncthreads();
-    for_chunks<BF16, NT, 4, false>(a, row, lo, hi, [&](auto &z, int v, int cnt) {
-#pragma unroll
-        for (int i = 0; i < kChunk<BF16>; ++i) {
-            const uint64_t key = key_of(z[i], v + i);
-            if (i < cnt && (uint32_t)(key >> 32) > kOrderOfMinusInf && key >= prefix) {
-                const int at = atomicAdd(&found[3], 1);
-                if (at < kTopMax)   // (n at most)
-                    list[at] = key;
-            }
+#pragma unroll 1
+    for (int v = lo + threadIdx.x; v < hi; v += NT) {
+        const uint64_t key = key_of(load1(a.Z, row * a.ldz + v, BF16), v);
+        if ((uint32_t)(key >> 32) > kOrderOfMinusInf && key >= prefix) {
+            const int at = atomicAdd(&found[3], 1);
+            if (at < kTopMax)   // (n at most)
+                list[at] = key;
         }
-    });
+    }
     __syncthreads();
     return min(found[3], n);
 }
 
-// A thread's largest logit and the chunk that holds it, and the largest maximum of its other chunks.
+// A thread's largest logit and the round of the chunk that holds it, and the largest maximum of its other chunks.
 struct Best {
     float m = -kInf, m2 = -kInf;
     int at = 0;
 
-    __device__ __forceinline__ void add(float mx, int v)
+    __device__ __forceinline__ void add(float mx, int round)
     {
         m2 = fmaxf(m2, fminf(mx, m));
-        at = mx > m ? v : at;
+        at = mx > m ? round : at;
         m = fmaxf(m, mx);
     }
 };
@@ -390,16 +394,18 @@ template <bool BF16>
 __device__ int list_top(const TokenLogprobs &a, int64_t row, int lo, int hi, const Best &best, TopLds &lds)
 {
     constexpr int N = kChunk<BF16>, NT = 256;
-    const int lane = threadIdx.x & 63, full = lo + (hi - lo) / N * N;
+    auto chunk = [&](int64_t round, int t) { return lo + (round * NT + t) * N; };
     // (of the maximum's chunk the last entry, as the place of the maximum in it is not known)
-    const uint64_t least = least_key(best.m > -kInf ? key_of(best.m, best.at + N - 1) : 0, a.top_n, lds);
+    const uint64_t least =
+        least_key(best.m > -kInf ? key_of(best.m, (int)chunk(best.at, threadIdx.x) + N - 1) : 0, a.top_n, lds);
     auto look = [&](int v) __attribute__((always_inline)) {
         Raw<BF16> r;
-        r.fill(-kInf);
-        if (v < full)
+        if (v + N <= hi) {
             r.load(a.Z, row * a.ldz + v);
-        else
+        } else {
+            r.fill(-kInf);
             r.load_part(a.Z, row * a.ldz + v, hi - v);
+        }
         float z[N];
         r.get(z);
 #pragma unroll
@@ -411,15 +417,13 @@ __device__ int list_top(const TokenLogprobs &a, int64_t row, int lo, int hi, con
     };
     auto counts = [&](float z) { return z > -kInf && order_of(z) >= (uint32_t)(least >> 32); };
     if (counts(best.m))
-        look(best.at);
+        look((int)chunk(best.at, threadIdx.x));
     for (uint64_t more = __ballot(counts(best.m2)); more != 0; more &= more - 1) {
         const int from = __builtin_ctzll(more), t = (int)(threadIdx.x & ~63u) + from;
         const int seen = __shfl(best.at, from, 64);
-        for (int64_t v = lo + ((int64_t)lane * NT + t) * N; v < full; v += (int64_t)64 * NT * N)
-            if (v != seen)
-                look((int)v);
-        if (t == NT - 1 && lane == 0 && full < hi && full != seen)
-            look(full);
+        for (int c = threadIdx.x & 63; chunk(c, t) < hi; c += 64)
+            if (c != seen)
+                look((int)chunk(c, t));
     }
     __syncthreads();
     int listed = lds.listed;
@@ -490,15 +494,15 @@ struct Token {
 template <bool BF16, bool ENT, bool TOP>
 __device__ __forceinline__ Sums scan(const TokenLogprobs &a, int64_t row, int lo, int hi, Best &best, float *part)
 {
-    constexpr int NT = 256, NW = NT / 64, N = kChunk<BF16>, RUN = 512 * NT * N;
+    constexpr int NT = 256, NW = NT / 64, ROUNDS = 512, RUN = ROUNDS * NT * kChunk<BF16>;
     const float c0 = kLog2e / a.temperature;
     Sums x;
-    for (int at = lo; at < hi; at += RUN) {
+    for (int at = lo, before = 0; at < hi; at += RUN, before += ROUNDS) {
         RunningSums<ENT> run(c0);
-        for_chunks<BF16, NT, kAhead, true>(a, row, at, min(hi, at + RUN), [&](auto &z, int v, int) {
+        for_chunks<BF16, NT, kAhead, true>(a, row, at, min(hi, at + RUN), [&](auto &z, int, int, int round) {
             const float mx = max_of(z);
             if constexpr (TOP)
-                best.add(mx, v);
+                best.add(mx, before + round);
             run.add(z, mx);
         });
         const Sums y = run.done();
@@ -525,19 +529,19 @@ __global__ __launch_bounds__(256) void token_logprobs_row_kernel(const TokenLogp
     __shared__ float part[12];
     __shared__ TopLds lds;
     const int64_t n = row_count(a.count, a.rows);
-    for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        Token token;
-        if (threadIdx.x == 0)
-            token.load<BF16>(a, row);
-        Best best;
-        const Row r(scan<BF16, ENT, TOP>(a, row, 0, a.V, best, part));
-        if (threadIdx.x == 0)
-            write_row(a, row, r, token.z, token.given);
-        if constexpr (TOP) {
-            const int listed = r.fine ? list_top<BF16>(a, row, 0, a.V, best, lds) : 0;
-            write_top(a, row, r, lds.list, listed);
-        }
-        __syncthreads();   // the LDS is taken again for the next row
+    const int64_t row = blockIdx.x;
+    if (row >= n)
+        return;
+    Token token;
+    if (threadIdx.x == 0)
+        token.load<BF16>(a, row);
+    Best best;
+    const Row r(scan<BF16, ENT, TOP>(a, row, 0, a.V, best, part));
+    if (threadIdx.x == 0)
+        write_row(a, row, r, token.z, token.given);
+    if constexpr (TOP) {
+        const int listed = r.fine ? list_top<BF16>(a, row, 0, a.V, best, lds) : 0;
+        write_top(a, row, r, lds.list, listed);
     }
 }
 
@@ -563,25 +567,25 @@ __global__ __launch_bounds__(256) void token_logprobs_part_kernel(const TokenLog
     __shared__ TopLds lds;
     const int64_t n = row_count(a.count, a.rows);
     const int parts = out.parts, chunks = (a.V + 7) / 8, each = (chunks + parts - 1) / parts;
-    for (int64_t b = blockIdx.x; b < n * parts; b += gridDim.x) {
-        const int64_t row = b / parts;
-        const int s = (int)(b % parts);
-        const int lo = min(s * each, chunks) * 8, hi = max(lo, min(min((s + 1) * each, chunks) * 8, a.V));
-        Best best;
-        const Sums x = scan<BF16, ENT, TOP>(a, row, min(lo, hi), hi, best, part);
-        if (threadIdx.x == 0) {
-            out.sums[3 * b] = x.m;
-            out.sums[3 * b + 1] = x.s;
-            out.sums[3 * b + 2] = x.u;
-        }
-        if constexpr (TOP) {
-            const int listed = list_top<BF16>(a, row, lo, hi, best, lds);
-            uint64_t *keys = out.keys + b * a.top_n;
-            place_top(lds.list, listed, a.top_n, [&](int place, uint64_t key) { keys[place] = key; });
-            for (int i = listed + threadIdx.x; i < a.top_n; i += 256)
-                keys[i] = 0;
-        }
-        __syncthreads();
+    const int64_t b = blockIdx.x;
+    if (b >= n * parts)
+        return;
+    const int64_t row = b / parts;
+    const int s = (int)(b % parts);
+    const int lo = min(s * each, chunks) * 8, hi = max(lo, min(min((s + 1) * each, chunks) * 8, a.V));
+    Best best;
+    const Sums x = scan<BF16, ENT, TOP>(a, row, min(lo, hi), hi, best, part);
+    if (threadIdx.x == 0) {
+        out.sums[3 * b] = x.m;
+        out.sums[3 * b + 1] = x.s;
+        out.sums[3 * b + 2] = x.u;
+    }
+    if constexpr (TOP) {
+        const int listed = list_top<BF16>(a, row, lo, hi, best, lds);
+        uint64_t *keys = out.keys + b * a.top_n;
+        place_top(lds.list, listed, a.top_n, [&](int place, uint64_t key) { keys[place] = key; });
+        for (int i = listed + threadIdx.x; i < a.top_n; i += 256)
+            keys[i] = 0;
     }
 }
 
@@ -593,38 +597,38 @@ __global__ __launch_bounds__(256) void token_logprobs_join_kernel(const TokenLog
     __shared__ TopLds lds;
     const int64_t n = row_count(a.count, a.rows);
     const float c0 = kLog2e / a.temperature;
-    for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        Token token;
-        if (threadIdx.x == 0)
-            token.load<BF16>(a, row);
-        Sums x;
-        const int lane = threadIdx.x & 63;
-        if (lane < in.parts) {
-            const float *p = in.sums + 3 * (row * in.parts + lane);
-            x.m = p[0];
-            x.s = p[1];
-            x.u = p[2];
+    const int64_t row = blockIdx.x;
+    if (row >= n)
+        return;
+    Token token;
+    if (threadIdx.x == 0)
+        token.load<BF16>(a, row);
+    Sums x;
+    const int lane = threadIdx.x & 63;
+    if (lane < in.parts) {
+        const float *p = in.sums + 3 * (row * in.parts + lane);
+        x.m = p[0];
+        x.s = p[1];
+        x.u = p[2];
+    }
+    x.join_wave(c0);
+    const Row r(x);
+    if (threadIdx.x == 0)
+        write_row(a, row, r, token.z, token.given);
+    if constexpr (TOP) {
+        const int total = r.fine ? in.parts * a.top_n : 0;
+        uint64_t mine = 0;
+        for (int i = threadIdx.x; i < total; i += 256) {
+            all[i] = in.keys[row * in.parts * a.top_n + i];
+            mine = max(mine, all[i]);
         }
-        x.join_wave(c0);
-        const Row r(x);
-        if (threadIdx.x == 0)
-            write_row(a, row, r, token.z, token.given);
-        if constexpr (TOP) {
-            const int total = r.fine ? in.parts * a.top_n : 0;
-            uint64_t mine = 0;
-            for (int i = threadIdx.x; i < total; i += 256) {
-                all[i] = in.keys[row * in.parts * a.top_n + i];
-                mine = max(mine, all[i]);
-            }
-            const uint64_t least = least_key(mine, a.top_n, lds);
-            for (int i = threadIdx.x; i < total; i += 256)
-                if (all[i] >= least)
-                    list_key(all[i], lds);
-            __syncthreads();
-            const int listed = lds.listed;
-            write_top(a, row, r, listed > kListMax ? all : lds.list, listed > kListMax ? total : listed);
-        }
+        const uint64_t least = least_key(mine, a.top_n, lds);
+        for (int i = threadIdx.x; i < total; i += 256)
+            if (all[i] >= least)
+                list_key(all[i], lds);
         __syncthreads();
+        const int listed = lds.listed;
+        write_top(a, row, r, listed > kListMax ? all : lds.list, listed > kListMax ? total : listed);
     }
 }
 
@@ -648,7 +652,7 @@ __global__ __launch_bounds__(NT) void token_logprobs_grad_kernel(const TokenLogp
         const float scale = fast_exp2(-ref.off) / expf(l);
         // log p + H = y ln 2 + this
         const float add = H - l - ref.off * kLn2;
-        for_chunks<BF16, NT, 4, false>(a, row, min(lo, hi), hi, [&](auto &z, int v, int cnt) {
+        for_chunks<BF16, NT, 4, false>(a, row, min(lo, hi), hi, [&](auto &z, int v, int cnt, int) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float y = ref.at(z[i]), p = scale * fast_exp2(y);
@@ -672,7 +676,7 @@ template <bool BF16>
 hipError_t run(const TokenLogprobs &a, hipStream_t stream)
 {
     const int parts = parts_of(a.rows, a.V);
-    const dim3 rows((unsigned)std::min<int64_t>(a.rows, 1 << 20));
+    const dim3 rows((unsigned)a.rows);   // (below 2^31)
     const Parts p(a, parts);
     auto go = [&](auto ent, auto top) {
         constexpr bool E = decltype(ent)::value, T = decltype(top)::value;
