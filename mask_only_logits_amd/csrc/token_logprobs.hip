@@ -28,8 +28,13 @@ using namespace rows;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 constexpr float kFar = -1000.0f;   // 2^kFar is 0
-constexpr int kAhead = 8;          // chunks of 16 bytes that a thread requests together
-constexpr int kPartsMax = 64, kPartTarget = 1024, kPartMin = 4096;
+// Chunks of 16 bytes that a thread requests together (1229 x 126464 bf16 with two alternatives: 60 us,
+// with four 64 us; short rows gain by four what long ones lose).
+constexpr int kAhead = 8;
+// Rows are split for kPartTarget workgroups, four on each of 256 CUs, into parts of kPartMin logits or
+// more (20 x 152064 with 20 alternatives: 14.8 us, parts of 4096 or 8192 15.4, whole 25.9; 4 x
+// 32000 with 64: whole 15.7, in parts of 8192 21.7, as the join has more keys to look at).
+constexpr int kPartsMax = 64, kPartTarget = 1024, kPartMin = 16384;
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -545,8 +550,8 @@ __global__ __launch_bounds__(256) void token_logprobs_row_kernel(const TokenLogp
     }
 }
 
-// What a split row's parts leave in the workspace: top_n keys of each, those without a logit 0, then
-// m, s and u of each.
+// What a split row's parts leave in the workspace: each part's largest key, each one's second and so
+// on, 0 without a logit, so that the join's threads get keys of all sizes; then m, s and u of each.
 struct Parts {
     uint64_t *keys;
     float *sums;
@@ -582,10 +587,10 @@ __global__ __launch_bounds__(256) void token_logprobs_part_kernel(const TokenLog
     }
     if constexpr (TOP) {
         const int listed = list_top<BF16>(a, row, lo, hi, best, lds);
-        uint64_t *keys = out.keys + b * a.top_n;
-        place_top(lds.list, listed, a.top_n, [&](int place, uint64_t key) { keys[place] = key; });
+        uint64_t *keys = out.keys + row * a.top_n * parts + s;
+        place_top(lds.list, listed, a.top_n, [&](int place, uint64_t key) { keys[place * parts] = key; });
         for (int i = listed + threadIdx.x; i < a.top_n; i += 256)
-            keys[i] = 0;
+            keys[i * parts] = 0;
     }
 }
 

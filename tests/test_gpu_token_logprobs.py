@@ -202,3 +202,28 @@ def test_long_rows_of_memory(m):
     g = torch.ones(M, device=DEV)
     grad = m.mosaic_token_logprobs_grad(z, t, st, g)
     head64.check_logprobs_grad(z[-2:], t[-2:], 1.0, g[-2:], None, grad[-2:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V,n", [(600, 40000, 20), (600, 130000, 3), (3, 130000, 20), (3, 130001, 64), (700, 5003, 5)])
+def test_largest_logits_close_together_in_memory(m, M, V, n, dtype):
+    """The largest logits in a few of every 256 chunks of 16 bytes, so that few threads see them all."""
+    z, t, _, _ = _draw(V, M, V, dtype)
+    v = torch.arange(V, device=z.device)
+    for lanes in (1, 2, 12):
+        x = torch.where(v // (8 if dtype == BF else 4) % 256 < lanes, z + 50, z)
+        head64.check_logprobs(x, t, 1.0, *m.mosaic_token_logprobs(x, t, top_n=n, with_entropy=True), f"{M} x {V}, {lanes}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,V,n", [(2, 2**20, 64), (1, 2**20 + 5, 63), (16, 2**20, 2)])
+def test_largest_logits_in_a_stretch_of_a_long_row(m, M, V, n, dtype):
+    """All of the largest logits at one end of the row, or in its middle, sorted either way."""
+    z, t, _, _ = _draw(V + n, M, V, dtype)
+    v = torch.arange(V, device=z.device)
+    for lo, hi in ((0, 9 * 16384), (V - 150000, V), (400000, 400064)):
+        x = torch.where((v >= lo) & (v < hi), z + 50, z)
+        head64.check_logprobs(x, t, 1.0, *m.mosaic_token_logprobs(x, t, top_n=n, with_entropy=True), f"{lo}:{hi}")
+    x = z.sort(dim=1).values
+    for y in (x, x.flip(1)):
+        head64.check_logprobs(y, t, 1.0, *m.mosaic_token_logprobs(y, t, top_n=n, with_entropy=True), "sorted")
