@@ -284,9 +284,13 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_block_kernel(const uint8_t *__
 // 128 bytes (eight blocks) a row requested straight to LDS, NSTAGE - 1 of them ahead, in a ring with
 // one barrier per step, the rows' 16-byte blocks XOR-swizzled.  The scale bytes of a wave's rows come
 // straight to registers, with the K tile's requests.  Several workgroups share a CU, and each goes
-// from tile to tile without letting its requests run dry (64 x 126464 x 4096: 77 us, 81 with a
-// workgroup per tile; 4096 x 126464 x 4000, 128 x 128 tiles: 3.5 ms, 4.4).  STREAM: W is read once (one row tile): its requests take
-// the streaming cache policy.
+// from tile to tile without letting its requests run dry (4096 x 126464 x 4000, 128 x 128 tiles: 3.5 ms,
+// 4.4 with a workgroup per tile).  STREAM: W is read once (one row tile): its requests take the streaming
+// cache policy.
+//
+// 20 x 152064 x 3584: 65 us, 4.6 TB/s of codes and scales; one row 52 us, 5.5 TB/s.  Between the two
+// lies the H tile, which every workgroup requests again with each W tile; tiles of 256 entries (62 us, one
+// row 55; 8 x 65536 x 8192: 66 us for 59) and K tiles of 64 bytes (99 us) gain nothing over these sizes.
 template <int BM, int BV, int WGM, int NSTAGE, bool STREAM, bool WORDS, bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_mxfp4_small_kernel(const uint8_t *__restrict__ Hq,
                                                                const uint8_t *__restrict__ hs,
@@ -931,15 +935,19 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
             words ? go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, true, B>, grid, 256)
                  : go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, false, B>, grid, 256);
         };
+        // Latency counts: eight stages, and a tile for each CU at most.
         if (tiles(32, 32) <= cus)
             return small(Small<32, 32, 2, 8, false>{});
         if (rows <= 32 && tiles(32, 128) >= cus)
             return small(Small<32, 128, 1, 4, true>{});
         if (rows <= 32)
             return small(Small<32, 64, 1, 4, true>{});
-        if (rows <= 64 && tiles(64, 128) >= cus)
+        // 33 to 64 rows over many entries take the large kernel's 128-row tiles, half empty or more,
+        // for its longer requests (64 x 126464 x 4096: 58 us, tiles of 64 x 128 77; 48 x 65536 x 4096: 30 us,
+        // 39; 33 x 152064 x 3584: 73 us, 70), if the scale rows are whole words.
+        if (rows <= 64 && !words && tiles(64, 128) >= cus)
             return small(Small<64, 128, 1, 3, true>{});
-        if (rows <= 64)
+        if (rows <= 64 && (!words || tiles(64, 128) < cus))
             return small(Small<64, 64, 2, 4, true>{});
         if (tiles(128, 128) < cus)
             return small(Small<64, 64, 2, 4, false>{});

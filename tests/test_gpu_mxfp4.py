@@ -170,3 +170,9 @@ def test_scales_at_any_address_and_guards(m, M, V, d):
     room = torch.full((M * V + 64,), 3.0, dtype=BF, device=DEV)
     m.mosaic_quantized_logits_mxfp4(hq, hs, wq, ws, out=room[:M * V].view(M, V))
     assert torch.equal(room[:M * V].view(M, V), want) and bool((room[M * V:] == 3).all())
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,V,d", [(33, 33000, 256), (64, 40001, 500), (48, 32769, 1504), (32, 70001, 160), (1, 70000, 544)])
+def test_few_rows_of_a_large_vocabulary(m, M, V, d, out):
+    test_logits(m, M, V, d, out)
