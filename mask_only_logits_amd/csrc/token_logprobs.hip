@@ -31,6 +31,7 @@ constexpr float kFar = -1000.0f;   // 2^kFar is 0
 // Chunks of 16 bytes that a thread requests together (1229 x 126464 bf16 with two alternatives: 60 us,
 // with four 64 us; short rows gain by four what long ones lose).
 constexpr int kAhead = 8;
+constexpr int64_t kLaunchRows = (int64_t)1 << 23;   // rows of a launch
 // Rows are split for kPartTarget workgroups, four on each of 256 CUs, into parts of kPartMin logits or
 // more (20 x 152064 with 20 alternatives: 14.8 us, parts of 4096 or 8192 15.4, whole 25.9; 4 x
 // 32000 with 64: whole 15.7, in parts of 8192 21.7, as the join has more keys to look at).
@@ -527,14 +528,14 @@ __device__ __forceinline__ Sums scan(const TokenLogprobs &a, int64_t row, int lo
     return x;
 }
 
-// One row per workgroup.
+// One row per workgroup, from row `from` on.
 template <bool BF16, bool ENT, bool TOP>
-__global__ __launch_bounds__(256) void token_logprobs_row_kernel(const TokenLogprobs a)
+__global__ __launch_bounds__(256) void token_logprobs_row_kernel(const TokenLogprobs a, int64_t from)
 {
     __shared__ float part[12];
     __shared__ TopLds lds;
     const int64_t n = row_count(a.count, a.rows);
-    const int64_t row = blockIdx.x;
+    const int64_t row = from + blockIdx.x;
     if (row >= n)
         return;
     Token token;
@@ -681,17 +682,19 @@ template <bool BF16>
 hipError_t run(const TokenLogprobs &a, hipStream_t stream)
 {
     const int parts = parts_of(a.rows, a.V);
-    const dim3 rows((unsigned)a.rows);   // (below 2^31)
     const Parts p(a, parts);
     auto go = [&](auto ent, auto top) {
         constexpr bool E = decltype(ent)::value, T = decltype(top)::value;
         if (parts == 1) {
-            hipLaunchKernelGGL((token_logprobs_row_kernel<BF16, E, T>), rows, dim3(256), 0, stream, a);
+            // (a launch holds fewer than 2^32 threads)
+            for (int64_t from = 0; from < a.rows; from += kLaunchRows)
+                hipLaunchKernelGGL((token_logprobs_row_kernel<BF16, E, T>),
+                                   dim3((unsigned)std::min(a.rows - from, kLaunchRows)), dim3(256), 0, stream, a, from);
             return;
         }
         hipLaunchKernelGGL((token_logprobs_part_kernel<BF16, E, T>), dim3((unsigned)(a.rows * parts)), dim3(256), 0,
                            stream, a, p);
-        hipLaunchKernelGGL((token_logprobs_join_kernel<BF16, T>), rows, dim3(256), 0, stream, a, p);
+        hipLaunchKernelGGL((token_logprobs_join_kernel<BF16, T>), dim3((unsigned)a.rows), dim3(256), 0, stream, a, p);
     };
     auto with = [&](auto ent) { a.top_n > 0 ? go(ent, std::true_type{}) : go(ent, std::false_type{}); };
     a.entropy ? with(std::true_type{}) : with(std::false_type{});

@@ -227,3 +227,24 @@ def test_largest_logits_in_a_stretch_of_a_long_row(m, M, V, n, dtype):
     x = z.sort(dim=1).values
     for y in (x, x.flip(1)):
         head64.check_logprobs(y, t, 1.0, *m.mosaic_token_logprobs(y, t, top_n=n, with_entropy=True), "sorted")
+
+
+def test_more_rows_than_a_launch_holds(m):
+    """17 million rows of one logit, or of two with one absent."""
+    M = 2**24 + 5
+    z = torch.randn(M, 1, device=DEV)
+    t = torch.zeros(M, dtype=torch.int32, device=DEV)
+    lp, H, ids, top, st = m.mosaic_token_logprobs(z, t, top_n=1, with_entropy=True)
+    # The entropy's sum is held against a rounded maximum k in powers of two: |k| < 16, so what k lost, off, is
+    # 2^-21 at most, and off - off, where both passed two roundings of 2^-24, is 4 * 2^-45 at most.
+    assert bool((H.abs() <= 2.0 ** -43).all())
+    assert bool((lp == 0).all()) and bool((ids == 0).all()) and bool((top == 0).all())
+    assert torch.equal(st[:, :1], z) and bool((st[:, 1] == 0).all())
+    g = m.mosaic_token_logprobs_grad(z, t, st, torch.ones(M, device=DEV))
+    # 1 - p, where p's two exponentials are off by 2^-23 and its quotient and product by 2^-24 each
+    assert bool((g.abs() <= 3 * 2.0 ** -23 + 2.0 ** -40).all())
+    two = torch.stack([z[:, 0], torch.full((M,), -float("inf"), device=DEV)], 1)
+    n = torch.tensor([M - 3], dtype=torch.int32, device=DEV)
+    lp = torch.full((M,), 5.0, device=DEV)
+    m.mosaic_token_logprobs(two, t, logprob=lp, count=n)
+    assert bool((lp[:M - 3] == 0).all()) and bool((lp[M - 3:] == 5).all())
