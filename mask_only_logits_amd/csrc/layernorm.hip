@@ -379,6 +379,7 @@ __global__ __launch_bounds__(NT) void layernorm_grad_kernel(const LayerNormGrad 
             load_row<BF16, CH, STEP, STREAM>(row_at<BF16>(a.dsum, row, a.lddsum), 0, t * N, a.d, x.ds);
     };
     const double over_d = 1.0 / a.d;
+    const bool ragged = a.d < LPR * CH * N;   // some threads have nothing in a place
     Loaded x, next;
     const int64_t first = (int64_t)blockIdx.x * RPB + row_group<LPR>(), step = (int64_t)gridDim.x * RPB;
     if (first < n)
@@ -410,6 +411,14 @@ __global__ __launch_bounds__(NT) void layernorm_grad_kernel(const LayerNormGrad 
         if (NEXT && row + step < n)
             fetch(row + step, next);
         const RowStats st(x.mean, x.rstd);
+        // Behind the row's end dy and s are 0.  Where mu rho passes fp32's range so would xh, and 0 times it
+        // is no number: there s takes mu, which is what such a row's elements are, all but equal in fp32.
+        // (Leaving the row's end out of the sums takes up to 36 registers.)
+        if (ragged && __builtin_expect(fabsf(st.xh(0.0f)) == __builtin_inff(), 0)) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                x.s[c].fill_from(a.d - c * STEP - t * N, (float)x.mean);
+        }
         float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -553,7 +562,7 @@ __global__ __launch_bounds__(1024) void layernorm_grad_long_kernel(const LayerNo
         const bool inside = src >= 0 && src < a.nsrc;
         const void *s = row_at<BF16>(a.S, inside ? src : 0, a.lds), *dy = row_at<BF16>(a.dY, row, a.lddy);
         const RowStats st(a.stats[2 * row], inside ? a.stats[2 * row + 1] : (double)__builtin_nanf(""));
-        // dy g (0 behind the row's end) and xh
+        // dy g and xh, both 0 behind the row's end
         auto terms = [&](int k, int cnt, float (&x)[N], float (&xh)[N]) __attribute__((always_inline)) {
             float g[N];
             load_some<BF16>(s, k, cnt, xh);
@@ -561,7 +570,7 @@ __global__ __launch_bounds__(1024) void layernorm_grad_long_kernel(const LayerNo
             load_weight_some(a.gain, a.gain_bf16, 1.0f, k, cnt, g);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                xh[i] = st.xh(xh[i]);
+                xh[i] = i < cnt ? st.xh(xh[i]) : 0.0f;
                 x[i] *= g[i];
             }
         };

@@ -125,6 +125,18 @@ struct Raw {
         const uint32_t b = __builtin_bit_cast(uint32_t, v), f = BF16 ? (b & 0xffff0000u) | (b >> 16) : b;
         w = u32x4_t{f, f, f, f};
     }
+    // v, rounded, in the place of the elements from the n-th on
+    __device__ __forceinline__ void fill_from(int n, float v)
+    {
+        const uint32_t e = BF16 ? pack_bf16(v, v) : __builtin_bit_cast(uint32_t, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16)
+                w[i] = 2 * i >= n ? e : 2 * i + 1 >= n ? (w[i] & 0xffffu) | (e & 0xffff0000u) : w[i];
+            else
+                w[i] = i >= n ? e : w[i];
+        }
+    }
     // Keeps the compiler from carrying the unpacked floats of an earlier use past this point:
     // rows held in registers are held as they are stored.
     __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
