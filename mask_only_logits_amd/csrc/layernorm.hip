@@ -62,23 +62,24 @@ __device__ __forceinline__ void moments(double s0, double sum, double sum2, int 
 }
 
 // A row's statistics for fp32 arithmetic: xh = (fma(s, h, -mu_hi) - mu_lo) * r.  Each of the two
-// differences rounds relative to itself, so a mean far from zero costs xh nothing.  h is 1, or 2^-66
-// for rows whose differences could pass fp32's range or whose rho lies below its normal numbers.
+// differences rounds relative to itself, so a mean far from zero costs xh nothing.  h is 1, or 2^-60
+// for rows whose differences could pass fp32's range or whose rho lies below its normal numbers: with
+// rho >= 2^-60 no element is further than 2^60 sqrt(d) from the mean, and no r passes 2^63.
 struct RowStats {
     float h, mu_hi, mu_lo, r;
 
     __device__ __forceinline__ RowStats(double mean, double rstd)
     {
-        const bool large = rstd < 0x1p-60 || fabs(mean) > 0x1p120;
-        h = large ? 0x1p-66f : 1.0f;
-        const double m = large ? mean * 0x1p-66 : mean;
+        const bool wide = rstd < 0x1p-60;
+        h = wide ? 0x1p-60f : 1.0f;
+        const double m = wide ? mean * 0x1p-60 : mean;
         mu_hi = (float)m;
         mu_lo = (float)(m - (double)mu_hi);
-        r = (float)(large ? rstd * 0x1p66 : rstd);
+        r = (float)(wide ? rstd * 0x1p60 : rstd);
     }
     __device__ __forceinline__ float xh(float s) const { return (__builtin_fmaf(s, h, -mu_hi) - mu_lo) * r; }
-    // rho t
-    __device__ __forceinline__ float times_rho(float t) const { return t * h * r; }
+    // rho t (r first: below 1 where h is not, so that neither product leaves fp32's range before the result does)
+    __device__ __forceinline__ float times_rho(float t) const { return t * r * h; }
 };
 
 // Gain (or bias) of a thread's CH chunks of N elements, chunk c from element c * STEP + t0 on;

@@ -58,3 +58,31 @@ def _check_constant_rows(m, d, dtype, eps):
 def test_constant_rows_far_from_zero(m, d, dtype):
     # mean times rho passes fp32's range
     _check_constant_rows(m, d, dtype, 1e-5)
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -126, 2.0 ** -124, 2.0 ** -100])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_constant_rows_with_the_smallest_eps(m, d, dtype, eps):
+    # rho is as large as it can be, 2^63, beside the largest means
+    _check_constant_rows(m, d, dtype, eps)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [100, 1021, 4096, 16501])
+def test_rows_of_any_deviation(m, d, dtype):
+    # either side of 2^60, where rows are scaled, up to the largest values and down to an eps that counts alone
+    g = torch.Generator(device=DEV).manual_seed(d)
+    scale = torch.tensor([2.0 ** e for e in (-70, -10, 50, 59, 60, 61, 70, 100, 120, 125, 126)], dtype=torch.float64,
+                         device=DEV)[:, None]
+    unit = 2 * torch.rand(len(scale), d, generator=g, device=DEV, dtype=torch.float64) - 1
+    for mean in (0.0, 1.0, -1.5):
+        x = ((unit + mean) * scale).to(dtype)
+        gain, bias = 1 + 0.2 * torch.randn(d, generator=g, device=DEV), torch.randn(d, generator=g, device=DEV)
+        _, y, st = m.mosaic_add_layernorm(x, gain, bias, with_stats=True)
+        head64.check_layernorm(x, None, gain, bias, 1e-5, None, None, y, st, f"{d} {mean}")
+        for size in (1.0, 2.0 ** 100):   # gradients of rho's size and far above
+            dy = (size * torch.randn(len(scale), d, generator=g, device=DEV)).to(dtype)
+            dx, _, _ = m.mosaic_layernorm_grad(dy, x, st, gain, with_gain=False, with_bias=False)
+            rows = st[:, 1] * size < 2.0 ** 120   # what fp32 holds
+            head64.check_layernorm_grad(dy[rows], x[rows], st[rows], gain, None, None, dx[rows], what=f"{d} {mean} {size}")
