@@ -69,12 +69,12 @@ struct Eight {
 };
 
 // 2^lpr threads (4 to 256) take a row, eight elements a thread and turn and four threads a block,
-// and a workgroup 256 >> lpr rows.
+// and a workgroup 256 >> lpr rows.  `values` may be X: each element is read and written by the same thread.
 template <bool BF16>
-__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const void *__restrict__ X, int64_t nsrc, int32_t d,
-                                                             int32_t blocks, int lpr, const int32_t *__restrict__ row_idx,
-                                                             int64_t rows, uint8_t *__restrict__ q,
-                                                             uint8_t *__restrict__ scale, void *values)
+__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const void *X, int64_t nsrc, int32_t d, int32_t blocks, int lpr,
+                                                             const int32_t *__restrict__ row_idx, int64_t rows,
+                                                             uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
+                                                             void *values)
 {
     constexpr int ES = BF16 ? 2 : 4, UN = 2;
     const int t = threadIdx.x & ((1 << lpr) - 1), each = 256 >> lpr, chunks = blocks * 4;

@@ -1,0 +1,46 @@
+"""What the compiler makes of the MXFP4 kernels: the device code is built to assembly and read."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from mask_only_logits_amd import build
+
+
+@pytest.fixture(scope="module")
+def assembly(tmp_path_factory):
+    try:
+        hipcc = build.hipcc()
+    except RuntimeError:
+        pytest.skip("hipcc not found")
+    out = str(tmp_path_factory.mktemp("code") / "gemm_mxfp4.s")
+    subprocess.run([hipcc, *build.HIPCC_FLAGS, "-I", str(build.ROOT / "include"), "-S", "--cuda-device-only",
+                    str(build.CSRC / "gemm_mxfp4.hip"), "-o", out], check=True, stderr=subprocess.DEVNULL)
+    with open(out) as f:
+        text = f.read()
+    os.remove(out)
+    return text
+
+
+def _arguments(text, kernel):
+    """For each instance of a kernel: its arguments, as {offset: description} of the code object's metadata."""
+    found = {}
+    for block in re.split(r"^  - ", text[text.index("amdhsa.kernels:"):], flags=re.M)[1:]:
+        name = re.search(r"\.symbol:\s+(\S+)\.kd", block)
+        if name and kernel in name.group(1):
+            args = re.split(r"^      - ", block[block.index(".args:"):], flags=re.M)[1:]
+            at = [(re.search(r"\.offset:\s+(\d+)", a), a) for a in args]
+            found[name.group(1)] = {int(o.group(1)): a for o, a in at if o}
+    return found
+
+
+def test_rows_may_be_quantized_in_place(assembly):
+    # X (the first argument) and values (the last before the launch's own) may be one array: the compiler must not
+    # take X for data that the kernel leaves alone, as it does of a pointer that nothing else may alias
+    kernels = _arguments(assembly, "quantize_mxfp4_kernel")
+    assert len(kernels) == 2
+    for name, args in kernels.items():
+        assert "global_buffer" in args[0] and "actual_access" not in args[0], name
+        pointers = [o for o in sorted(args) if "global_buffer" in args[o]]
+        assert len(pointers) == 5 and "actual_access" not in args[pointers[-1]], name
