@@ -878,11 +878,11 @@ gemm_mxfp4_kernel(const uint8_t *__restrict__ Hq, const uint8_t *__restrict__ hs
         main_loop(std::false_type{});
 }
 
-// The forms of the small kernel.
-template <int BM_, int BV_, int WGM_, int NSTAGE_, bool STREAM_>
+// The forms of the small kernel.  BYTES: taken only where the scale rows are no whole words.
+template <int BM_, int BV_, int WGM_, int NSTAGE_, bool STREAM_, bool BYTES_ = false>
 struct Small {
     static constexpr int BM = BM_, BV = BV_, WGM = WGM_, NSTAGE = NSTAGE_;
-    static constexpr bool STREAM = STREAM_;
+    static constexpr bool STREAM = STREAM_, BYTES = BYTES_;
     static constexpr int PER_CU = 163840 / (NSTAGE_ * (BM_ + BV_) * 128);   // workgroups that the LDS holds
 };
 
@@ -932,8 +932,10 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
             using F = decltype(form);
             const int64_t slots = std::max(8, cus / 8 * 8) * F::PER_CU;
             const int64_t grid = std::min(tiles(F::BM, F::BV), slots);
-            words ? go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, true, B>, grid, 256)
-                 : go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, false, B>, grid, 256);
+            if constexpr (!F::BYTES)
+                if (words)
+                    return go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, true, B>, grid, 256);
+            go(gemm_mxfp4_small_kernel<F::BM, F::BV, F::WGM, F::NSTAGE, F::STREAM, false, B>, grid, 256);
         };
         // Latency counts: eight stages, and a tile for each CU at most.
         if (tiles(32, 32) <= cus)
@@ -946,13 +948,13 @@ hipError_t launch_gemm_mxfp4(const uint8_t *Hq, const uint8_t *hs, const int32_t
         // for its longer requests (64 x 126464 x 4096: 58 us, tiles of 64 x 128 77; 48 x 65536 x 4096: 30 us,
         // 39; 33 x 152064 x 3584: 73 us, 70), if the scale rows are whole words.
         if (rows <= 64 && !words && tiles(64, 128) >= cus)
-            return small(Small<64, 128, 1, 3, true>{});
+            return small(Small<64, 128, 1, 3, true, true>{});
         if (rows <= 64 && (!words || tiles(64, 128) < cus))
             return small(Small<64, 64, 2, 4, true>{});
         if (tiles(128, 128) < cus)
             return small(Small<64, 64, 2, 4, false>{});
         if (!words)
-            return small(Small<128, 128, 2, 3, false>{});
+            return small(Small<128, 128, 2, 3, false, true>{});
         auto large = [&](auto bm_tag) {
             constexpr int BM = decltype(bm_tag)::value;
             const int64_t n = tiles(BM, 256);

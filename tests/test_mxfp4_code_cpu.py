@@ -44,3 +44,17 @@ def test_rows_may_be_quantized_in_place(assembly):
         assert "global_buffer" in args[0] and "actual_access" not in args[0], name
         pointers = [o for o in sorted(args) if "global_buffer" in args[o]]
         assert len(pointers) == 5 and "actual_access" not in args[pointers[-1]], name
+
+
+def _small_forms(text):
+    """Template arguments (BM, BV, WGM, NSTAGE, STREAM, WORDS, OUT_BF16) of the small product kernels, and their names."""
+    names = set(re.findall(r"^(_ZN\S*gemm_mxfp4_small_kernel\S*):", text, flags=re.M))
+    return {tuple(int(x) for x in re.findall(r"L[ib](\d+)E", n)): n for n in names}
+
+
+def test_no_form_is_built_that_no_call_takes(assembly):
+    # five forms with scales by words or by bytes, and two that only scale rows of no whole words take, for either type
+    forms = _small_forms(assembly)
+    assert len(forms) == 2 * (5 * 2 + 2)
+    for f in forms:
+        assert f[:2] not in ((64, 128), (128, 128)) or f[5] == 0, f
