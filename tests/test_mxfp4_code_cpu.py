@@ -58,3 +58,56 @@ def test_no_form_is_built_that_no_call_takes(assembly):
     assert len(forms) == 2 * (5 * 2 + 2)
     for f in forms:
         assert f[:2] not in ((64, 128), (128, 128)) or f[5] == 0, f
+
+
+def _requests(text, name):
+    """What a kernel asks of memory, in the assembly's order: s a load of scales to a register, L a request to LDS, W n a
+    wait for all but n of them, | a barrier, and a space where its blocks of instructions end."""
+    body = text[text.index(f"\n{name}:"):]
+    body = body[:body.index(".Lfunc_end")]
+    found = []
+    for line in body.splitlines():
+        line = line.strip()
+        wait = re.match(r"s_waitcnt\b.*vmcnt\((\d+)\)", line)
+        if wait:
+            found.append(f"W{wait.group(1)} ")
+        elif line.startswith("s_barrier"):
+            found.append("| ")
+        elif line.startswith("global_load_lds"):
+            found.append("L")
+        elif re.match(r"(global|flat|buffer|scratch)_load", line):
+            found.append("s")
+        elif re.match(r"s_c?branch|\.LBB", line):
+            found.append(" ")
+    return re.sub(r" +", " ", "".join(found))
+
+
+def test_counted_waits_of_the_small_tiles(assembly):
+    """A step waits until all but the requests of the K tiles behind its own have come.  That counts each K tile's loads
+    and requests, so the compiler must leave their number and order: NSTAGE - 1 K tiles before the first barrier, one
+    after each, and nothing else."""
+    forms = _small_forms(assembly)
+    assert forms
+    for (bm, bv, wgm, nstage, _, words, _), name in forms.items():
+        tile = "s" * ((bv // (4 // wgm) // 16 + bm // wgm // 16) * (1 if words else 2)) + "L" * (bv // 32 + bm // 32)
+        steps = _requests(assembly, name).split("|")
+        assert len(steps) == nstage + 1, name
+        first = [w for w in steps[0].split() if w != "W0"]
+        assert first == [tile] * (nstage - 1) + [f"W{(nstage - 2) * len(tile)}"], name
+        for k, step in enumerate(steps[1:]):
+            want = [tile, f"W{(nstage - 2) * len(tile)}" if k < nstage - 1 else "W0"]
+            assert step.split() == want, name
+
+
+def test_counted_waits_of_the_large_tiles(assembly):
+    """An output tile's first wait leaves its second K tile's codes under way: 12 requests (128 rows) or 16 a wave, which
+    have to be the last of the prologue, behind all others."""
+    names = sorted(set(re.findall(r"^(_ZN\S*gemm_mxfp4_kernel\S*):", assembly, flags=re.M)))
+    assert len(names) == 2 * 2 * 3
+    for name in names:
+        bm, _, _, grouped = (int(x) for x in re.findall(r"L[ib](\d+)E", name))
+        codes = 8 + bm // 32
+        scales = 6 if grouped else 3 * (2 + bm // 128)
+        seen = _requests(assembly, name)
+        assert f" {'L' * (scales + codes)} {'L' * codes} W0 W{codes} | " in seen, name
+        assert not re.search(rf"W{codes} (?!\|)", seen), name
