@@ -471,9 +471,9 @@ mosaic_status_t mosaic_distill_topk_grad(const void *logits, int64_t ldz, int64_
  *             stride ldsum; out is [rows, d] contiguous in in_dtype; stats is double[rows, 2].
  *             Without row_idx, sum may be X or R itself (same pointer and stride).  No other
  *             overlap of outputs with inputs or each other is allowed.
- * Rows >= n of every output are not written.  A row with a NaN or an infinity is NaN.  Any
- * d >= 1 and element-aligned pointers.  rows == 0: OK, nothing enqueued.  Errors as for
- * mosaic_add_rmsnorm. */
+ * Rows >= n of every output are not written.  A row whose s, in fp32, has a NaN or an infinity has
+ * NaN for out and rho.  Any d >= 1 and element-aligned pointers.  rows == 0: OK, nothing enqueued.
+ * Errors as for mosaic_add_rmsnorm. */
 mosaic_status_t mosaic_add_layernorm(const void *X, int64_t ldx, const void *R, int64_t ldr, int64_t nsrc, int64_t d,
                                      mosaic_dtype_t in_dtype, const void *gain, const void *bias,
                                      mosaic_dtype_t gain_dtype, float eps, const int32_t *row_idx,

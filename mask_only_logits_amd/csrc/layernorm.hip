@@ -334,7 +334,9 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(const LayerNorm a)
 }
 
 // Partial sums of the weight gradients: [parts][2][width], width = d rounded up to 64 (for
-// 16-byte accesses), in fp32 where a part has kRun rows at most, else in fp64.
+// 16-byte accesses).  Where a row group (the threads of a row) has kRun rows at most, its sums are
+// fp32, those of a workgroup's groups (32 at most) are joined in fp32, and a part is a workgroup; else
+// a part is a row group, in fp64, to which it adds its fp32 sums of every kRun rows.
 constexpr int kRun = 128;
 __host__ __device__ inline int64_t partial_width(int64_t d) { return (d + 63) / 64 * 64; }
 
